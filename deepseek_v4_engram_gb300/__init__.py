@@ -10,4 +10,6 @@ from .api import (DeviceLayerHash, DeviceTables, DeviceWeights, EngramError, Eng
                   engram_forward_workspace_size, engram_gate_and_add, engram_hash,
                   engram_hash_rows_layers, engram_wkv, engram_wkv_gate,
                   engram_wkv_gate_workspace_size, make_desc)
+from .attn import (engram_attn_paged, engram_attn_prompt, engram_attn_workspace_size,  # noqa: F401
+                   engram_kv_append, make_attn_desc)
 from .shard import embed_rows_sharded, exchange_rows, row_owner, table_shard_range  # noqa: F401

@@ -18,6 +18,10 @@ DEVERR_TOKEN_RANGE = 1
 DEVERR_CACHE_FULL = 2
 DEVERR_ID_RANGE = 4
 DEVERR_WAIT_TIMEOUT = 8
+DEVERR_PAGE_RANGE = 16
+
+BF16 = 0
+F16 = 1
 
 
 class EngramDesc(ctypes.Structure):
@@ -46,6 +50,26 @@ class EngramLayerHash(ctypes.Structure):
                 ("rows", ctypes.c_void_p), ("hash_ids", ctypes.c_void_p)]
 
 
+class EngramAttnDesc(ctypes.Structure):
+    _fields_ = [("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class EngramAttnView(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class EngramKvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_page_stride", ctypes.c_int64), ("k_slot_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("v_slot_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("table_width", ctypes.c_int32)]
+
+
 MAX_HASH_LAYERS = 16
 
 _P = ctypes.c_void_p
@@ -55,6 +79,9 @@ _SZ = ctypes.c_size_t
 _DESC = ctypes.POINTER(EngramDesc)
 _TAB = ctypes.POINTER(EngramTables)
 _WTS = ctypes.POINTER(EngramWeights)
+_ADESC = ctypes.POINTER(EngramAttnDesc)
+_VIEW = ctypes.POINTER(EngramAttnView)
+_CACHE = ctypes.POINTER(EngramKvCache)
 
 # name -> (restype, argtypes); the same names as include/engram.h
 SIGNATURES = {
@@ -84,6 +111,12 @@ SIGNATURES = {
                                           _P]),
     "engram_forward_noalloc": (ctypes.c_int, [_DESC, _TAB, _WTS, _P, _P, _I32, _I32, _P, _P,
                                               _I32, _P, _P, _P, _P, _P, _P]),
+    "engram_attn_workspace_size": (_SZ, [_ADESC]),
+    "engram_attn_prompt": (ctypes.c_int, [_ADESC, _VIEW, _VIEW, _VIEW, _P, _I32, _I32, _VIEW, _P,
+                                          _P, _SZ, _P]),
+    "engram_attn_paged": (ctypes.c_int, [_ADESC, _VIEW, _P, _I32, _I32, _I32, _P, _CACHE, _VIEW,
+                                         _P, _P, _SZ, _P]),
+    "engram_kv_append": (ctypes.c_int, [_ADESC, _VIEW, _VIEW, _P, _I32, _I32, _P, _CACHE, _P]),
 }
 
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024

@@ -1,0 +1,98 @@
+// Attention over packed prompts and over a paged cache: what the C ABI (attn_capi.cu) hands to the
+// kernels. Host-only launch declarations; pointers are device pointers already validated.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "attn_plan.cuh"
+
+namespace engram {
+
+struct AttnArgs {
+  AttnPlan plan;             // tokens, workers, min_units and whole are the launcher's
+  bool bf16;                 // else f16
+  int32_t heads;             // query heads
+  int32_t group;             // query heads per key-value head
+  int32_t head_dim;
+  float scale_log2;          // softmax scale * log2(e): scores go straight to exp2
+  const uint16_t* q;         // element strides of a token and of a head follow each pointer
+  int64_t q_token, q_head;
+  uint16_t* out;
+  int64_t o_token, o_head;
+  float* lse;                // [total, heads] or null
+  const uint16_t* k;         // packed: [total, kv_heads, D]; paged: [pages, page_size, kv_heads, D]
+  const uint16_t* v;
+  int64_t k_token, k_head, v_token, v_head;
+  int64_t k_page, v_page;    // paged only
+  const int32_t* table;      // [n_seqs, table_width], null: packed
+  int32_t table_width, page_size, n_pages;
+  int32_t granule;           // keys per copy: a power of two that divides page_size; 128 if packed
+  void* workspace;
+  uint32_t* err;
+};
+
+// The pieces of cut items: per worker one AttnMeta (the item that it begins and does not end) and
+// two slots of `rows` rows: slot 0 for the item that it continues, slot 1 for the one it begins.
+struct AttnMeta {
+  int32_t b, h, rt, pieces;  // pieces = 0: nothing to join
+};
+struct AttnPieces {
+  AttnMeta* meta;            // [workers]
+  float* ml;                 // [workers * 2, rows, 2]: running maximum (of log2 scores) and sum
+  float* o;                  // [workers * 2, rows, width]: sum of 2^(x - max) v
+};
+
+constexpr size_t attn_round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+inline size_t attn_pieces_bytes(int32_t workers, int32_t rows, int32_t width) {
+  return attn_round256(size_t(workers) * sizeof(AttnMeta)) +
+         attn_round256(size_t(workers) * 2 * rows * 2 * 4) + size_t(workers) * 2 * rows * width * 4;
+}
+
+inline AttnPieces attn_pieces_at(void* workspace, int32_t workers, int32_t rows) {
+  uint8_t* p = static_cast<uint8_t*>(workspace);
+  AttnPieces r;
+  r.meta = reinterpret_cast<AttnMeta*>(p);
+  p += attn_round256(size_t(workers) * sizeof(AttnMeta));
+  r.ml = reinterpret_cast<float*>(p);
+  p += attn_round256(size_t(workers) * 2 * rows * 2 * 4);
+  r.o = reinterpret_cast<float*>(p);
+  return r;
+}
+
+// Width of a row in the kernels: 64 or 128 columns, those past head_dim zero.
+constexpr int32_t attn_width(int32_t head_dim) { return head_dim <= 64 ? 64 : 128; }
+
+// Items of up to 16 rows (attn_rows_sm103.cu): decoding.
+constexpr int32_t kAttnRows = 16;
+cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t st);
+
+// Joins the pieces of items of `rows` rows.
+cudaError_t launch_attn_combine(const AttnArgs& a, int32_t rows, cudaStream_t st);
+
+struct KvAppendArgs {
+  const int32_t* cu;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int32_t n_seqs, total, table_width, page_size, n_pages, kv_heads, head_dim;
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t k_token, k_head, v_token, v_head;
+  uint16_t* k_cache;
+  uint16_t* v_cache;
+  int64_t k_page, k_slot, k_chead, v_page, v_slot, v_chead;
+  uint32_t* err;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t st);
+
+// Tensor map of the keys or values (capi.cu): element (d, head, token, page) of a 16-bit tensor
+// with the given strides in elements, boxes of 64 columns of one head by `granule` tokens, with
+// the 128-byte swizzle; columns past `dim` read as zero.
+bool tensor_map_kv(void* map_out, const void* base, bool bf16, uint64_t dim, uint64_t heads,
+                   uint64_t tokens, uint64_t pages, int64_t head_stride, int64_t token_stride,
+                   int64_t page_stride, uint32_t granule);
+
+}  // namespace engram

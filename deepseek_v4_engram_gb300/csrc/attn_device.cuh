@@ -1,0 +1,128 @@
+// What the attention kernels share on the device.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "attn.h"
+#include "device.cuh"
+
+namespace engram {
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two f32 -> packed pair of the 16-bit type (lo in the low half), round to nearest even.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
+  if constexpr (kBf16) return pack_bf16x2(lo, hi);
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Whether one of the two 16-bit values in `w` is an infinity or NaN.
+template <bool kBf16>
+__device__ __forceinline__ bool any_nonfinite(uint32_t w) {
+  constexpr uint32_t e = kBf16 ? 0x7F80u : 0x7C00u;
+  return (w & e) == e || (w & (e << 16)) == (e << 16);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float to_f32(uint16_t bits) {
+  if constexpr (kBf16) return bf16_bits_to_f32(bits);
+  return __half2float(__ushort_as_half(bits));
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// Where the keys of the granule that starts at position `pos` of sequence b lie: z and w
+// coordinates of the tensor maps. A page number that the cache does not have is reported and
+// addressed past the end, where a copy reads zeros.
+struct KvPlace {
+  int32_t z, w;
+};
+__device__ __forceinline__ KvPlace kv_place(const AttnArgs& a, const AttnSeq& s, int32_t b,
+                                            int32_t pos) {
+  if (a.table == nullptr) return {s.q0 + pos, 0};
+  const int32_t col = pos / a.page_size;
+  int32_t page = a.table[static_cast<int64_t>(b) * a.table_width + col];
+  if (page < 0 || page >= a.n_pages) {
+    set_error(a.err, kErrPageRange);
+    page = a.n_pages;
+  }
+  return {pos - col * a.page_size, page};
+}
+
+// A wait that never blocks twice: once a role has given up, every later wait returns at once and
+// the roles run to their end without touching memory that was never filled in earnest.
+__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          uint32_t* err) {
+  if (*abort) return false;
+  return mbar_wait(bar, parity, abort, err);
+}
+
+// Finds the calling CTA's range: every thread sums a run of sequences, a scan over the CTA finds
+// the run that holds the range's first unit, and that run's thread walks it and places the
+// cursor. One pass over the lengths; all kThreads threads call it. A worker without work gets a
+// cursor that has nothing left. Worker 0 reports lengths beyond the page table.
+struct AttnStart {
+  int64_t sums[33];
+  int64_t per;
+  AttnCursor cursor;
+};
+
+template <int kThreads>
+__device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worker,
+                                                AttnStart* sh, uint32_t* err) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int32_t run = (p.n_seqs + kThreads - 1) / kThreads;
+  const int32_t b0 = tid * run;
+  const int32_t b1 = b0 + run < p.n_seqs ? b0 + run : p.n_seqs;
+  int64_t mine = 0;
+  for (int32_t b = b0; b < b1; ++b) {
+    mine += attn_seq_units(p, attn_seq(p, b));
+    if (worker == 0 && p.kv_len && p.kv_len[b] > p.kv_cap) set_error(err, kErrCacheCapacity);
+  }
+  int64_t scan = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+    if (lane >= o) scan += v;
+  }
+  if (lane == 31) sh->sums[warp] = scan;
+  if (tid == 0) {
+    sh->cursor.left = 0;
+    sh->cursor.b = p.n_seqs;
+  }
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sh->sums[w];
+    total += sh->sums[w];
+  }
+  const int64_t per = attn_share(p, total);
+  const int64_t u0 = per * worker;
+  int64_t at = before + scan - mine;
+  if (tid == 0) sh->per = per;
+  if (u0 < total && at <= u0 && u0 < at + mine) {
+    int32_t b = b0;
+    for (;; ++b) {
+      const int64_t u = attn_seq_units(p, attn_seq(p, b));
+      if (u0 < at + u) break;
+      at += u;
+    }
+    sh->cursor.start(p, b, u0 - at, total - u0 < per ? total - u0 : per);
+  }
+  __syncthreads();
+}
+
+}  // namespace engram

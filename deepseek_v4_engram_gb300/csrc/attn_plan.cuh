@@ -1,0 +1,203 @@
+// How the attention kernels share out their work.
+//
+// An item is `tokens` consecutive query tokens of one sequence with all the query heads of one
+// key-value head: rows token * G + g, so a key tile that is loaded once serves every head that
+// shares it. Its cost is the number of kTileKeys-key tiles that its last token sees, at least 1
+// (an item that sees nothing still has to write zeros). Within a sequence, items go key-value
+// head by key-value head and then by token tile, so that workers that run side by side read the
+// same keys.
+//
+// All the items' tiles laid end to end are units 0 .. W-1, and worker w (a CTA) takes the units
+// [w * per, (w + 1) * per) with per = ceil(W / workers), at least `min_units`. Prompts of any
+// lengths, causal triangles and long caches with few rows are so balanced by one rule that needs
+// no lengths on the host: every worker evaluates it for itself from the lengths in device memory.
+// An item that a boundary cuts is computed in pieces, each with its own running maximum and sum;
+// the pieces are joined afterwards (attn_combine.cu), always in the same order.
+//
+// With `whole`, an item is not cut: it belongs to the worker whose range holds its first unit.
+//
+// A worker holds at most two pieces: one of an item that an earlier worker began (its first
+// segment), and one of an item that it begins and a later worker finishes (its last segment).
+#pragma once
+
+#include <cstdint>
+
+namespace engram {
+
+constexpr int32_t kTileKeys = 128;   // keys per unit
+
+struct AttnPlan {
+  const int32_t* cu;       // [n_seqs + 1] first token of each sequence, and the end
+  const int32_t* kv_len;   // [n_seqs] positions in the cache; null: keys are the tokens themselves
+  int32_t n_seqs;
+  int32_t total;           // tokens in q
+  int32_t kv_cap;          // positions that a sequence's page table can hold
+  int32_t kv_heads;
+  int32_t tokens;          // query tokens per item
+  int32_t workers;
+  int32_t min_units;       // smallest share of a worker
+  int32_t whole;           // items are not cut
+};
+
+// One sequence: tokens [q0, q0 + n), of which token t sees the keys [0, max(0, m - n + t + 1)).
+struct AttnSeq {
+  int32_t q0, n, m;
+};
+
+__host__ __device__ inline int32_t attn_clamp(int32_t v, int32_t lo, int32_t hi) {
+  return v < lo ? lo : v > hi ? hi : v;
+}
+
+// Lengths come from device memory and are clamped to what the tensors hold.
+__host__ __device__ inline AttnSeq attn_seq(const AttnPlan& p, int32_t b) {
+  AttnSeq s;
+  s.q0 = attn_clamp(p.cu[b], 0, p.total);
+  s.n = attn_clamp(p.cu[b + 1], s.q0, p.total) - s.q0;
+  s.m = p.kv_len ? attn_clamp(p.kv_len[b], 0, p.kv_cap) : s.n;
+  return s;
+}
+
+__host__ __device__ inline int32_t attn_items(const AttnPlan& p, const AttnSeq& s) {
+  return (s.n + p.tokens - 1) / p.tokens;
+}
+
+// Keys that the last token of token tile rt sees, and the tiles they fill (at least one).
+__host__ __device__ inline int32_t attn_keys(const AttnPlan& p, const AttnSeq& s, int32_t rt) {
+  const int64_t last = int64_t(rt + 1) * p.tokens;
+  const int32_t x = s.m - s.n + (last < s.n ? static_cast<int32_t>(last) : s.n);
+  return x > 0 ? x : 0;
+}
+__host__ __device__ inline int32_t attn_cost(const AttnPlan& p, const AttnSeq& s, int32_t rt) {
+  const int32_t t = (attn_keys(p, s, rt) + kTileKeys - 1) / kTileKeys;
+  return t > 0 ? t : 1;
+}
+
+// sum_{i < n} floor((a i + b) / m), by the Euclidean reduction of the lattice-point count:
+// exchange the roles of a and m once both a and b are below m. a n + b stays below 2^32 here
+// (a < 2^8 after the first step, n < 2^24).
+__host__ __device__ inline uint64_t attn_floor_sum(uint32_t n, uint32_t m, uint32_t a,
+                                                   uint32_t b) {
+  uint64_t sum = 0;
+  while (n > 0) {
+    sum += (static_cast<uint64_t>(n) * (n - 1) / 2) * (a / m) + static_cast<uint64_t>(n) * (b / m);
+    a %= m;
+    b %= m;
+    const uint32_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const uint32_t t = m;
+    m = a;
+    a = t;
+  }
+  return sum;
+}
+
+// Units of the token tiles 0 .. k-1 of one key-value head (k <= attn_items).
+__host__ __device__ inline int64_t attn_units_before(const AttnPlan& p, const AttnSeq& s,
+                                                     int32_t k) {
+  if (k <= 0) return 0;
+  int64_t u = 0;
+  if (k == attn_items(p, s)) u += attn_cost(p, s, --k);   // the last one may hold fewer tokens
+  const int32_t a = s.m - s.n;
+  int32_t z = a < 0 ? -a / p.tokens : 0;   // tiles that see nothing: one unit each
+  if (z > k) z = k;
+  u += z;
+  return u + static_cast<int64_t>(attn_floor_sum(
+                 static_cast<uint32_t>(k - z), kTileKeys, p.tokens,
+                 static_cast<uint32_t>(a + (z + 1) * p.tokens + kTileKeys - 1)));
+}
+
+__host__ __device__ inline int64_t attn_seq_units(const AttnPlan& p, const AttnSeq& s) {
+  return s.n == 0 ? 0 : attn_units_before(p, s, attn_items(p, s)) * p.kv_heads;
+}
+
+__host__ __device__ inline int64_t attn_share(const AttnPlan& p, int64_t units) {
+  const int64_t per = (units + p.workers - 1) / p.workers;
+  return per > p.min_units ? per : p.min_units;
+}
+
+// A stretch of one item's key tiles, [tile0, tile1) of `cost`.
+struct AttnSegment {
+  AttnSeq seq;
+  int32_t b, h, rt;
+  int32_t tile0, tile1, cost;
+  int32_t keys;        // that the item's last token sees
+  int32_t token0;      // first token of the item in q
+  int32_t ntok;        // its tokens
+  int32_t first_keys;  // keys that its first token sees (at least 0)
+  __host__ __device__ bool begins() const { return tile0 == 0; }
+  __host__ __device__ bool ends() const { return tile1 == cost; }
+};
+
+// Walks a worker's segments in order. (b, h, rt, tile) is where its range begins and `left` the
+// units in it.
+struct AttnCursor {
+  AttnSeq seq;
+  int32_t b, h, rt, tile;
+  int64_t left;
+
+  __host__ __device__ bool next(const AttnPlan& p, AttnSegment& out) {
+    if (left <= 0 || b >= p.n_seqs) return false;
+    out.seq = seq;
+    out.b = b;
+    out.h = h;
+    out.rt = rt;
+    out.cost = attn_cost(p, seq, rt);
+    out.tile0 = tile;
+    out.tile1 = p.whole || left >= out.cost - tile ? out.cost
+                                                   : tile + static_cast<int32_t>(left);
+    out.keys = attn_keys(p, seq, rt);
+    const int32_t t0 = rt * p.tokens;
+    out.token0 = seq.q0 + t0;
+    out.ntok = seq.n - t0 < p.tokens ? seq.n - t0 : p.tokens;
+    const int32_t f = seq.m - seq.n + t0 + 1;
+    out.first_keys = f > 0 ? f : 0;
+    left -= out.tile1 - tile;
+    if (out.tile1 == out.cost) step(p);
+    return true;
+  }
+
+  // To the next item.
+  __host__ __device__ void step(const AttnPlan& p) {
+    tile = 0;
+    if (++rt < attn_items(p, seq)) return;
+    rt = 0;
+    if (++h < p.kv_heads) return;
+    h = 0;
+    do {
+      if (++b >= p.n_seqs) return;
+      seq = attn_seq(p, b);
+    } while (seq.n == 0);
+  }
+
+  // The worker's range begins inside sequence b, `pos` units into it, and holds `units`.
+  __host__ __device__ void start(const AttnPlan& p, int32_t b_, int64_t pos, int64_t units) {
+    b = b_;
+    seq = attn_seq(p, b);
+    left = units;
+    const int64_t head = attn_units_before(p, seq, attn_items(p, seq));
+    h = static_cast<int32_t>(pos / head);
+    const int64_t in = pos - h * head;
+    int32_t lo = 0, hi = attn_items(p, seq);   // units_before(lo) <= in < units_before(hi)
+    while (hi - lo > 1) {
+      const int32_t mid = lo + (hi - lo) / 2;
+      if (attn_units_before(p, seq, mid) <= in) lo = mid;
+      else hi = mid;
+    }
+    rt = lo;
+    tile = static_cast<int32_t>(in - attn_units_before(p, seq, lo));
+    if (p.whole && tile > 0) {   // the item belongs to the worker before
+      left -= attn_cost(p, seq, rt) - tile;
+      step(p);
+    }
+  }
+};
+
+// Workers that hold a piece of the item that `s`, a worker's last segment, begins but does not
+// end: this one and the ones that follow.
+__host__ __device__ inline int32_t attn_pieces(const AttnSegment& s, int64_t per) {
+  return 1 + static_cast<int32_t>((s.cost - s.tile1 + per - 1) / per);
+}
+
+}  // namespace engram

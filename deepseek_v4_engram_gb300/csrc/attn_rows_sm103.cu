@@ -1,0 +1,430 @@
+// Attention for items of at most 16 query rows: decoding, a few drafted tokens, any chunk of a
+// sequence whose rows (tokens x heads that share a key-value head) are few.
+//
+//   o_r = sum_j 2^(x_rj - M_r) v_j / sum_j 2^(x_rj - M_r),   x_rj = scale log2(e) q_r . k_j
+//
+// in one pass over the keys with a running maximum M and sum. What bounds it is the cache's bytes:
+// 16 rows make 16 multiply-adds of each key or value element, far below what the tensor cores do in
+// the time that the element takes to arrive. So the work is shared out by key tiles alone
+// (attn_plan.cuh), one CTA per SM streams its tiles through a ring of three 64 KB stages (six of
+// 32 KB where heads have up to 64 columns), which keeps more bytes in flight per SM than the memory's
+// latency needs, and the ring runs on across the ends of items.
+//
+// Roles (288 threads): warp 8 requests the tiles by TMA, one page granule per lane; warps 0-7 take
+// 16 of a tile's 128 keys each, so every warp has its own maximum, sum and output and no step of
+// the loop waits for another warp. The products run on mma.sync m16n8k16: its 16 rows are the whole
+// item, its fragments stay in registers (scores come out in the layout in which they go back in as
+// probabilities), and a tcgen05 tile would be seven eighths padding.
+#include "attn_device.cuh"
+#include "kernels.h"
+#include "wkv_tiles.cuh"
+
+namespace engram {
+
+namespace {
+
+constexpr int kConsumers = 8;
+constexpr int kThreads = (kConsumers + 1) * 32;
+
+template <int DH>
+struct Geo {
+  static constexpr int kHalves = DH / 64;                          // 64-column boxes per row
+  static constexpr int kTensorBytes = kTileKeys * DH * 2;          // K or V of a stage
+  static constexpr int kStages = DH == 128 ? 3 : 6;
+  static constexpr int kJoinBytes = 4 * 16 * DH * 4;               // four warps' outputs
+};
+
+template <int DH>
+struct Shared {
+  uint64_t full[Geo<DH>::kStages];
+  uint64_t empty[Geo<DH>::kStages];
+  AttnStart start;
+  float ml[kConsumers][kAttnRows][2];
+  int abort;
+};
+
+template <int DH>
+constexpr size_t smem_bytes() {
+  return 1024 + size_t(Geo<DH>::kStages) * 2 * Geo<DH>::kTensorBytes + Geo<DH>::kJoinBytes +
+         sizeof(Shared<DH>);
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  if constexpr (kBf16) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+
+// Byte offset of 16-byte chunk `c` (8 columns) of key `row` in a K or V tile: 64-column boxes of
+// 128 rows of 128 bytes, 128-byte swizzle.
+__device__ __forceinline__ uint32_t tile_offset(int row, int c) {
+  return static_cast<uint32_t>((c >> 3) * (kTileKeys * 128) + row * 128 +
+                               (((c & 7) ^ (row & 7)) << 4));
+}
+
+template <int DH, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_rows_kernel(const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const AttnArgs a,
+                     const AttnPieces pieces) {
+  using G = Geo<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_1024(smem_raw);
+  float* join = reinterpret_cast<float*>(smem + G::kStages * 2 * G::kTensorBytes);
+  Shared<DH>* sh = reinterpret_cast<Shared<DH>*>(reinterpret_cast<uint8_t*>(join) + G::kJoinBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < G::kStages; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], kConsumers);
+    }
+    sh->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  pdl_wait();   // queries, lengths and the cache may come from the previous kernel
+  pdl_launch_dependents();
+  attn_find_start<kThreads>(a.plan, blockIdx.x, &sh->start, a.err);
+  volatile int* abort = &sh->abort;
+  AttnCursor cur = sh->start.cursor;
+  AttnSegment seg;
+
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------- TMA producer
+    TmaRingT<G::kStages> ring;
+    const int gran = lane & 15;                     // lanes 0-15 the keys' granules, 16-31 the values'
+    const CUtensorMap* map = lane < 16 ? &tmK : &tmV;
+    bool stop = false;
+    while (!stop && cur.next(a.plan, seg)) {
+      for (int32_t t = seg.tile0; t < seg.tile1 && t * kTileKeys < seg.keys; ++t) {
+        const int32_t k0 = t * kTileKeys;
+        const int32_t n = seg.keys - k0 < kTileKeys ? seg.keys - k0 : kTileKeys;
+        const int32_t grans = (n + a.granule - 1) / a.granule;
+        KvPlace at{0, 0};
+        if (gran < grans) at = kv_place(a, seg.seq, seg.b, k0 + gran * a.granule);
+        stop = __any_sync(0xFFFFFFFFu, !ring.acquire(sh->empty, abort, a.err));
+        if (stop) break;
+        uint8_t* dst = smem + (ring.stage * 2 + (lane < 16 ? 0 : 1)) * G::kTensorBytes;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&sh->full[ring.stage],
+                                static_cast<uint32_t>(grans * a.granule) * 128 * G::kHalves * 2);
+        __syncwarp();
+        if (gran < grans) {
+#pragma unroll
+          for (int hf = 0; hf < G::kHalves; ++hf)
+            tma_load_4d(dst + hf * (kTileKeys * 128) + gran * a.granule * 128, map,
+                        &sh->full[ring.stage], hf * 64, seg.h, at.z, at.w);
+        }
+        ring.issued();
+      }
+    }
+    __syncwarp();
+    ring.drain(sh->full);
+  } else {
+    // ------------------------------------------------------------- consumers
+    const int gid = lane >> 2, tid = lane & 3;
+    uint32_t stage = 0, phase = 0;
+    AttnMeta meta{0, 0, 0, 0};
+    while (cur.next(a.plan, seg)) {
+      // Rows gid and gid + 8: token row / G of the item, head h * G + row % G.
+      int32_t limit[2];
+      uint32_t qf[DH / 16][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int32_t r = gid + 8 * i, tok = r / a.group;
+        const bool valid = tok < seg.ntok;
+        const int32_t lim = seg.seq.m - seg.seq.n + (seg.token0 - seg.seq.q0) + tok + 1;
+        limit[i] = valid && lim > 0 ? lim : 0;
+        const uint16_t* qp = a.q + static_cast<int64_t>(seg.token0 + tok) * a.q_token +
+                             static_cast<int64_t>(seg.h * a.group + (r - tok * a.group)) * a.q_head;
+#pragma unroll
+        for (int c = 0; c < DH / 8; ++c) {   // 8-column chunk c: columns 8 c + 2 tid, + 1
+          uint32_t w = 0;
+          if (valid && c * 8 < a.head_dim)
+            w = *reinterpret_cast<const uint32_t*>(qp + c * 8 + tid * 2);
+          qf[c / 2][(c & 1) * 2 + i] = w;
+        }
+      }
+      float mx[2] = {-INFINITY, -INFINITY}, sum[2] = {0.f, 0.f};
+      float o[DH / 8][4];
+#pragma unroll
+      for (int n = 0; n < DH / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+
+      for (int32_t t = seg.tile0; t < seg.tile1 && t * kTileKeys < seg.keys; ++t) {
+        const bool here = !__any_sync(
+            0xFFFFFFFFu, !attn_wait(&sh->full[stage], phase, abort, a.err));
+        const uint32_t sk = smem_u32(smem + stage * 2 * G::kTensorBytes);
+        const uint32_t sv = sk + G::kTensorBytes;
+        const int32_t key0 = t * kTileKeys + warp * 16;   // this warp's keys
+        if (here && key0 < seg.keys) {
+          // scores of 16 rows by 16 keys
+          float s[2][4] = {};
+          {
+            const int row = warp * 16 + ((lane >> 4) << 3) + (lane & 7);
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk) {
+              uint32_t b[4];
+              ldmatrix_x4(b, sk + tile_offset(row, kk * 2 + ((lane >> 3) & 1)));
+              mma_16816<kBf16>(s[0], qf[kk], b[0], b[1]);
+              mma_16816<kBf16>(s[1], qf[kk], b[2], b[3]);
+            }
+          }
+          const bool edge = key0 + 16 > seg.first_keys;   // some row does not see all of them
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = s[n][e] * a.scale_log2;
+              s[n][e] = edge && key0 + n * 8 + tid * 2 + (e & 1) >= limit[e >> 1] ? -INFINITY : x;
+            }
+          uint32_t p[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float m = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+            m = fmaxf(m, mx[i]);
+            const float base = m == -INFINITY ? 0.f : m;   // nothing seen yet: every term is 0
+            const float f = exp2_fast(mx[i] - base);
+            mx[i] = m;
+            float e[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              e[2 * n] = exp2_fast(s[n][2 * i] - base);
+              e[2 * n + 1] = exp2_fast(s[n][2 * i + 1] - base);
+              p[2 * n + i] = pack16x2<kBf16>(e[2 * n], e[2 * n + 1]);
+            }
+            sum[i] = sum[i] * f + ((e[0] + e[1]) + (e[2] + e[3]));
+#pragma unroll
+            for (int n = 0; n < DH / 8; ++n) {
+              o[n][2 * i] *= f;
+              o[n][2 * i + 1] *= f;
+            }
+          }
+          const int row = warp * 16 + (lane & 15);
+          const int32_t seen = seg.keys - key0;   // keys past it hold whatever the memory held
+          if (!edge) {
+#pragma unroll
+            for (int n = 0; n < DH / 16; ++n) {
+              uint32_t b[4];
+              ldmatrix_x4_trans(b, sv + tile_offset(row, n * 2 + (lane >> 4)));
+              mma_16816<kBf16>(o[2 * n], p, b[0], b[1]);
+              mma_16816<kBf16>(o[2 * n + 1], p, b[2], b[3]);
+            }
+          } else {
+            // A probability of 0 does not undo an infinity or NaN that it multiplies: values past
+            // the last key are cleared, and if one that only some rows see is not finite, the
+            // products of these 16 keys are formed one by one for the rows that see them.
+            uint32_t keep[2];   // this lane's key pairs 2 tid, + 1 and 2 tid + 8, + 9
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              keep[i] = (tid * 2 + 8 * i < seen ? 0x0000FFFFu : 0u) |
+                        (tid * 2 + 8 * i + 1 < seen ? 0xFFFF0000u : 0u);
+            bool bad = false;
+#pragma unroll
+            for (int n = 0; n < DH / 16; ++n) {
+              uint32_t b[4];
+              ldmatrix_x4_trans(b, sv + tile_offset(row, n * 2 + (lane >> 4)));
+#pragma unroll
+              for (int e = 0; e < 4; ++e) bad |= any_nonfinite<kBf16>(b[e] & keep[e & 1]);
+            }
+            if (!__any_sync(0xFFFFFFFFu, bad)) {
+#pragma unroll
+              for (int n = 0; n < DH / 16; ++n) {
+                uint32_t b[4];
+                ldmatrix_x4_trans(b, sv + tile_offset(row, n * 2 + (lane >> 4)));
+                mma_16816<kBf16>(o[2 * n], p, b[0] & keep[0], b[1] & keep[1]);
+                mma_16816<kBf16>(o[2 * n + 1], p, b[2] & keep[0], b[3] & keep[1]);
+              }
+            } else {
+              for (int j = 0; j < 16; ++j) {
+                // row i's probability of key j sits in lane (row, (j % 8) / 2)
+                const int src = gid * 4 + ((j & 7) >> 1);
+                float pj[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t lo = __shfl_sync(0xFFFFFFFFu, p[i], src);
+                  const uint32_t hi = __shfl_sync(0xFFFFFFFFu, p[2 + i], src);
+                  const uint32_t w = j < 8 ? lo : hi;
+                  pj[i] = to_f32<kBf16>(static_cast<uint16_t>(j & 1 ? w >> 16 : w));
+                }
+#pragma unroll
+                for (int n = 0; n < DH / 8; ++n) {
+                  uint32_t w;
+                  asm volatile("ld.shared.u32 %0, [%1];"
+                               : "=r"(w)
+                               : "r"(sv + tile_offset(warp * 16 + j, n) + tid * 4)
+                               : "memory");
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    if (key0 + j < limit[i]) {
+                      o[n][2 * i] += pj[i] * to_f32<kBf16>(static_cast<uint16_t>(w));
+                      o[n][2 * i + 1] += pj[i] * to_f32<kBf16>(static_cast<uint16_t>(w >> 16));
+                    }
+                }
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->empty[stage]);
+        if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+      }
+
+      // ---- the eight warps' maxima, sums and outputs become one
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
+        sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
+        if (tid == 0) {
+          sh->ml[warp][gid + 8 * i][0] = mx[i];
+          sh->ml[warp][gid + 8 * i][1] = sum[i];
+        }
+      }
+      named_bar_sync(1, kConsumers * 32);
+      float m_all[2], l_all[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float m = -INFINITY;
+        for (int w = 0; w < kConsumers; ++w) m = fmaxf(m, sh->ml[w][gid + 8 * i][0]);
+        const float base = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+        for (int w = 0; w < kConsumers; ++w)
+          l += sh->ml[w][gid + 8 * i][1] * exp2_fast(sh->ml[w][gid + 8 * i][0] - base);
+        m_all[i] = m;
+        l_all[i] = l;
+        const float f = exp2_fast(mx[i] - base);
+#pragma unroll
+        for (int n = 0; n < DH / 8; ++n) {
+          o[n][2 * i] *= f;
+          o[n][2 * i + 1] *= f;
+        }
+      }
+      // warps 4-7 hand theirs to 0-3, then 2-3 to 0-1, then 1 to 0: each lane to the same lane
+      for (int give = 4; give >= 1; give >>= 1) {
+        if (warp >= give && warp < 2 * give) {
+#pragma unroll
+          for (int n = 0; n < DH / 8; ++n)
+            *reinterpret_cast<float4*>(join + (((warp - give) * (DH / 8) + n) * 32 + lane) * 4) =
+                make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
+        }
+        named_bar_sync(1, kConsumers * 32);
+        if (warp < give) {
+#pragma unroll
+          for (int n = 0; n < DH / 8; ++n) {
+            const float4 v =
+                *reinterpret_cast<const float4*>(join + ((warp * (DH / 8) + n) * 32 + lane) * 4);
+            o[n][0] += v.x;
+            o[n][1] += v.y;
+            o[n][2] += v.z;
+            o[n][3] += v.w;
+          }
+        }
+        if (give > 1) named_bar_sync(1, kConsumers * 32);
+      }
+      if (warp == 0) {
+        const bool whole = seg.begins() && seg.ends();
+        const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg.begins() ? 1 : 0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int32_t r = gid + 8 * i, tok = r / a.group;
+          if (tok >= seg.ntok) continue;
+          const int32_t head = seg.h * a.group + (r - tok * a.group);
+          if (whole) {
+            const float inv = l_all[i] == 0.f ? 0.f : 1.f / l_all[i];
+            uint16_t* op = a.out + static_cast<int64_t>(seg.token0 + tok) * a.o_token +
+                           static_cast<int64_t>(head) * a.o_head;
+#pragma unroll
+            for (int n = 0; n < DH / 8; ++n)
+              if (n * 8 < a.head_dim)
+                *reinterpret_cast<uint32_t*>(op + n * 8 + tid * 2) =
+                    pack16x2<kBf16>(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
+            if (a.lse != nullptr && tid == 0)
+              a.lse[static_cast<int64_t>(seg.token0 + tok) * a.heads + head] =
+                  (m_all[i] + log2f(l_all[i])) * 0.69314718055994531f;
+          } else {
+            float* po = pieces.o + (slot * kAttnRows + r) * DH;
+#pragma unroll
+            for (int n = 0; n < DH / 8; ++n)
+              *reinterpret_cast<float2*>(po + n * 8 + tid * 2) =
+                  make_float2(o[n][2 * i], o[n][2 * i + 1]);
+            if (tid == 0)
+              *reinterpret_cast<float2*>(pieces.ml + (slot * kAttnRows + r) * 2) =
+                  make_float2(m_all[i], l_all[i]);
+          }
+        }
+        if (seg.begins() && !seg.ends())
+          meta = AttnMeta{seg.b, seg.h, seg.rt, attn_pieces(seg, sh->start.per)};
+      }
+    }
+    if (threadIdx.x == 0) pieces.meta[blockIdx.x] = meta;
+  }
+  __syncwarp();
+  cta_sync_all();
+}
+
+template <int DH, bool kBf16>
+cudaError_t launch(const AttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                   cudaStream_t st) {
+  const cudaError_t e = ensure_dynamic_smem(
+      reinterpret_cast<const void*>(attn_rows_kernel<DH, kBf16>), smem_bytes<DH>());
+  if (e != cudaSuccess) return e;
+  return launch_ex(attn_rows_kernel<DH, kBf16>, dim3(a.plan.workers), dim3(kThreads),
+                   smem_bytes<DH>(), st, true, tmK, tmV, a,
+                   attn_pieces_at(a.workspace, a.plan.workers, kAttnRows));
+}
+
+}  // namespace
+
+cudaError_t launch_attn_rows(const AttnArgs& in, cudaStream_t st) {
+  AttnArgs a = in;
+  a.plan.tokens = kAttnRows / a.group;
+  a.plan.workers = device_sm_count();
+  a.plan.min_units = 1;
+  a.plan.whole = 0;
+  alignas(64) CUtensorMap tmK, tmV;
+  const bool paged = a.table != nullptr;
+  const uint64_t tokens = paged ? a.page_size : a.plan.total;
+  const uint64_t pages = paged ? a.n_pages : 1;
+  if (!tensor_map_kv(&tmK, a.k, a.bf16, a.head_dim, a.plan.kv_heads, tokens, pages, a.k_head,
+                     a.k_token, a.k_page, a.granule) ||
+      !tensor_map_kv(&tmV, a.v, a.bf16, a.head_dim, a.plan.kv_heads, tokens, pages, a.v_head,
+                     a.v_token, a.v_page, a.granule))
+    return cudaErrorInvalidValue;
+  cudaError_t e;
+  if (attn_width(a.head_dim) == 64)
+    e = a.bf16 ? launch<64, true>(a, tmK, tmV, st) : launch<64, false>(a, tmK, tmV, st);
+  else
+    e = a.bf16 ? launch<128, true>(a, tmK, tmV, st) : launch<128, false>(a, tmK, tmV, st);
+  if (e != cudaSuccess) return e;
+  return launch_attn_combine(a, kAttnRows, st);
+}
+
+}  // namespace engram

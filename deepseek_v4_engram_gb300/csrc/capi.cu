@@ -8,6 +8,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "attn.h"
 #include "engram.h"
 #include "kernels.h"
 #include "shard.h"
@@ -45,7 +46,7 @@ std::mutex g_mu;
 std::mutex g_dev_mu;
 int g_sm_count[kMaxDevices] = {};
 int g_fused_pairs[kMaxDevices] = {};
-constexpr int kMaxSmemKernels = 16;
+constexpr int kMaxSmemKernels = 32;
 const void* g_smem_kernel[kMaxDevices][kMaxSmemKernels] = {};
 
 int current_device() {
@@ -304,6 +305,29 @@ bool tensor_map_2d_bf16(void* map_out, const void* base, uint64_t inner, uint64_
   return r == CUDA_SUCCESS;
 }
 
+bool tensor_map_kv(void* map_out, const void* base, bool bf16, uint64_t dim, uint64_t heads,
+                   uint64_t tokens, uint64_t pages, int64_t head_stride, int64_t token_stride,
+                   int64_t page_stride, uint32_t granule) {
+  if (!have_encoder()) return false;
+  // a dimension of one element has no step: any stride that the encoder accepts will do
+  auto bytes = [&](uint64_t n, int64_t stride) { return (n > 1 ? uint64_t(stride) : dim) * 2; };
+  const cuuint64_t dims[4] = {dim, heads, tokens, pages};
+  const cuuint64_t strides[3] = {bytes(heads, head_stride), bytes(tokens, token_stride),
+                                 bytes(pages, page_stride)};
+  const cuuint32_t box[4] = {64, 1, granule, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(static_cast<CUtensorMap*>(map_out),
+                              bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                              4, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+uint32_t* device_error_word(cudaError_t* e) { return error_word(e); }
+
 // Smallest workspace engram_forward accepts for M tokens (0 for an invalid descriptor).
 size_t forward_min_workspace_bytes(const engram_desc_t* desc, int64_t M) {
   if (check_desc(desc) != ENGRAM_OK || M < 0) return 0;
@@ -343,9 +367,9 @@ ENGRAM_API int engram_check_errors(void* stream, uint32_t* bits_out) {
   if (bits_out) *bits_out = bits;
   if (bits == 0) return ENGRAM_OK;
   if (bits == ENGRAM_DEVERR_CACHE_FULL)
-    return fail(ENGRAM_ECAPACITY, "a look-back cache ran out of capacity");
+    return fail(ENGRAM_ECAPACITY, "a look-back or paged cache ran out of capacity");
   return fail(ENGRAM_EDEVICE, "device error word 0x%x (1 token range, 2 cache full, 4 id range, "
-              "8 wait timeout)", bits);
+              "8 wait timeout, 16 page range)", bits);
 }
 
 ENGRAM_API int engram_hash(const engram_desc_t* desc, const engram_tables_t* tables,

@@ -53,7 +53,7 @@ extern "C" {
 typedef enum engram_status {
   ENGRAM_OK = 0,
   ENGRAM_EINVAL = 1,       /* bad argument: NULL, negative size, misaligned, aliasing, geometry */
-  ENGRAM_ECAPACITY = 2,    /* a look-back cache ran out of capacity (device-detected)        */
+  ENGRAM_ECAPACITY = 2,    /* a cache ran out of capacity (device-detected)                  */
   ENGRAM_ECUDA = 3,        /* a CUDA runtime call or launch failed                             */
   ENGRAM_EDEVICE = 4,      /* the device error word was set (see engram_check_errors)         */
   ENGRAM_EUNSUPPORTED = 5  /* valid, but outside the shapes these kernels implement           */
@@ -61,9 +61,10 @@ typedef enum engram_status {
 
 /* Device error word bits, as returned through engram_check_errors(..., &bits). */
 #define ENGRAM_DEVERR_TOKEN_RANGE 1u    /* token id outside [0, vocab)            */
-#define ENGRAM_DEVERR_CACHE_FULL 2u     /* cache_len + T > capacity                */
+#define ENGRAM_DEVERR_CACHE_FULL 2u     /* cache_len + T > capacity, kv_len > pages */
 #define ENGRAM_DEVERR_ID_RANGE 4u       /* hash id outside [0, num_embeddings)     */
 #define ENGRAM_DEVERR_WAIT_TIMEOUT 8u   /* a bounded in-kernel wait gave up        */
+#define ENGRAM_DEVERR_PAGE_RANGE 16u    /* page number outside [0, n_pages)        */
 
 /*
  * Geometry of one Engram layer (Engram listing, __init__: dim, hc_mult, the layout's n_heads,
@@ -413,6 +414,115 @@ ENGRAM_API int engram_graph_destroy(engram_graph_t* graph);
  */
 ENGRAM_API int engram_probe_stream_read(const void* src, size_t bytes, int32_t method,
                                         void* stream);
+
+/*
+ * The attention of the decoder layer that holds the block: over packed prompts, and over a paged
+ * cache that a prompt's keys and values were written to. The pages have no counterpart; a layer
+ * that serves prompts and decodes with engram_forward needs it next to the block.
+ *
+ *   n_heads query heads share n_kv_heads key-value heads: head h reads key-value head
+ *   h / (n_heads / n_kv_heads). dtype is the type of queries, keys, values and outputs. scale
+ *   multiplies the products q . k (usually head_dim^-1/2).
+ * Requirements: n_heads % n_kv_heads == 0; 1 <= head_dim <= 128, head_dim % 8 == 0; at most 16
+ * query heads per key-value head (else ENGRAM_EUNSUPPORTED); scale finite and > 0.
+ */
+#define ENGRAM_BF16 0
+#define ENGRAM_F16 1
+typedef struct engram_attn_desc {
+  int32_t n_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t dtype;
+  float scale;
+} engram_attn_desc_t;
+
+/*
+ * A tensor [tokens, heads, head_dim] of 16-bit values whose last dimension is dense: the strides
+ * of a token and of a head in elements, multiples of 8 and > 0 (one of a dimension of a single
+ * element is not read); ptr 16-byte aligned. So a part of a projection's output or of an array of
+ * either order of heads and tokens is passed as it lies.
+ */
+typedef struct engram_attn_view {
+  const void* ptr;
+  int64_t token_stride;
+  int64_t head_stride;
+} engram_attn_view_t;
+
+/*
+ * A paged cache: keys and values [n_pages, page_size, n_kv_heads, head_dim], each with its own
+ * element strides of a page, of a slot and of a head (as in engram_attn_view). page_size % 8 == 0.
+ * block_table int32 [n_seqs, table_width]: position p of sequence b is slot p % page_size of page
+ * block_table[b, p / page_size]; entries past a sequence's last position are not read.
+ */
+typedef struct engram_kv_cache {
+  const void* k;
+  const void* v;
+  int64_t k_page_stride, k_slot_stride, k_head_stride;
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+  int32_t n_pages;
+  int32_t page_size;
+  const int32_t* block_table;
+  int32_t table_width;
+} engram_kv_cache_t;
+
+/*
+ * Scratch for engram_attn_prompt and engram_attn_paged on the current device: the partial results
+ * of query tiles that were shared between SMs. It does not depend on the lengths. 256-byte
+ * aligned, not shared with a concurrent call; nothing in it needs to start at zero. 0 for a bad
+ * descriptor.
+ */
+ENGRAM_API size_t engram_attn_workspace_size(const engram_attn_desc_t* desc);
+
+/*
+ * Causal attention over whole prompts, packed: sequence b holds the tokens
+ * [cu_seqlens[b], cu_seqlens[b + 1]), and its token t sees its tokens 0 .. t:
+ *   out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j, h']) v[j, h'],  lse = ln sum_j exp(scale ...).
+ * Scores, maxima and sums in f32, probabilities rounded to dtype for the product with the values,
+ * one rounding of the result. Keys and values that a token does not see do not reach its row,
+ * whatever they hold (infinities and NaN too).
+ *   q, out [total, n_heads, head_dim]; k, v [total, n_kv_heads, head_dim]; cu_seqlens int32
+ *   [n_seqs + 1] (device); lse f32 [total, n_heads] or NULL. Tokens of no sequence are not
+ *   written. cu_seqlens is clamped to [0, total]. total < 2^24.
+ * total = 0 or n_seqs = 0 launches nothing. out must not overlap q, k or v.
+ */
+ENGRAM_API int engram_attn_prompt(const engram_attn_desc_t* desc, const engram_attn_view_t* q,
+                                  const engram_attn_view_t* k, const engram_attn_view_t* v,
+                                  const int32_t* cu_seqlens, int32_t n_seqs, int32_t total,
+                                  const engram_attn_view_t* out, float* lse, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of a chunk of new tokens per sequence over a paged cache (one token each: decoding).
+ * Sequence b's chunk is the tokens [cu_seqlens[b], cu_seqlens[b + 1]) of q, n of them; its cache
+ * holds kv_len[b] positions, the chunk's own among them (engram_kv_append writes them first), and
+ * chunk token t sees the positions 0 .. kv_len[b] - n + t. A row that sees nothing (kv_len[b] < n,
+ * an empty cache) is written as zeros, with lse -infinity.
+ *   kv_len int32 [n_seqs]: cache_len as engram_forward leaves it after the same tokens. A length
+ *   beyond table_width * page_size is cut there and sets ENGRAM_DEVERR_CACHE_FULL; a page number
+ *   outside [0, n_pages) reads as zeros and sets ENGRAM_DEVERR_PAGE_RANGE.
+ *   max_q: the longest chunk, which picks the kernel (up to 16 rows of a key-value head take the
+ *   one made for decoding); a longer chunk than it says is computed all the same.
+ * Everything else as engram_attn_prompt. out must not overlap q or the cache.
+ */
+ENGRAM_API int engram_attn_paged(const engram_attn_desc_t* desc, const engram_attn_view_t* q,
+                                 const int32_t* cu_seqlens, int32_t n_seqs, int32_t total,
+                                 int32_t max_q, const int32_t* kv_len,
+                                 const engram_kv_cache_t* cache, const engram_attn_view_t* out,
+                                 float* lse, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
+ * Writes the keys and values [total, n_kv_heads, head_dim] of a chunk per sequence (cu_seqlens as
+ * in engram_attn_paged) into a paged cache: token t of n goes to position kv_len[b] - n + t, where
+ * kv_len already counts the chunk. A position before 0 is not kept; one beyond the block table is
+ * not written and sets ENGRAM_DEVERR_CACHE_FULL; nor is one whose page number is outside
+ * [0, n_pages), which sets ENGRAM_DEVERR_PAGE_RANGE. Slots of the same page given to two
+ * sequences are written by both, in no order.
+ */
+ENGRAM_API int engram_kv_append(const engram_attn_desc_t* desc, const engram_attn_view_t* k,
+                                const engram_attn_view_t* v, const int32_t* cu_seqlens,
+                                int32_t n_seqs, int32_t total, const int32_t* kv_len,
+                                const engram_kv_cache_t* cache, void* stream);
 
 #ifdef __cplusplus
 }
