@@ -70,6 +70,10 @@ constexpr int32_t attn_width(int32_t head_dim) { return head_dim <= 64 ? 64 : 12
 constexpr int32_t kAttnRows = 16;
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t st);
 
+// Items of up to 256 rows on tcgen05 (attn_tiles_sm103.cu): prompts and long chunks.
+constexpr int32_t kAttnItemRows = 256;
+cudaError_t launch_attn_tiles(const AttnArgs& a, cudaStream_t st);
+
 // Joins the pieces of items of `rows` rows.
 cudaError_t launch_attn_combine(const AttnArgs& a, int32_t rows, cudaStream_t st);
 
@@ -94,5 +98,15 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t st);
 bool tensor_map_kv(void* map_out, const void* base, bool bf16, uint64_t dim, uint64_t heads,
                    uint64_t tokens, uint64_t pages, int64_t head_stride, int64_t token_stride,
                    int64_t page_stride, uint32_t granule);
+
+// The tensor maps of a call's keys and values.
+inline bool attn_tensor_maps(const AttnArgs& a, void* k_map, void* v_map) {
+  const bool paged = a.table != nullptr;
+  const uint64_t tokens = paged ? a.page_size : a.plan.total, pages = paged ? a.n_pages : 1;
+  return tensor_map_kv(k_map, a.k, a.bf16, a.head_dim, a.plan.kv_heads, tokens, pages, a.k_head,
+                       a.k_token, a.k_page, a.granule) &&
+         tensor_map_kv(v_map, a.v, a.bf16, a.head_dim, a.plan.kv_heads, tokens, pages, a.v_head,
+                       a.v_token, a.v_page, a.granule);
+}
 
 }  // namespace engram

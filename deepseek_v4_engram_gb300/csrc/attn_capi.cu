@@ -36,8 +36,8 @@ int check_desc(const engram_attn_desc_t* d) {
     return fail(ENGRAM_EINVAL, "scale must be finite and > 0");
   if (d->head_dim > 128 || d->head_dim % 8 != 0)
     return fail(ENGRAM_EUNSUPPORTED, "head_dim must be a multiple of 8 up to 128");
-  if (d->n_heads / d->n_kv_heads > 16)
-    return fail(ENGRAM_EUNSUPPORTED, "at most 16 query heads per key-value head");
+  if (d->n_heads / d->n_kv_heads > 128)
+    return fail(ENGRAM_EUNSUPPORTED, "at most 128 query heads per key-value head");
   return ENGRAM_OK;
 }
 
@@ -173,7 +173,7 @@ extern "C" {
 
 ENGRAM_API size_t engram_attn_workspace_size(const engram_attn_desc_t* desc) {
   if (check_desc(desc) != ENGRAM_OK) return 0;
-  return attn_pieces_bytes(device_sm_count(), kAttnRows, attn_width(desc->head_dim));
+  return attn_pieces_bytes(device_sm_count(), kAttnItemRows, attn_width(desc->head_dim));
 }
 
 ENGRAM_API int engram_attn_prompt(const engram_attn_desc_t* desc, const engram_attn_view_t* q,
@@ -206,7 +206,7 @@ ENGRAM_API int engram_attn_prompt(const engram_attn_desc_t* desc, const engram_a
   a.v_token = v->token_stride;
   a.v_head = v->head_stride;
   a.granule = kTileKeys;
-  return report(launch_attn_rows(a, static_cast<cudaStream_t>(stream)), "engram_attn_prompt");
+  return report(launch_attn_tiles(a, static_cast<cudaStream_t>(stream)), "engram_attn_prompt");
 }
 
 ENGRAM_API int engram_attn_paged(const engram_attn_desc_t* desc, const engram_attn_view_t* q,
@@ -254,7 +254,9 @@ ENGRAM_API int engram_attn_paged(const engram_attn_desc_t* desc, const engram_at
   a.page_size = cache->page_size;
   a.n_pages = cache->n_pages;
   a.granule = granule_of(cache->page_size);
-  return report(launch_attn_rows(a, static_cast<cudaStream_t>(stream)), "engram_attn_paged");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool few = int64_t(max_q) * a.group <= kAttnRows;
+  return report(few ? launch_attn_rows(a, st) : launch_attn_tiles(a, st), "engram_attn_paged");
 }
 
 ENGRAM_API int engram_kv_append(const engram_attn_desc_t* desc, const engram_attn_view_t* k,

@@ -410,14 +410,7 @@ cudaError_t launch_attn_rows(const AttnArgs& in, cudaStream_t st) {
   a.plan.min_units = 1;
   a.plan.whole = 0;
   alignas(64) CUtensorMap tmK, tmV;
-  const bool paged = a.table != nullptr;
-  const uint64_t tokens = paged ? a.page_size : a.plan.total;
-  const uint64_t pages = paged ? a.n_pages : 1;
-  if (!tensor_map_kv(&tmK, a.k, a.bf16, a.head_dim, a.plan.kv_heads, tokens, pages, a.k_head,
-                     a.k_token, a.k_page, a.granule) ||
-      !tensor_map_kv(&tmV, a.v, a.bf16, a.head_dim, a.plan.kv_heads, tokens, pages, a.v_head,
-                     a.v_token, a.v_page, a.granule))
-    return cudaErrorInvalidValue;
+  if (!attn_tensor_maps(a, &tmK, &tmV)) return cudaErrorInvalidValue;
   cudaError_t e;
   if (attn_width(a.head_dim) == 64)
     e = a.bf16 ? launch<64, true>(a, tmK, tmV, st) : launch<64, false>(a, tmK, tmV, st);

@@ -1,0 +1,620 @@
+// Attention for items of many query rows, prompts and long chunks, on tcgen05.
+//
+// An item is up to 256 rows (tokens x the query heads that share a key-value head), two row tiles
+// of 128; key tiles of 128 pass by once:
+//   S_t = Q_t K^T                 tcgen05.mma, both operands in shared memory, f32 in TMEM
+//   P_t = 2^(c S_t - c M_t)       one thread per row, in registers; M_t the row's maximum
+//   O_t = O_t + P_t V             tcgen05.mma, P_t from TMEM (it takes the place of S_t), V as it
+//                                 lies: its rows are keys, so it enters transposed (MN-major)
+// with c = scale log2(e). Bound by the tensor cores for heads of 128 columns: a tile pair costs
+// 4 * 128 * 128 * D multiply-adds there and 2 * 128 * 128 exponentials on the special-function
+// units, which are the nearer bound for heads of 64. So the two row tiles take turns: while the
+// tensor cores work on one, the other's softmax runs. Both read the same key and value tiles.
+//
+// The maximum that a row subtracts lags: it is only raised when a tile exceeds it by more than
+// 2^8, because raising it means rescaling O in TMEM. Probabilities are then up to 2^8 instead of
+// 1, which f32 sums and both 16-bit types hold as exactly, and the result is the same quotient.
+//
+// Roles (384 threads): warps 0-3 and 4-7 softmax and output of row tile 0 and 1 (thread = row =
+// TMEM lane); warp 8 issues the MMAs; warp 9 requests key and value tiles by TMA (one page granule
+// per lane); warp 10 gathers the rows of Q, in any strides, with cp.async; warp 11 makes the
+// values that some row of the item must not see harmless (below). Registers: the softmax warps
+// hold a row of 128 scores, so they take 208 each and the other four 88.
+//
+// A probability of 0 does not undo an infinity or NaN that it multiplies. In the tiles that reach
+// past what the item's first row sees, warp 11 clears the value rows that no row sees (another
+// sequence's, or memory that was never written) and replaces infinities and NaN in the others by
+// 0; if it replaced any, the rows that do see them get them added at the end.
+#include "attn_device.cuh"
+#include "kernels.h"
+#include "wkv_tiles.cuh"
+
+namespace engram {
+
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kTileRows = 128;
+constexpr int kItemRows = kAttnItemRows;   // two row tiles
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 256 * 208 + 128 * 88 = 384 * 168
+constexpr int kPoisonSlots = 8;
+
+template <int DH>
+struct Geo {
+  static constexpr int kHalves = DH / 64;
+  static constexpr int kTileBytes = 128 * DH * 2;            // a tile of Q, K or V
+  static constexpr int kStages = DH == 128 ? 5 : 10;         // of one K or V tile each
+  static constexpr uint32_t kO = 256;                        // TMEM columns: S0 S1 O0 O1
+};
+
+template <int DH>
+struct Shared {
+  uint64_t full[Geo<DH>::kStages], empty[Geo<DH>::kStages], vok[Geo<DH>::kStages];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2];
+  uint64_t drain;
+  AttnStart start;
+  int poison[kPoisonSlots];
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int DH>
+constexpr size_t smem_bytes() {
+  return 1024 + size_t(2 + Geo<DH>::kStages) * Geo<DH>::kTileBytes + sizeof(Shared<DH>);
+}
+
+// Instruction descriptor: f32 accumulator, A and B bf16 or f16, B K-major or (transposed)
+// MN-major.
+template <bool kBf16>
+constexpr uint32_t idesc(int M, int N, bool b_mn) {
+  return (1u << 4) | ((kBf16 ? 1u : 0u) << 7) | ((kBf16 ? 1u : 0u) << 10) |
+         ((b_mn ? 1u : 0u) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// Shared-memory descriptor of a 128-byte-swizzled tile read MN-major: rows are K (keys), 64
+// columns of 128 B per box; boxes of 128 rows 16 KB apart (leading), 8-row groups 1 KB apart.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((128u * 128u) >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], A 16-bit pairs in 32-bit columns.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                          uint32_t id, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(id), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(
+          r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void set_max_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(real ? 16 : 0)
+               : "memory");
+}
+
+// Pairs of f32 in one 64-bit register: two multiply-adds or adds per instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Value row of position `pos` (for the rare rows that see an infinity or NaN).
+__device__ __forceinline__ const uint16_t* value_row(const AttnArgs& a, const AttnSegment& s,
+                                                     int32_t pos) {
+  if (a.table == nullptr) return a.v + (int64_t(s.seq.q0) + pos) * a.v_token + s.h * a.v_head;
+  const int32_t col = pos / a.page_size;
+  const int32_t page = a.table[int64_t(s.b) * a.table_width + col];
+  if (page < 0 || page >= a.n_pages) return nullptr;   // read as zeros
+  return a.v + page * a.v_page + (pos - int64_t(col) * a.page_size) * a.v_token + s.h * a.v_head;
+}
+
+template <int DH, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK,
+                      const __grid_constant__ CUtensorMap tmV, const AttnArgs a,
+                      const AttnPieces pieces) {
+  using G = Geo<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_1024(smem_raw);
+  uint8_t* sQ = smem;
+  uint8_t* sKV = smem + 2 * G::kTileBytes;
+  Shared<DH>* sh = reinterpret_cast<Shared<DH>*>(sKV + G::kStages * G::kTileBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < G::kStages; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], 2);   // the MMAs that read it, and warp 11
+      mbar_init(&sh->vok[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh->qfull[t], 1);
+      mbar_init(&sh->qempty[t], 1);
+      mbar_init(&sh->sfull[t], 1);
+      mbar_init(&sh->pfull[t], 4);   // a lane of each warp
+      mbar_init(&sh->ofull[t], 1);
+    }
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+  }
+  if (warp == 8) {
+    tmem_alloc(&sh->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  pdl_wait();   // queries, lengths and the cache may come from the previous kernel
+  pdl_launch_dependents();
+  attn_find_start<kThreads>(a.plan, blockIdx.x, &sh->start, a.err);   // synchronises the CTA
+  tc_fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  volatile int* abort = &sh->abort;
+  AttnCursor cur = sh->start.cursor;
+  AttnSegment seg;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------- softmax and output
+    set_max_regs_up<kSoftmaxRegs>();
+    const int t = warp >> 2;
+    const int32_t row = t * kTileRows + (warp & 3) * 32 + lane;   // of the item
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + t * 128, tO = tmem + lanes + G::kO + t * DH;
+    const float c = a.scale_log2;
+    const int32_t tok = row / a.group, sub = row - tok * a.group;
+    uint32_t s_phase = 0, o_phase = 0, count = 0;
+    AttnMeta meta{0, 0, 0, 0};
+    while (cur.next(a.plan, seg)) {
+      if (threadIdx.x == 0 && seg.begins() && !seg.ends())
+        meta = AttnMeta{seg.b, seg.h, seg.rt, attn_pieces(seg, sh->start.per)};
+      const bool tiles = seg.keys > 0;
+      const uint32_t slot8 = count % kPoisonSlots;
+      if (tiles) ++count;
+      if (t * kTileRows >= seg.ntok * a.group) continue;   // this row tile is empty
+      const bool valid = tok < seg.ntok;
+      const int32_t lim = seg.seq.m - seg.seq.n + (seg.token0 - seg.seq.q0) + tok + 1;
+      const int32_t limit = valid && lim > 0 ? lim : 0;
+      float m = -INFINITY, l = 0.f;
+      if (tiles) {
+        for (int32_t j = seg.tile0; j < seg.tile1; ++j) {
+          attn_wait(&sh->sfull[t], s_phase, abort, a.err);
+          s_phase ^= 1u;
+          tc_fence_after();
+          uint32_t s[4][32];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tc_ld_32x32b_x32(tS + i * 32, s[i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tc_wait_ld(s[i]);
+          const int32_t left = limit - j * kTileKeys;   // keys of the tile that this row sees
+          if (__any_sync(0xFFFFFFFFu, left < kTileKeys)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (i * 32 + e >= left) s[i][e] = 0xFF800000u;   // -infinity
+          }
+          float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mt[i] = fmaxf(mt[i], __uint_as_float(s[i][e]));
+          const float top = fmaxf(m, fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])));
+          if (j == seg.tile0) {
+            m = top;
+          } else if (__any_sync(0xFFFFFFFFu, (top - m) * c > 8.f)) {
+            // The score MMA that this tile waited for came after the last product with V, so O
+            // is at rest.
+            const float f = m == -INFINITY ? 0.f : exp2_fast((m - top) * c);
+            m = top;
+            l *= f;
+#pragma unroll 1
+            for (int i = 0; i < DH / 32; ++i) {
+              uint32_t o[32];
+              tc_ld_32x32b_x32(tO + i * 32, o);
+              tc_wait_ld(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tc_st_32x32b_x32(tO + i * 32, o);
+            }
+          }
+          const float base = m == -INFINITY ? 0.f : -m * c;
+          const uint64_t c2 = pair(c, c), b2 = pair(base, base);
+          uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float x, y;
+              unpair(fma2(pair(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])), c2,
+                          b2),
+                     x, y);
+              x = exp2_fast(x);
+              y = exp2_fast(y);
+              sum[e & 1] = add2(sum[e & 1], pair(x, y));
+              p[e] = pack16x2<kBf16>(x, y);
+            }
+            tc_st_32x32b_x16(tS + i * 16, p);
+          }
+          tc_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->pfull[t]);
+          float x, y;
+          unpair(add2(sum[0], sum[1]), x, y);
+          l += x + y;
+        }
+        attn_wait(&sh->ofull[t], o_phase, abort, a.err);
+        o_phase ^= 1u;
+        tc_fence_after();
+      }
+      const bool whole = seg.begins() && seg.ends();
+      const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+      const int32_t head = seg.h * a.group + sub;
+      const int64_t slot =
+          (static_cast<int64_t>(blockIdx.x) * 2 + (seg.begins() ? 1 : 0)) * kItemRows + row;
+      const bool poison = tiles && *static_cast<volatile int*>(&sh->poison[slot8]) != 0;
+#pragma unroll 1
+      for (int i = 0; i < DH / 32; ++i) {
+        uint32_t o[32];
+        if (tiles) {
+          tc_ld_32x32b_x32(tO + i * 32, o);
+          tc_wait_ld(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        if (poison) {
+          const int32_t k0 = seg.first_keys > seg.tile0 * kTileKeys ? seg.first_keys
+                                                                    : seg.tile0 * kTileKeys;
+          const int32_t k1 = limit < seg.tile1 * kTileKeys ? limit : seg.tile1 * kTileKeys;
+          for (int32_t k = k0; k < k1; ++k) {
+            const uint16_t* v = value_row(a, seg, k);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (v == nullptr || i * 32 + e >= a.head_dim) continue;
+              const float x = to_f32<kBf16>(v[i * 32 + e]);
+              if (!(fabsf(x) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+            }
+          }
+        }
+        if (!valid) continue;
+        if (whole) {
+          uint16_t* op = a.out + static_cast<int64_t>(seg.token0 + tok) * a.o_token +
+                         static_cast<int64_t>(head) * a.o_head + i * 32;
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = pack16x2<kBf16>(__uint_as_float(o[8 * v + 2 * e]) * inv,
+                                     __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
+            if (i * 32 + v * 8 < a.head_dim)
+              *reinterpret_cast<uint4*>(op + v * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else {
+          uint4* op = reinterpret_cast<uint4*>(pieces.o + slot * DH + i * 32);
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            op[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+        }
+      }
+      tc_fence_before();   // the next product into O follows this thread's next P
+      if (valid) {
+        if (!whole)
+          *reinterpret_cast<float2*>(pieces.ml + slot * 2) = make_float2(m * c, l);
+        else if (a.lse != nullptr)
+          a.lse[static_cast<int64_t>(seg.token0 + tok) * a.heads + head] =
+              (m * c + log2f(l)) * 0.69314718055994531f;
+      }
+      __syncwarp();
+    }
+    if (threadIdx.x == 0) pieces.meta[blockIdx.x] = meta;
+  } else {
+    set_max_regs_down<kOtherRegs>();
+    if (warp == 8) {
+      // ----------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t kIdS = idesc<kBf16>(128, 128, false), kIdO = idesc<kBf16>(128, DH, true);
+        uint32_t stage = 0, phase = 0;           // next K or V tile
+        uint32_t vphase = 0;                     // per stage: parity of its next vok
+        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        bool ok = true;
+        auto scores = [&](int t, uint32_t ks) {
+          const uint32_t q = smem_u32(sQ + t * G::kTileBytes);
+          const uint32_t k = smem_u32(sKV + ks * G::kTileBytes);
+#pragma unroll
+          for (int kk = 0; kk < DH / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (128 * 128);
+            tc_mma_bf16(tmem + t * 128, sw128_kmajor_desc(q + off) + 2ull * (kk & 3),
+                        sw128_kmajor_desc(k + off) + 2ull * (kk & 3), kIdS, kk != 0);
+          }
+          tc_commit(&sh->sfull[t]);
+        };
+        while (ok && cur.next(a.plan, seg)) {
+          if (seg.keys == 0) continue;
+          const int nt = seg.ntok * a.group > kTileRows ? 2 : 1;
+          const int32_t n = seg.tile1 - seg.tile0;
+          // scores of the first tile
+          ok = ok && attn_wait(&sh->full[stage], phase, abort, a.err);
+          for (int t = 0; t < nt && ok; ++t) {
+            ok = attn_wait(&sh->qfull[t], q_phase[t], abort, a.err);
+            if (!ok) break;
+            q_phase[t] ^= 1u;
+            tc_fence_after();
+            scores(t, stage);
+            if (n == 1) tc_commit(&sh->qempty[t]);
+          }
+          if (!ok) break;
+          tc_commit(&sh->empty[stage]);
+          if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+          for (int32_t j = 0; j < n && ok; ++j) {
+            const uint32_t vs = stage, vph = phase;
+            if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+            const uint32_t ks = stage, kph = phase;
+            const bool more = j + 1 < n;
+            const bool guarded = (seg.tile0 + j + 1) * kTileKeys > seg.first_keys;
+            for (int t = 0; t < nt && ok; ++t) {
+              ok = attn_wait(&sh->pfull[t], p_phase[t], abort, a.err);
+              p_phase[t] ^= 1u;
+              if (t == 0 && ok) {
+                if (guarded) {
+                  ok = attn_wait(&sh->vok[vs], (vphase >> vs) & 1u, abort, a.err);
+                  vphase ^= 1u << vs;
+                } else {
+                  ok = attn_wait(&sh->full[vs], vph, abort, a.err);
+                }
+              }
+              if (!ok) break;
+              tc_fence_after();
+              const uint32_t v = smem_u32(sKV + vs * G::kTileBytes);
+#pragma unroll
+              for (int kk = 0; kk < kTileKeys / 16; ++kk)
+                tc_mma_ts(tmem + G::kO + t * DH, tmem + t * 128 + kk * 8,
+                          sw128_mnmajor_desc(v + kk * 16 * 128), kIdO, (j | kk) != 0);
+              if (!more) {
+                tc_commit(&sh->ofull[t]);
+              } else {
+                if (t == 0) {
+                  ok = attn_wait(&sh->full[ks], kph, abort, a.err);
+                  if (!ok) break;
+                  tc_fence_after();
+                }
+                scores(t, ks);
+                if (j + 2 == n) tc_commit(&sh->qempty[t]);
+              }
+            }
+            if (!ok) break;
+            tc_commit(&sh->empty[vs]);
+            if (more) {
+              tc_commit(&sh->empty[ks]);
+              if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+            }
+          }
+        }
+        // Every MMA this thread issued has finished before TMEM is released.
+        tc_commit(&sh->drain);
+        mbar_wait_drain(&sh->drain, 0);
+      }
+    } else if (warp == 9) {
+      // ----------------------------------------------------------- TMA producer
+      TmaRingT<G::kStages> ring;
+      bool stop = false;
+      while (!stop && cur.next(a.plan, seg)) {
+        if (seg.keys == 0) continue;
+        for (int32_t j = seg.tile0; j < seg.tile1 && !stop; ++j) {
+          const int32_t k0 = j * kTileKeys;
+          const int32_t n = seg.keys - k0 < kTileKeys ? seg.keys - k0 : kTileKeys;
+          const int32_t grans = (n + a.granule - 1) / a.granule;
+          KvPlace at{0, 0};
+          if (lane < grans) at = kv_place(a, seg.seq, seg.b, k0 + lane * a.granule);
+          for (int kv = 0; kv < 2; ++kv) {
+            stop = __any_sync(0xFFFFFFFFu, !ring.acquire(sh->empty, abort, a.err));
+            if (stop) break;
+            uint8_t* dst = sKV + ring.stage * G::kTileBytes;
+            if (lane == 0)
+              mbar_arrive_expect_tx(&sh->full[ring.stage],
+                                    static_cast<uint32_t>(grans * a.granule) * 128 * G::kHalves);
+            __syncwarp();
+            if (lane < grans) {
+#pragma unroll
+              for (int hf = 0; hf < G::kHalves; ++hf)
+                tma_load_4d(dst + hf * (128 * 128) + lane * a.granule * 128, kv ? &tmV : &tmK,
+                            &sh->full[ring.stage], hf * 64, seg.h, at.z, at.w);
+            }
+            ring.issued();
+          }
+        }
+      }
+      __syncwarp();
+      ring.drain(sh->full);
+    } else if (warp == 10) {
+      // ----------------------------------------------------------- rows of Q
+      uint32_t q_phase[2] = {0, 0};
+      constexpr int kChunks = DH / 8, kStep = 32 / kChunks;   // rows per pass of the warp
+      const int ch = lane % kChunks;
+      while (cur.next(a.plan, seg)) {
+        if (seg.keys == 0) continue;
+        const int32_t rows = seg.ntok * a.group;
+        for (int t = 0; t * kTileRows < rows; ++t) {
+          attn_wait(&sh->qempty[t], q_phase[t] ^ 1u, abort, a.err);
+          q_phase[t] ^= 1u;
+          int32_t r = lane / kChunks;
+          int32_t tk = (t * kTileRows + r) / a.group;
+          int32_t sub = t * kTileRows + r - tk * a.group;
+          const uint32_t dst = smem_u32(sQ + t * G::kTileBytes) + (ch >> 3) * (128 * 128);
+#pragma unroll 4
+          for (; r < kTileRows; r += kStep) {
+            const bool real = t * kTileRows + r < rows && ch * 8 < a.head_dim;
+            const uint16_t* src = a.q;
+            if (real)
+              src += static_cast<int64_t>(seg.token0 + tk) * a.q_token +
+                     static_cast<int64_t>(seg.h * a.group + sub) * a.q_head + ch * 8;
+            cp_async_16(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, real);
+            sub += kStep;
+            while (sub >= a.group) {
+              sub -= a.group;
+              ++tk;
+            }
+          }
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh->qfull[t]);
+        }
+      }
+    } else {
+      // ----------------------------------------------------------- values nobody may see
+      uint32_t stage = 0, phase = 0, count = 0;
+      while (cur.next(a.plan, seg)) {
+        if (seg.keys == 0) continue;
+        const uint32_t slot8 = count++ % kPoisonSlots;
+        if (lane == 0) sh->poison[slot8] = 0;
+        __syncwarp();
+        for (int32_t j = seg.tile0; j < seg.tile1; ++j) {
+          for (int kv = 0; kv < 2; ++kv) {
+            attn_wait(&sh->full[stage], phase, abort, a.err);
+            __syncwarp();
+            if (kv == 1 && (j + 1) * kTileKeys > seg.first_keys) {
+              const uint32_t v = smem_u32(sKV + stage * G::kTileBytes);
+              int32_t r0 = seg.first_keys - j * kTileKeys;
+              if (r0 < 0) r0 = 0;
+              const int32_t r1 = seg.keys - j * kTileKeys;   // rows from here on: nobody's
+              constexpr int kChunks = DH / 8;
+              bool found = false;
+#pragma unroll 4
+              for (int32_t i = r0 * kChunks + lane; i < kTileKeys * kChunks; i += 32) {
+                const int32_t r = i / kChunks, ch = i % kChunks;
+                const uint32_t at = v + (ch >> 3) * (128 * 128) + r * 128 +
+                                    (((ch & 7) ^ (r & 7)) << 4);
+                if (r >= r1) {
+                  sts128(at, make_uint4(0, 0, 0, 0));
+                  continue;
+                }
+                const uint4 w = lds128(at);
+                uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                bool bad = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) bad |= any_nonfinite<kBf16>(x[e]);
+                if (bad) {
+                  found = true;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    if (any_nonfinite<kBf16>(x[e] & 0xFFFFu)) x[e] &= 0xFFFF0000u;
+                    if (any_nonfinite<kBf16>(x[e] & 0xFFFF0000u)) x[e] &= 0xFFFFu;
+                  }
+                  sts128(at, make_uint4(x[0], x[1], x[2], x[3]));
+                }
+              }
+              if (found) *static_cast<volatile int*>(&sh->poison[slot8]) = 1;
+              fence_proxy_async_shared();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh->vok[stage]);
+            }
+            if (lane == 0) mbar_arrive(&sh->empty[stage]);
+            if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  cta_sync_all();   // every role is done with TMEM (each thread counted on its own)
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int DH, bool kBf16>
+cudaError_t launch(const AttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
+                   cudaStream_t st) {
+  const cudaError_t e = ensure_dynamic_smem(
+      reinterpret_cast<const void*>(attn_tiles_kernel<DH, kBf16>), smem_bytes<DH>());
+  if (e != cudaSuccess) return e;
+  return launch_ex(attn_tiles_kernel<DH, kBf16>, dim3(a.plan.workers), dim3(kThreads),
+                   smem_bytes<DH>(), st, true, tmK, tmV, a,
+                   attn_pieces_at(a.workspace, a.plan.workers, kItemRows));
+}
+
+}  // namespace
+
+cudaError_t launch_attn_tiles(const AttnArgs& in, cudaStream_t st) {
+  AttnArgs a = in;
+  a.plan.tokens = kItemRows / a.group;
+  a.plan.workers = device_sm_count();
+  a.plan.min_units = 1;
+  a.plan.whole = 0;
+  alignas(64) CUtensorMap tmK, tmV;
+  if (!attn_tensor_maps(a, &tmK, &tmV)) return cudaErrorInvalidValue;
+  cudaError_t e;
+  if (attn_width(a.head_dim) == 64)
+    e = a.bf16 ? launch<64, true>(a, tmK, tmV, st) : launch<64, false>(a, tmK, tmV, st);
+  else
+    e = a.bf16 ? launch<128, true>(a, tmK, tmV, st) : launch<128, false>(a, tmK, tmV, st);
+  if (e != cudaSuccess) return e;
+  return launch_attn_combine(a, kItemRows, st);
+}
+
+}  // namespace engram

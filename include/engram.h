@@ -423,7 +423,7 @@ ENGRAM_API int engram_probe_stream_read(const void* src, size_t bytes, int32_t m
  *   n_heads query heads share n_kv_heads key-value heads: head h reads key-value head
  *   h / (n_heads / n_kv_heads). dtype is the type of queries, keys, values and outputs. scale
  *   multiplies the products q . k (usually head_dim^-1/2).
- * Requirements: n_heads % n_kv_heads == 0; 1 <= head_dim <= 128, head_dim % 8 == 0; at most 16
+ * Requirements: n_heads % n_kv_heads == 0; 1 <= head_dim <= 128, head_dim % 8 == 0; at most 128
  * query heads per key-value head (else ENGRAM_EUNSUPPORTED); scale finite and > 0.
  */
 #define ENGRAM_BF16 0

@@ -69,6 +69,12 @@ def test_prompt_odd_widths(head_dim):
     check_prompt([150, 29], 6, 2, head_dim, F16, seed=4)
 
 
+@pytest.mark.parametrize("heads,kv_heads", [(17, 1), (64, 2), (100, 1), (128, 1)])
+def test_many_heads_share_a_key(heads, kv_heads):
+    check_prompt([70, 1, 5], heads, kv_heads, 64, BF16, seed=16)
+    check_paged([1, 2, 9], [5, 300, 1031], 16, heads, kv_heads, 128, F16, seed=16)
+
+
 def test_prompt_separate_buffers_and_orders():
     check_prompt([260, 31], 8, 4, 64, BF16, seed=5, fused=False)
 
