@@ -92,21 +92,21 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t st);
 
-// Tensor map of the keys or values (capi.cu): element (d, head, token, page) of a 16-bit tensor
-// with the given strides in elements, boxes of 64 columns of one head by `granule` tokens, with
-// the 128-byte swizzle; columns past `dim` read as zero.
-bool tensor_map_kv(void* map_out, const void* base, bool bf16, uint64_t dim, uint64_t heads,
-                   uint64_t tokens, uint64_t pages, int64_t head_stride, int64_t token_stride,
-                   int64_t page_stride, uint32_t granule);
+// Tensor map of queries, keys or values (capi.cu): element (d, head, token, page) of a 16-bit tensor
+// with the given strides in elements, boxes of 64 columns of `box_heads` heads by `box_tokens`
+// tokens, with the 128-byte swizzle; columns past `dim` read as zero.
+bool tensor_map_attn(void* map_out, const void* base, bool bf16, uint64_t dim, uint64_t heads,
+                     uint64_t tokens, uint64_t pages, int64_t head_stride, int64_t token_stride,
+                     int64_t page_stride, uint32_t box_heads, uint32_t box_tokens);
 
 // The tensor maps of a call's keys and values.
 inline bool attn_tensor_maps(const AttnArgs& a, void* k_map, void* v_map) {
   const bool paged = a.table != nullptr;
   const uint64_t tokens = paged ? a.page_size : a.plan.total, pages = paged ? a.n_pages : 1;
-  return tensor_map_kv(k_map, a.k, a.bf16, a.head_dim, a.plan.kv_heads, tokens, pages, a.k_head,
-                       a.k_token, a.k_page, a.granule) &&
-         tensor_map_kv(v_map, a.v, a.bf16, a.head_dim, a.plan.kv_heads, tokens, pages, a.v_head,
-                       a.v_token, a.v_page, a.granule);
+  return tensor_map_attn(k_map, a.k, a.bf16, a.head_dim, a.plan.kv_heads, tokens, pages, a.k_head,
+                         a.k_token, a.k_page, 1, a.granule) &&
+         tensor_map_attn(v_map, a.v, a.bf16, a.head_dim, a.plan.kv_heads, tokens, pages, a.v_head,
+                         a.v_token, a.v_page, 1, a.granule);
 }
 
 }  // namespace engram

@@ -22,11 +22,18 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Whether one of the two 16-bit values in `w` is an infinity or NaN.
+// Not zero where one of the two 16-bit values in `w` is an infinity or NaN: one added to an
+// exponent of all ones carries into the sign's place.
 template <bool kBf16>
-__device__ __forceinline__ bool any_nonfinite(uint32_t w) {
-  constexpr uint32_t e = kBf16 ? 0x7F80u : 0x7C00u;
-  return (w & e) == e || (w & (e << 16)) == (e << 16);
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) {
+  return ((w & 0x7FFF7FFFu) + (kBf16 ? 0x00800080u : 0x04000400u)) & 0x80008000u;
+}
+
+// `w` with an infinity or NaN replaced by 0.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+  const uint32_t b = nonfinite_bits<kBf16>(w);
+  return w & ((b & 0x8000u ? 0u : 0x0000FFFFu) | (b & 0x80000000u ? 0u : 0xFFFF0000u));
 }
 
 template <bool kBf16>

@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               uint32_t b[4];
               ldmatrix_x4_trans(b, sv + tile_offset(row, n * 2 + (lane >> 4)));
 #pragma unroll
-              for (int e = 0; e < 4; ++e) bad |= any_nonfinite<kBf16>(b[e] & keep[e & 1]);
+              for (int e = 0; e < 4; ++e) bad |= nonfinite_bits<kBf16>(b[e] & keep[e & 1]) != 0;
             }
             if (!__any_sync(0xFFFFFFFFu, bad)) {
 #pragma unroll

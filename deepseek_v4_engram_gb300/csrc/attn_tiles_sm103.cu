@@ -17,14 +17,15 @@
 //
 // Roles (384 threads): warps 0-3 and 4-7 softmax and output of row tile 0 and 1 (thread = row =
 // TMEM lane); warp 8 issues the MMAs; warp 9 requests key and value tiles by TMA (one page granule
-// per lane); warp 10 gathers the rows of Q, in any strides, with cp.async; warp 11 makes the
-// values that some row of the item must not see harmless (below). Registers: the softmax warps
-// hold a row of 128 scores, so they take 208 each and the other four 88.
+// per lane) and each item's queries (a box of its tokens by the heads that share its key-value
+// head is the item's rows in order, whatever their number); warps 10-11 make the values that some
+// row of the item must not see harmless (below). Registers: the softmax warps hold a row of 128
+// scores, so they take 208 each and the other four 88.
 //
 // A probability of 0 does not undo an infinity or NaN that it multiplies. In the tiles that reach
-// past what the item's first row sees, warp 11 clears the value rows that no row sees (another
-// sequence's, or memory that was never written) and replaces infinities and NaN in the others by
-// 0; if it replaced any, the rows that do see them get them added at the end.
+// past what the item's first row sees, warps 10-11 clear the value rows that no row sees (another
+// sequence's, or memory that was never written) and replace infinities and NaN in the others by
+// 0; if they replaced any, the rows that do see them get them added at the end.
 #include "attn_device.cuh"
 #include "kernels.h"
 #include "wkv_tiles.cuh"
@@ -50,10 +51,10 @@ struct Geo {
 template <int DH>
 struct Shared {
   uint64_t full[Geo<DH>::kStages], empty[Geo<DH>::kStages], vok[Geo<DH>::kStages];
-  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2];
+  uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2];
   uint64_t drain;
   AttnStart start;
-  int poison[kPoisonSlots];
+  int poison[2][kPoisonSlots];   // of warps 10 and 11, by segment
   uint32_t tmem_base;
   int abort;
 };
@@ -130,12 +131,6 @@ __device__ __forceinline__ void set_max_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(real ? 16 : 0)
-               : "memory");
-}
-
 // Pairs of f32 in one 64-bit register: two multiply-adds or adds per instruction.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;
@@ -168,13 +163,14 @@ __device__ __forceinline__ const uint16_t* value_row(const AttnArgs& a, const At
 
 template <int DH, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tiles_kernel(const __grid_constant__ CUtensorMap tmK,
+    attn_tiles_kernel(const __grid_constant__ CUtensorMap tmQ,
+                      const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const AttnArgs a,
                       const AttnPieces pieces) {
   using G = Geo<DH>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
-  uint8_t* sQ = smem;
+  uint8_t* sQ = smem;                       // 64-column boxes of 256 rows
   uint8_t* sKV = smem + 2 * G::kTileBytes;
   Shared<DH>* sh = reinterpret_cast<Shared<DH>*>(sKV + G::kStages * G::kTileBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -182,12 +178,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < G::kStages; ++s) {
       mbar_init(&sh->full[s], 1);
-      mbar_init(&sh->empty[s], 2);   // the MMAs that read it, and warp 11
-      mbar_init(&sh->vok[s], 1);
+      mbar_init(&sh->empty[s], 3);   // the MMAs that read it, and warps 10 and 11
+      mbar_init(&sh->vok[s], 2);
     }
+    mbar_init(&sh->qfull, 1);
+    mbar_init(&sh->qempty, 1);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&sh->qfull[t], 1);
-      mbar_init(&sh->qempty[t], 1);
       mbar_init(&sh->sfull[t], 1);
       mbar_init(&sh->pfull[t], 4);   // a lane of each warp
       mbar_init(&sh->ofull[t], 1);
@@ -195,6 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
   }
@@ -312,7 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t head = seg.h * a.group + sub;
       const int64_t slot =
           (static_cast<int64_t>(blockIdx.x) * 2 + (seg.begins() ? 1 : 0)) * kItemRows + row;
-      const bool poison = tiles && *static_cast<volatile int*>(&sh->poison[slot8]) != 0;
+      const bool poison = tiles && (*static_cast<volatile int*>(&sh->poison[0][slot8]) |
+                                    *static_cast<volatile int*>(&sh->poison[1][slot8])) != 0;
 #pragma unroll 1
       for (int i = 0; i < DH / 32; ++i) {
         uint32_t o[32];
@@ -377,17 +375,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kIdS = idesc<kBf16>(128, 128, false), kIdO = idesc<kBf16>(128, DH, true);
         uint32_t stage = 0, phase = 0;           // next K or V tile
         uint32_t vphase = 0;                     // per stage: parity of its next vok
-        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        uint32_t q_phase = 0, p_phase[2] = {0, 0};
         bool ok = true;
         auto scores = [&](int t, uint32_t ks) {
-          const uint32_t q = smem_u32(sQ + t * G::kTileBytes);
+          const uint32_t q = smem_u32(sQ + t * (kTileRows * 128));
           const uint32_t k = smem_u32(sKV + ks * G::kTileBytes);
 #pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (128 * 128);
-            tc_mma_bf16(tmem + t * 128, sw128_kmajor_desc(q + off) + 2ull * (kk & 3),
-                        sw128_kmajor_desc(k + off) + 2ull * (kk & 3), kIdS, kk != 0);
-          }
+          for (int kk = 0; kk < DH / 16; ++kk)
+            tc_mma_bf16(tmem + t * 128,
+                        sw128_kmajor_desc(q + (kk >> 2) * (kItemRows * 128)) + 2ull * (kk & 3),
+                        sw128_kmajor_desc(k + (kk >> 2) * (kTileKeys * 128)) + 2ull * (kk & 3),
+                        kIdS, kk != 0);
           tc_commit(&sh->sfull[t]);
         };
         while (ok && cur.next(a.plan, seg)) {
@@ -395,16 +393,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int nt = seg.ntok * a.group > kTileRows ? 2 : 1;
           const int32_t n = seg.tile1 - seg.tile0;
           // scores of the first tile
-          ok = ok && attn_wait(&sh->full[stage], phase, abort, a.err);
-          for (int t = 0; t < nt && ok; ++t) {
-            ok = attn_wait(&sh->qfull[t], q_phase[t], abort, a.err);
-            if (!ok) break;
-            q_phase[t] ^= 1u;
-            tc_fence_after();
-            scores(t, stage);
-            if (n == 1) tc_commit(&sh->qempty[t]);
-          }
+          ok = attn_wait(&sh->full[stage], phase, abort, a.err) &&
+               attn_wait(&sh->qfull, q_phase, abort, a.err);
           if (!ok) break;
+          q_phase ^= 1u;
+          tc_fence_after();
+          for (int t = 0; t < nt; ++t) scores(t, stage);
+          if (n == 1) tc_commit(&sh->qempty);
           tc_commit(&sh->empty[stage]);
           if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
           for (int32_t j = 0; j < n && ok; ++j) {
@@ -440,12 +435,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tc_fence_after();
                 }
                 scores(t, ks);
-                if (j + 2 == n) tc_commit(&sh->qempty[t]);
               }
             }
             if (!ok) break;
             tc_commit(&sh->empty[vs]);
             if (more) {
+              if (j + 2 == n) tc_commit(&sh->qempty);
               tc_commit(&sh->empty[ks]);
               if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
             }
@@ -459,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------- TMA producer
       TmaRingT<G::kStages> ring;
       bool stop = false;
+      uint32_t q_phase = 0, q_loads = 0;
       while (!stop && cur.next(a.plan, seg)) {
         if (seg.keys == 0) continue;
         for (int32_t j = seg.tile0; j < seg.tile1 && !stop; ++j) {
@@ -478,94 +474,78 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane < grans) {
 #pragma unroll
               for (int hf = 0; hf < G::kHalves; ++hf)
-                tma_load_4d(dst + hf * (128 * 128) + lane * a.granule * 128, kv ? &tmV : &tmK,
-                            &sh->full[ring.stage], hf * 64, seg.h, at.z, at.w);
+                tma_load_4d(dst + hf * (kTileKeys * 128) + lane * a.granule * 128,
+                            kv ? &tmV : &tmK, &sh->full[ring.stage], hf * 64, seg.h, at.z, at.w);
             }
             ring.issued();
+            if (kv == 0 && j == seg.tile0) {   // the item's rows, behind its first keys
+              stop = __any_sync(0xFFFFFFFFu,
+                                !attn_wait(&sh->qempty, q_phase ^ 1u, abort, a.err));
+              if (stop) break;
+              q_phase ^= 1u;
+              ++q_loads;
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&sh->qfull, static_cast<uint32_t>(a.plan.tokens * a.group) *
+                                                      128 * G::kHalves);
+#pragma unroll
+                for (int hf = 0; hf < G::kHalves; ++hf)
+                  tma_load_4d(sQ + hf * (kItemRows * 128), &tmQ, &sh->qfull, hf * 64,
+                              seg.h * a.group, seg.token0, 0);
+              }
+              __syncwarp();
+            }
           }
         }
       }
       __syncwarp();
       ring.drain(sh->full);
-    } else if (warp == 10) {
-      // ----------------------------------------------------------- rows of Q
-      uint32_t q_phase[2] = {0, 0};
-      constexpr int kChunks = DH / 8, kStep = 32 / kChunks;   // rows per pass of the warp
-      const int ch = lane % kChunks;
-      while (cur.next(a.plan, seg)) {
-        if (seg.keys == 0) continue;
-        const int32_t rows = seg.ntok * a.group;
-        for (int t = 0; t * kTileRows < rows; ++t) {
-          attn_wait(&sh->qempty[t], q_phase[t] ^ 1u, abort, a.err);
-          q_phase[t] ^= 1u;
-          int32_t r = lane / kChunks;
-          int32_t tk = (t * kTileRows + r) / a.group;
-          int32_t sub = t * kTileRows + r - tk * a.group;
-          const uint32_t dst = smem_u32(sQ + t * G::kTileBytes) + (ch >> 3) * (128 * 128);
-#pragma unroll 4
-          for (; r < kTileRows; r += kStep) {
-            const bool real = t * kTileRows + r < rows && ch * 8 < a.head_dim;
-            const uint16_t* src = a.q;
-            if (real)
-              src += static_cast<int64_t>(seg.token0 + tk) * a.q_token +
-                     static_cast<int64_t>(seg.h * a.group + sub) * a.q_head + ch * 8;
-            cp_async_16(dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, real);
-            sub += kStep;
-            while (sub >= a.group) {
-              sub -= a.group;
-              ++tk;
-            }
-          }
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh->qfull[t]);
-        }
-      }
+      if (q_loads > 0) mbar_wait_drain(&sh->qfull, (q_loads - 1) & 1u);
     } else {
       // ----------------------------------------------------------- values nobody may see
       uint32_t stage = 0, phase = 0, count = 0;
       while (cur.next(a.plan, seg)) {
         if (seg.keys == 0) continue;
         const uint32_t slot8 = count++ % kPoisonSlots;
-        if (lane == 0) sh->poison[slot8] = 0;
+        const int half = warp - 10;   // of the rows: every other pair
+        if (lane == 0) sh->poison[half][slot8] = 0;
         __syncwarp();
         for (int32_t j = seg.tile0; j < seg.tile1; ++j) {
           for (int kv = 0; kv < 2; ++kv) {
             attn_wait(&sh->full[stage], phase, abort, a.err);
             __syncwarp();
             if (kv == 1 && (j + 1) * kTileKeys > seg.first_keys) {
-              const uint32_t v = smem_u32(sKV + stage * G::kTileBytes);
-              int32_t r0 = seg.first_keys - j * kTileKeys;
-              if (r0 < 0) r0 = 0;
-              const int32_t r1 = seg.keys - j * kTileKeys;   // rows from here on: nobody's
-              constexpr int kChunks = DH / 8;
-              bool found = false;
-#pragma unroll 4
-              for (int32_t i = r0 * kChunks + lane; i < kTileKeys * kChunks; i += 32) {
-                const int32_t r = i / kChunks, ch = i % kChunks;
-                const uint32_t at = v + (ch >> 3) * (128 * 128) + r * 128 +
-                                    (((ch & 7) ^ (r & 7)) << 4);
-                if (r >= r1) {
-                  sts128(at, make_uint4(0, 0, 0, 0));
-                  continue;
-                }
-                const uint4 w = lds128(at);
-                uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                bool bad = false;
+              // Each lane takes one 16-byte chunk column and every kStep-th row.
+              constexpr int kChunks = DH / 8, kStep = 2 * (32 / kChunks);
+              const int ch = lane % kChunks;
+              const uint32_t v = smem_u32(sKV + stage * G::kTileBytes) +
+                                 (ch >> 3) * (kTileKeys * 128);
+              auto at = [&](int32_t r) { return v + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
+              const int32_t f = seg.first_keys - j * kTileKeys, e = seg.keys - j * kTileKeys;
+              const int32_t r1 = e < kTileKeys ? e : kTileKeys;   // rows from here on: nobody's
+              int32_t r = (f > 0 ? f : 0) + half * (32 / kChunks) + lane / kChunks;
+              uint32_t any = 0;
+              const int32_t r_first = r;
+#pragma unroll 1
+              for (; r < r1; r += 8 * kStep) {
+                uint4 w[8];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) bad |= any_nonfinite<kBf16>(x[e]);
-                if (bad) {
-                  found = true;
+                for (int i = 0; i < 8; ++i)
+                  w[i] = r + i * kStep < r1 ? lds128(at(r + i * kStep)) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    if (any_nonfinite<kBf16>(x[e] & 0xFFFFu)) x[e] &= 0xFFFF0000u;
-                    if (any_nonfinite<kBf16>(x[e] & 0xFFFF0000u)) x[e] &= 0xFFFFu;
-                  }
-                  sts128(at, make_uint4(x[0], x[1], x[2], x[3]));
+                for (int i = 0; i < 8; ++i)
+                  any |= nonfinite_bits<kBf16>(w[i].x) | nonfinite_bits<kBf16>(w[i].y) |
+                         nonfinite_bits<kBf16>(w[i].z) | nonfinite_bits<kBf16>(w[i].w);
+              }
+              if (any != 0) {   // rare: replace what is not finite
+                *static_cast<volatile int*>(&sh->poison[half][slot8]) = 1;
+                for (r = r_first; r < r1; r += kStep) {
+                  const uint4 w = lds128(at(r));
+                  sts128(at(r), make_uint4(finite_only<kBf16>(w.x), finite_only<kBf16>(w.y),
+                                           finite_only<kBf16>(w.z), finite_only<kBf16>(w.w)));
                 }
               }
-              if (found) *static_cast<volatile int*>(&sh->poison[slot8]) = 1;
+              for (r = r1 + half * (32 / kChunks) + lane / kChunks; r < kTileKeys; r += kStep)
+                sts128(at(r), make_uint4(0, 0, 0, 0));
               fence_proxy_async_shared();
               __syncwarp();
               if (lane == 0) mbar_arrive(&sh->vok[stage]);
@@ -588,13 +568,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int DH, bool kBf16>
-cudaError_t launch(const AttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
-                   cudaStream_t st) {
+cudaError_t launch(const AttnArgs& a, const CUtensorMap& tmQ, const CUtensorMap& tmK,
+                   const CUtensorMap& tmV, cudaStream_t st) {
   const cudaError_t e = ensure_dynamic_smem(
       reinterpret_cast<const void*>(attn_tiles_kernel<DH, kBf16>), smem_bytes<DH>());
   if (e != cudaSuccess) return e;
   return launch_ex(attn_tiles_kernel<DH, kBf16>, dim3(a.plan.workers), dim3(kThreads),
-                   smem_bytes<DH>(), st, true, tmK, tmV, a,
+                   smem_bytes<DH>(), st, true, tmQ, tmK, tmV, a,
                    attn_pieces_at(a.workspace, a.plan.workers, kItemRows));
 }
 
@@ -606,13 +586,17 @@ cudaError_t launch_attn_tiles(const AttnArgs& in, cudaStream_t st) {
   a.plan.workers = device_sm_count();
   a.plan.min_units = 1;
   a.plan.whole = 0;
-  alignas(64) CUtensorMap tmK, tmV;
-  if (!attn_tensor_maps(a, &tmK, &tmV)) return cudaErrorInvalidValue;
+  alignas(64) CUtensorMap tmQ, tmK, tmV;
+  if (!attn_tensor_maps(a, &tmK, &tmV) ||
+      !tensor_map_attn(&tmQ, a.q, a.bf16, a.head_dim, a.heads, a.plan.total, 1, a.q_head, a.q_token,
+                       0, a.group, a.plan.tokens))
+    return cudaErrorInvalidValue;
   cudaError_t e;
   if (attn_width(a.head_dim) == 64)
-    e = a.bf16 ? launch<64, true>(a, tmK, tmV, st) : launch<64, false>(a, tmK, tmV, st);
+    e = a.bf16 ? launch<64, true>(a, tmQ, tmK, tmV, st) : launch<64, false>(a, tmQ, tmK, tmV, st);
   else
-    e = a.bf16 ? launch<128, true>(a, tmK, tmV, st) : launch<128, false>(a, tmK, tmV, st);
+    e = a.bf16 ? launch<128, true>(a, tmQ, tmK, tmV, st)
+               : launch<128, false>(a, tmQ, tmK, tmV, st);
   if (e != cudaSuccess) return e;
   return launch_attn_combine(a, kItemRows, st);
 }

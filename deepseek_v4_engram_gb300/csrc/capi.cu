@@ -305,16 +305,16 @@ bool tensor_map_2d_bf16(void* map_out, const void* base, uint64_t inner, uint64_
   return r == CUDA_SUCCESS;
 }
 
-bool tensor_map_kv(void* map_out, const void* base, bool bf16, uint64_t dim, uint64_t heads,
-                   uint64_t tokens, uint64_t pages, int64_t head_stride, int64_t token_stride,
-                   int64_t page_stride, uint32_t granule) {
+bool tensor_map_attn(void* map_out, const void* base, bool bf16, uint64_t dim, uint64_t heads,
+                     uint64_t tokens, uint64_t pages, int64_t head_stride, int64_t token_stride,
+                     int64_t page_stride, uint32_t box_heads, uint32_t box_tokens) {
   if (!have_encoder()) return false;
   // a dimension of one element has no step: any stride that the encoder accepts will do
   auto bytes = [&](uint64_t n, int64_t stride) { return (n > 1 ? uint64_t(stride) : dim) * 2; };
   const cuuint64_t dims[4] = {dim, heads, tokens, pages};
   const cuuint64_t strides[3] = {bytes(heads, head_stride), bytes(tokens, token_stride),
                                  bytes(pages, page_stride)};
-  const cuuint32_t box[4] = {64, 1, granule, 1};
+  const cuuint32_t box[4] = {64, box_heads, box_tokens, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = g_encode(static_cast<CUtensorMap*>(map_out),
                               bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
