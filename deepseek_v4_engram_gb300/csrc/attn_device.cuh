@@ -69,12 +69,27 @@ __device__ __forceinline__ KvPlace kv_place(const AttnArgs& a, const AttnSeq& s,
   return {pos - col * a.page_size, page};
 }
 
-// A wait that never blocks twice: once a role has given up, every later wait returns at once and
-// the roles run to their end without touching memory that was never filled in earnest.
+// Wait for the phase of `bar` with the given parity: mbar_wait of device.cuh with nothing but the
+// wait itself on the way of a phase that is about to complete (the clock and the abort flag are
+// only read after a number of tries). Gives up like it, after kWaitLimitNs or once another role
+// has: the roles then run to their end without waiting, and without touching memory that was
+// never filled in earnest.
 __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           uint32_t* err) {
-  if (*abort) return false;
-  return mbar_wait(bar, parity, abort, err);
+  const uint32_t at = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t i = 1; !mbar_try_wait(at, parity); ++i) {
+    if ((i & 31u) != 0) continue;
+    if (*abort) return false;
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
+      *abort = 1;
+      set_error(err, kErrWaitTimeout);
+      return false;
+    }
+  }
+  return true;
 }
 
 // Finds the calling CTA's range: every thread sums a run of sequences, a scan over the CTA finds

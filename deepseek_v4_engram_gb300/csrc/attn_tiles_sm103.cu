@@ -54,6 +54,8 @@ struct Shared {
   uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2];
   uint64_t drain;
   AttnStart start;
+  AttnCursor cur[kThreads / 32];   // each warp's own
+  AttnSegment seg[kThreads / 32];
   int poison[2][kPoisonSlots];   // of warps 10 and 11, by segment
   uint32_t tmem_base;
   int abort;
@@ -73,26 +75,40 @@ constexpr uint32_t idesc(int M, int N, bool b_mn) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// Shared-memory descriptor of a 128-byte-swizzled tile read MN-major: rows are K (keys), 64
-// columns of 128 B per box; boxes of 128 rows 16 KB apart (leading), 8-row groups 1 KB apart.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((128u * 128u) >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
-  return d;
+// The MMA warp runs converged, with one lane predicated on: descriptors that are the same in every
+// lane then come from uniform registers. (Issued from a branch that lane 0 takes alone, each MMA
+// first moved its descriptors there, and the issue, not the tensor cores, set the pace.)
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+// Low and high words of a shared-memory descriptor: the low one holds the address (in 16-byte
+// units, 14 bits) and the leading offset, the high one stride, version and swizzle.
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+  constexpr uint32_t hi = (1024u >> 4) | (1u << 14) | (2u << 29);
+  return (static_cast<uint64_t>(hi) << 32) | lo;
+}
+// K-major tile with the 128-byte swizzle (rows of 64 elements, 8-row groups 1 KB apart).
+__device__ __forceinline__ uint32_t kmajor_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((16u >> 4) << 16);
+}
+// The same tile read MN-major: its rows are K (keys); boxes of 128 rows by 64 columns 16 KB apart.
+__device__ __forceinline__ uint32_t mnmajor_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | (((128u * 128u) >> 4) << 16);
+}
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], A 16-bit pairs in 32-bit columns.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                          uint32_t id, uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bd, uint32_t id,
+                                       uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(id), "r"(accumulate)
+      "r"(a_tmem), "l"(bd), "r"(id), "r"(accumulate)
       : "memory");
 }
 
@@ -206,8 +222,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort = &sh->abort;
-  AttnCursor cur = sh->start.cursor;
-  AttnSegment seg;
+  // Every warp walks the segments for itself; one lane does, and the others read what it left.
+  AttnCursor& cur = sh->cur[warp];
+  const AttnSegment& seg = sh->seg[warp];
+  auto next_segment = [&]() {
+    __syncwarp();
+    bool more = false;
+    if (lane == 0) more = cur.next(a.plan, sh->seg[warp]);
+    return __shfl_sync(0xFFFFFFFFu, more, 0);
+  };
+  if (lane == 0) cur = sh->start.cursor;
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax and output
@@ -220,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t tok = row / a.group, sub = row - tok * a.group;
     uint32_t s_phase = 0, o_phase = 0, count = 0;
     AttnMeta meta{0, 0, 0, 0};
-    while (cur.next(a.plan, seg)) {
+    while (next_segment()) {
       if (threadIdx.x == 0 && seg.begins() && !seg.ends())
         meta = AttnMeta{seg.b, seg.h, seg.rt, attn_pieces(seg, sh->start.per)};
       const bool tiles = seg.keys > 0;
@@ -371,91 +395,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     set_max_regs_down<kOtherRegs>();
     if (warp == 8) {
       // ----------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t kIdS = idesc<kBf16>(128, 128, false), kIdO = idesc<kBf16>(128, DH, true);
-        uint32_t stage = 0, phase = 0;           // next K or V tile
-        uint32_t vphase = 0;                     // per stage: parity of its next vok
-        uint32_t q_phase = 0, p_phase[2] = {0, 0};
-        bool ok = true;
-        auto scores = [&](int t, uint32_t ks) {
-          const uint32_t q = smem_u32(sQ + t * (kTileRows * 128));
-          const uint32_t k = smem_u32(sKV + ks * G::kTileBytes);
+      constexpr uint32_t kIdS = idesc<kBf16>(128, 128, false), kIdO = idesc<kBf16>(128, DH, true);
+      uint32_t stage = 0, phase = 0;           // next K or V tile
+      uint32_t vphase = 0;                     // per stage: parity of its next vok
+      uint32_t q_phase = 0, p_phase[2] = {0, 0};
+      const uint32_t td = uniform(tmem);
+      const uint32_t q_lo = uniform(kmajor_lo(smem_u32(sQ))), kv = uniform(smem_u32(sKV));
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && __all_sync(0xFFFFFFFFu, attn_wait(bar, parity, abort, a.err));
+        tc_fence_after();
+        return ok;
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) tc_commit(bar);
+        __syncwarp();
+      };
+      auto scores = [&](int t, uint32_t ks) {
+        const uint32_t k_lo = kmajor_lo(kv + ks * G::kTileBytes);
+        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk)
-            tc_mma_bf16(tmem + t * 128,
-                        sw128_kmajor_desc(q + (kk >> 2) * (kItemRows * 128)) + 2ull * (kk & 3),
-                        sw128_kmajor_desc(k + (kk >> 2) * (kTileKeys * 128)) + 2ull * (kk & 3),
-                        kIdS, kk != 0);
-          tc_commit(&sh->sfull[t]);
-        };
-        while (ok && cur.next(a.plan, seg)) {
-          if (seg.keys == 0) continue;
-          const int nt = seg.ntok * a.group > kTileRows ? 2 : 1;
-          const int32_t n = seg.tile1 - seg.tile0;
-          // scores of the first tile
-          ok = attn_wait(&sh->full[stage], phase, abort, a.err) &&
-               attn_wait(&sh->qfull, q_phase, abort, a.err);
-          if (!ok) break;
-          q_phase ^= 1u;
-          tc_fence_after();
-          for (int t = 0; t < nt; ++t) scores(t, stage);
-          if (n == 1) tc_commit(&sh->qempty);
-          tc_commit(&sh->empty[stage]);
+        for (int kk = 0; kk < DH / 16; ++kk)
+          tc_mma_bf16(td + t * 128,
+                 desc_of(q_lo + ((t * kTileRows + (kk >> 2) * kItemRows) * 128 >> 4) + 2 * (kk & 3)),
+                 desc_of(k_lo + ((kk >> 2) * kTileKeys * 128 >> 4) + 2 * (kk & 3)), kIdS, kk != 0);
+        tc_commit(&sh->sfull[t]);
+        }
+        __syncwarp();
+      };
+      while (ok && next_segment()) {
+        if (seg.keys == 0) continue;
+        const bool two = uniform(seg.ntok * a.group > kTileRows) != 0;
+        const int32_t n = uniform(seg.tile1 - seg.tile0);
+        const int32_t j_guard = uniform(seg.first_keys / kTileKeys - seg.tile0);   // from here on: vok
+        // scores of the first tile
+        if (!wait(&sh->full[stage], phase) || !wait(&sh->qfull, q_phase)) break;
+        q_phase ^= 1u;
+        scores(0, stage);
+        if (two) scores(1, stage);
+        if (n == 1) commit(&sh->qempty);
+        commit(&sh->empty[stage]);
+        if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+        for (int32_t j = 0; j < n; ++j) {
+          const uint32_t vs = stage, vph = phase;
           if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
-          for (int32_t j = 0; j < n && ok; ++j) {
-            const uint32_t vs = stage, vph = phase;
-            if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
-            const uint32_t ks = stage, kph = phase;
-            const bool more = j + 1 < n;
-            const bool guarded = (seg.tile0 + j + 1) * kTileKeys > seg.first_keys;
-            for (int t = 0; t < nt && ok; ++t) {
-              ok = attn_wait(&sh->pfull[t], p_phase[t], abort, a.err);
-              p_phase[t] ^= 1u;
-              if (t == 0 && ok) {
-                if (guarded) {
-                  ok = attn_wait(&sh->vok[vs], (vphase >> vs) & 1u, abort, a.err);
-                  vphase ^= 1u << vs;
-                } else {
-                  ok = attn_wait(&sh->full[vs], vph, abort, a.err);
-                }
+          const uint32_t ks = stage, kph = phase;
+          const bool more = j + 1 < n;
+          const uint32_t v_lo = mnmajor_lo(kv + vs * G::kTileBytes);
+          auto tile = [&](int t) {
+            if (!wait(&sh->pfull[t], p_phase[t])) return;
+            p_phase[t] ^= 1u;
+            if (t == 0) {
+              if (j >= j_guard) {
+                if (!wait(&sh->vok[vs], (vphase >> vs) & 1u)) return;
+                vphase ^= 1u << vs;
+              } else if (!wait(&sh->full[vs], vph)) {
+                return;
               }
-              if (!ok) break;
-              tc_fence_after();
-              const uint32_t v = smem_u32(sKV + vs * G::kTileBytes);
+            }
+            if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < kTileKeys / 16; ++kk)
-                tc_mma_ts(tmem + G::kO + t * DH, tmem + t * 128 + kk * 8,
-                          sw128_mnmajor_desc(v + kk * 16 * 128), kIdO, (j | kk) != 0);
-              if (!more) {
-                tc_commit(&sh->ofull[t]);
-              } else {
-                if (t == 0) {
-                  ok = attn_wait(&sh->full[ks], kph, abort, a.err);
-                  if (!ok) break;
-                  tc_fence_after();
-                }
-                scores(t, ks);
-              }
+            for (int kk = 0; kk < kTileKeys / 16; ++kk)
+              mma_ts(td + G::kO + t * DH, td + t * 128 + kk * 8,
+                     desc_of(v_lo + (kk * 16 * 128 >> 4)), kIdO, (j | kk) != 0);
             }
-            if (!ok) break;
-            tc_commit(&sh->empty[vs]);
-            if (more) {
-              if (j + 2 == n) tc_commit(&sh->qempty);
-              tc_commit(&sh->empty[ks]);
-              if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+            __syncwarp();
+            if (!more) {
+              commit(&sh->ofull[t]);
+            } else {
+              if (t == 0 && !wait(&sh->full[ks], kph)) return;
+              scores(t, ks);
             }
+          };
+          tile(0);
+          if (two && ok) tile(1);
+          if (!ok) break;
+          commit(&sh->empty[vs]);
+          if (more) {
+            if (j + 2 == n) commit(&sh->qempty);
+            commit(&sh->empty[ks]);
+            if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
           }
         }
-        // Every MMA this thread issued has finished before TMEM is released.
-        tc_commit(&sh->drain);
-        mbar_wait_drain(&sh->drain, 0);
       }
+      // Every MMA this warp issued has finished before TMEM is released.
+      commit(&sh->drain);
+      mbar_wait_drain(&sh->drain, 0);
     } else if (warp == 9) {
       // ----------------------------------------------------------- TMA producer
       TmaRingT<G::kStages> ring;
       bool stop = false;
       uint32_t q_phase = 0, q_loads = 0;
-      while (!stop && cur.next(a.plan, seg)) {
+      while (!stop && next_segment()) {
         if (seg.keys == 0) continue;
         for (int32_t j = seg.tile0; j < seg.tile1 && !stop; ++j) {
           const int32_t k0 = j * kTileKeys;
@@ -503,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
       // ----------------------------------------------------------- values nobody may see
       uint32_t stage = 0, phase = 0, count = 0;
-      while (cur.next(a.plan, seg)) {
+      while (next_segment()) {
         if (seg.keys == 0) continue;
         const uint32_t slot8 = count++ % kPoisonSlots;
         const int half = warp - 10;   // of the rows: every other pair
