@@ -3,18 +3,18 @@
 // An item is `tokens` consecutive query tokens of one sequence with all the query heads of one
 // key-value head: rows token * G + g, so a key tile that is loaded once serves every head that
 // shares it. Its cost is the number of kTileKeys-key tiles that its last token sees, at least 1
-// (an item that sees nothing still has to write zeros). Within a sequence, items go key-value
+// (an item that sees nothing still has to write zeros), and `extra`, the time that an item takes
+// beside its tiles (fetching the queries, filling the pipeline, writing the result) in the same
+// unit; an item's units are the extra ones first and then its tiles. Within a sequence, items go key-value
 // head by key-value head and then by token tile, so that workers that run side by side read the
 // same keys.
 //
-// All the items' tiles laid end to end are units 0 .. W-1, and worker w (a CTA) takes the units
+// All the items' units laid end to end are units 0 .. W-1, and worker w (a CTA) takes the units
 // [w * per, (w + 1) * per) with per = ceil(W / workers), at least `min_units`. Prompts of any
 // lengths, causal triangles and long caches with few rows are so balanced by one rule that needs
 // no lengths on the host: every worker evaluates it for itself from the lengths in device memory.
 // An item that a boundary cuts is computed in pieces, each with its own running maximum and sum;
 // the pieces are joined afterwards (attn_combine.cu), always in the same order.
-//
-// With `whole`, an item is not cut: it belongs to the worker whose range holds its first unit.
 //
 // A worker holds at most two pieces: one of an item that an earlier worker began (its first
 // segment), and one of an item that it begins and a later worker finishes (its last segment).
@@ -36,7 +36,7 @@ struct AttnPlan {
   int32_t tokens;          // query tokens per item
   int32_t workers;
   int32_t min_units;       // smallest share of a worker
-  int32_t whole;           // items are not cut
+  int32_t extra;           // units of an item beside its tiles
 };
 
 // One sequence: tokens [q0, q0 + n), of which token t sees the keys [0, max(0, m - n + t + 1)).
@@ -97,7 +97,7 @@ __host__ __device__ inline uint64_t attn_floor_sum(uint32_t n, uint32_t m, uint3
 __host__ __device__ inline int64_t attn_units_before(const AttnPlan& p, const AttnSeq& s,
                                                      int32_t k) {
   if (k <= 0) return 0;
-  int64_t u = 0;
+  int64_t u = static_cast<int64_t>(k) * p.extra;
   if (k == attn_items(p, s)) u += attn_cost(p, s, --k);   // the last one may hold fewer tokens
   const int32_t a = s.m - s.n;
   int32_t z = a < 0 ? -a / p.tokens : 0;   // tiles that see nothing: one unit each
@@ -130,11 +130,11 @@ struct AttnSegment {
   __host__ __device__ bool ends() const { return tile1 == cost; }
 };
 
-// Walks a worker's segments in order. (b, h, rt, tile) is where its range begins and `left` the
+// Walks a worker's segments in order. (b, h, rt, unit) is where its range begins and `left` the
 // units in it.
 struct AttnCursor {
   AttnSeq seq;
-  int32_t b, h, rt, tile;
+  int32_t b, h, rt, unit;
   int64_t left;
 
   __host__ __device__ bool next(const AttnPlan& p, AttnSegment& out) {
@@ -144,23 +144,24 @@ struct AttnCursor {
     out.h = h;
     out.rt = rt;
     out.cost = attn_cost(p, seq, rt);
-    out.tile0 = tile;
-    out.tile1 = p.whole || left >= out.cost - tile ? out.cost
-                                                   : tile + static_cast<int32_t>(left);
+    const int32_t units = out.cost + p.extra;
+    const int32_t end = left >= units - unit ? units : unit + static_cast<int32_t>(left);
+    out.tile0 = unit > p.extra ? unit - p.extra : 0;
+    out.tile1 = end > p.extra ? end - p.extra : 0;
     out.keys = attn_keys(p, seq, rt);
     const int32_t t0 = rt * p.tokens;
     out.token0 = seq.q0 + t0;
     out.ntok = seq.n - t0 < p.tokens ? seq.n - t0 : p.tokens;
     const int32_t f = seq.m - seq.n + t0 + 1;
     out.first_keys = f > 0 ? f : 0;
-    left -= out.tile1 - tile;
-    if (out.tile1 == out.cost) step(p);
-    return true;
+    left -= end - unit;
+    if (end == units) step(p);
+    return out.tile1 > out.tile0;   // a range may end before the item's first tile
   }
 
   // To the next item.
   __host__ __device__ void step(const AttnPlan& p) {
-    tile = 0;
+    unit = 0;
     if (++rt < attn_items(p, seq)) return;
     rt = 0;
     if (++h < p.kv_heads) return;
@@ -186,11 +187,7 @@ struct AttnCursor {
       else hi = mid;
     }
     rt = lo;
-    tile = static_cast<int32_t>(in - attn_units_before(p, seq, lo));
-    if (p.whole && tile > 0) {   // the item belongs to the worker before
-      left -= attn_cost(p, seq, rt) - tile;
-      step(p);
-    }
+    unit = static_cast<int32_t>(in - attn_units_before(p, seq, lo));
   }
 };
 

@@ -24,6 +24,7 @@ namespace engram {
 namespace {
 
 constexpr int kConsumers = 8;
+constexpr int kExtraUnits = 1;
 constexpr int kThreads = (kConsumers + 1) * 32;
 
 template <int DH>
@@ -408,7 +409,7 @@ cudaError_t launch_attn_rows(const AttnArgs& in, cudaStream_t st) {
   a.plan.tokens = kAttnRows / a.group;
   a.plan.workers = device_sm_count();
   a.plan.min_units = 1;
-  a.plan.whole = 0;
+  a.plan.extra = kExtraUnits;
   alignas(64) CUtensorMap tmK, tmV;
   if (!attn_tensor_maps(a, &tmK, &tmV)) return cudaErrorInvalidValue;
   cudaError_t e;

@@ -17,7 +17,7 @@
 //
 // Roles (384 threads): warps 0-3 and 4-7 softmax and output of row tile 0 and 1 (thread = row =
 // TMEM lane); warp 8 issues the MMAs; warp 9 requests key and value tiles by TMA (one page granule
-// per lane) and each item's queries (a box of its tokens by the heads that share its key-value
+// per lane), warp 10 each item's queries (a box of its tokens by the heads that share its key-value
 // head is the item's rows in order, whatever their number); warps 10-11 make the values that some
 // row of the item must not see harmless (below). Registers: the softmax warps hold a row of 128
 // scores, so they take 208 each and the other four 88.
@@ -34,11 +34,13 @@ namespace engram {
 
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kSoftmaxWarps = 8;
+constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
 constexpr int kTileRows = 128;
 constexpr int kItemRows = kAttnItemRows;   // two row tiles
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 256 * 208 + 128 * 88 = 384 * 168
 constexpr int kPoisonSlots = 8;
+constexpr int kExtraUnits = 2;
 
 template <int DH>
 struct Geo {
@@ -147,6 +149,12 @@ __device__ __forceinline__ void set_max_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Pairs of f32 in one 64-bit register: two multiply-adds or adds per instruction.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;
@@ -165,6 +173,24 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
+}
+
+// Four lanes transpose their four 16-byte pieces: lane q's piece v becomes lane v's piece q.
+__device__ __forceinline__ void exchange4(uint32_t (&w)[4][4], int own) {
+#pragma unroll
+  for (int mask = 1; mask < 4; mask <<= 1)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      if (v & mask) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const bool up = own & mask;
+        const uint32_t got =
+            __shfl_xor_sync(0xFFFFFFFFu, up ? w[v][e] : w[v | mask][e], mask);
+        w[v][e] = up ? got : w[v][e];
+        w[v | mask][e] = up ? w[v | mask][e] : got;
+      }
+    }
 }
 
 // Value row of position `pos` (for the rare rows that see an infinity or NaN).
@@ -275,9 +301,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
+          for (int e = 0; e < 32; e += 2)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mt[i] = fmaxf(mt[i], __uint_as_float(s[i][e]));
+            for (int i = 0; i < 4; ++i)
+              mt[i] = max3(mt[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
           const float top = fmaxf(m, fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])));
           if (j == seg.tile0) {
             m = top;
@@ -335,6 +362,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           (static_cast<int64_t>(blockIdx.x) * 2 + (seg.begins() ? 1 : 0)) * kItemRows + row;
       const bool poison = tiles && (*static_cast<volatile int*>(&sh->poison[0][slot8]) |
                                     *static_cast<volatile int*>(&sh->poison[1][slot8])) != 0;
+      // Rows leave in pieces of 16 bytes that four lanes exchange, so that each store writes 64
+      // bytes of a row: the lane's own row, and those of its three neighbours.
+      const int64_t place = !valid ? -1
+                            : whole ? static_cast<int64_t>(seg.token0 + tok) * a.o_token +
+                                          static_cast<int64_t>(head) * a.o_head
+                                    : slot * DH;
+      int64_t to[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        to[e] = __shfl_sync(0xFFFFFFFFu, place, (lane & ~3) + e);
+      const int own = lane & 3;
 #pragma unroll 1
       for (int i = 0; i < DH / 32; ++i) {
         uint32_t o[32];
@@ -358,26 +396,37 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (!(fabsf(x) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
             }
           }
+          __syncwarp();
         }
-        if (!valid) continue;
         if (whole) {
-          uint16_t* op = a.out + static_cast<int64_t>(seg.token0 + tok) * a.o_token +
-                         static_cast<int64_t>(head) * a.o_head + i * 32;
+          uint32_t w[4][4];
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            uint32_t w[4];
+          for (int v = 0; v < 4; ++v)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              w[e] = pack16x2<kBf16>(__uint_as_float(o[8 * v + 2 * e]) * inv,
-                                     __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
-            if (i * 32 + v * 8 < a.head_dim)
-              *reinterpret_cast<uint4*>(op + v * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else {
-          uint4* op = reinterpret_cast<uint4*>(pieces.o + slot * DH + i * 32);
+              w[v][e] = pack16x2<kBf16>(__uint_as_float(o[8 * v + 2 * e]) * inv,
+                                        __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
+          exchange4(w, own);
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            op[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          for (int v = 0; v < 4; ++v)
+            if (to[v] >= 0 && i * 32 + own * 8 < a.head_dim)
+              *reinterpret_cast<uint4*>(a.out + to[v] + i * 32 + own * 8) =
+                  make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
+        } else {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            uint32_t w[4][4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[v][e] = o[hf * 16 + 4 * v + e];
+            exchange4(w, own);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (to[v] >= 0)
+                *reinterpret_cast<uint4*>(pieces.o + to[v] + i * 32 + hf * 16 + own * 4) =
+                    make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
+          }
         }
       }
       tc_fence_before();   // the next product into O follows this thread's next P
@@ -442,17 +491,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t ks = stage, kph = phase;
           const bool more = j + 1 < n;
           const uint32_t v_lo = mnmajor_lo(kv + vs * G::kTileBytes);
+          // what was requested long ago first, so that nothing else stands between P and its MMAs
+          if (j >= j_guard) {
+            if (!wait(&sh->vok[vs], (vphase >> vs) & 1u)) break;
+            vphase ^= 1u << vs;
+          } else if (!wait(&sh->full[vs], vph)) {
+            break;
+          }
           auto tile = [&](int t) {
             if (!wait(&sh->pfull[t], p_phase[t])) return;
             p_phase[t] ^= 1u;
-            if (t == 0) {
-              if (j >= j_guard) {
-                if (!wait(&sh->vok[vs], (vphase >> vs) & 1u)) return;
-                vphase ^= 1u << vs;
-              } else if (!wait(&sh->full[vs], vph)) {
-                return;
-              }
-            }
             if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kTileKeys / 16; ++kk)
@@ -485,7 +533,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------- TMA producer
       TmaRingT<G::kStages> ring;
       bool stop = false;
-      uint32_t q_phase = 0, q_loads = 0;
       while (!stop && next_segment()) {
         if (seg.keys == 0) continue;
         for (int32_t j = seg.tile0; j < seg.tile1 && !stop; ++j) {
@@ -509,36 +556,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                             kv ? &tmV : &tmK, &sh->full[ring.stage], hf * 64, seg.h, at.z, at.w);
             }
             ring.issued();
-            if (kv == 0 && j == seg.tile0) {   // the item's rows, behind its first keys
-              stop = __any_sync(0xFFFFFFFFu,
-                                !attn_wait(&sh->qempty, q_phase ^ 1u, abort, a.err));
-              if (stop) break;
-              q_phase ^= 1u;
-              ++q_loads;
-              if (lane == 0) {
-                mbar_arrive_expect_tx(&sh->qfull, static_cast<uint32_t>(a.plan.tokens * a.group) *
-                                                      128 * G::kHalves);
-#pragma unroll
-                for (int hf = 0; hf < G::kHalves; ++hf)
-                  tma_load_4d(sQ + hf * (kItemRows * 128), &tmQ, &sh->qfull, hf * 64,
-                              seg.h * a.group, seg.token0, 0);
-              }
-              __syncwarp();
-            }
           }
         }
       }
       __syncwarp();
       ring.drain(sh->full);
-      if (q_loads > 0) mbar_wait_drain(&sh->qfull, (q_loads - 1) & 1u);
     } else {
       // ----------------------------------------------------------- values nobody may see
-      uint32_t stage = 0, phase = 0, count = 0;
+      const int part = warp - kSoftmaxWarps - 2;   // of the rows
+      uint32_t stage = 0, phase = 0, count = 0, q_phase = 0, q_loads = 0;
       while (next_segment()) {
         if (seg.keys == 0) continue;
         const uint32_t slot8 = count++ % kPoisonSlots;
-        const int half = warp - 10;   // of the rows: every other pair
-        if (lane == 0) sh->poison[half][slot8] = 0;
+        if (part == 0) {   // the item's rows, once the MMAs have read the last ones
+          const bool ok = !__any_sync(0xFFFFFFFFu, !attn_wait(&sh->qempty, q_phase ^ 1u, abort, a.err));
+          q_phase ^= 1u;
+          if (ok && lane == 0) {
+            ++q_loads;
+            mbar_arrive_expect_tx(&sh->qfull, static_cast<uint32_t>(a.plan.tokens * a.group) * 128 *
+                                                  G::kHalves);
+#pragma unroll
+            for (int hf = 0; hf < G::kHalves; ++hf)
+              tma_load_4d(sQ + hf * (kItemRows * 128), &tmQ, &sh->qfull, hf * 64,
+                          seg.h * a.group, seg.token0, 0);
+          }
+          __syncwarp();
+        }
+        if (lane == 0) sh->poison[part][slot8] = 0;
         __syncwarp();
         for (int32_t j = seg.tile0; j < seg.tile1; ++j) {
           for (int kv = 0; kv < 2; ++kv) {
@@ -553,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               auto at = [&](int32_t r) { return v + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
               const int32_t f = seg.first_keys - j * kTileKeys, e = seg.keys - j * kTileKeys;
               const int32_t r1 = e < kTileKeys ? e : kTileKeys;   // rows from here on: nobody's
-              int32_t r = (f > 0 ? f : 0) + half * (32 / kChunks) + lane / kChunks;
+              int32_t r = (f > 0 ? f : 0) + part * (32 / kChunks) + lane / kChunks;
               uint32_t any = 0;
               const int32_t r_first = r;
 #pragma unroll 1
@@ -568,14 +612,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                          nonfinite_bits<kBf16>(w[i].z) | nonfinite_bits<kBf16>(w[i].w);
               }
               if (any != 0) {   // rare: replace what is not finite
-                *static_cast<volatile int*>(&sh->poison[half][slot8]) = 1;
+                *static_cast<volatile int*>(&sh->poison[part][slot8]) = 1;
                 for (r = r_first; r < r1; r += kStep) {
                   const uint4 w = lds128(at(r));
                   sts128(at(r), make_uint4(finite_only<kBf16>(w.x), finite_only<kBf16>(w.y),
                                            finite_only<kBf16>(w.z), finite_only<kBf16>(w.w)));
                 }
               }
-              for (r = r1 + half * (32 / kChunks) + lane / kChunks; r < kTileKeys; r += kStep)
+              for (r = r1 + part * (32 / kChunks) + lane / kChunks; r < kTileKeys; r += kStep)
                 sts128(at(r), make_uint4(0, 0, 0, 0));
               fence_proxy_async_shared();
               __syncwarp();
@@ -586,6 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
+      if (q_loads > 0) mbar_wait_drain(&sh->qfull, (q_loads - 1) & 1u);
     }
   }
 
@@ -616,7 +661,7 @@ cudaError_t launch_attn_tiles(const AttnArgs& in, cudaStream_t st) {
   a.plan.tokens = kItemRows / a.group;
   a.plan.workers = device_sm_count();
   a.plan.min_units = 1;
-  a.plan.whole = 0;
+  a.plan.extra = kExtraUnits;
   alignas(64) CUtensorMap tmQ, tmK, tmV;
   if (!attn_tensor_maps(a, &tmK, &tmV) ||
       !tensor_map_attn(&tmQ, a.q, a.bf16, a.head_dim, a.heads, a.plan.total, 1, a.q_head, a.q_token,

@@ -37,7 +37,7 @@ static long check(AttnPlan p) {
       long x = s.m - s.n + std::min<long>((long)(rt + 1) * p.tokens, s.n);
       long t = x <= 0 ? 1 : (x + kTileKeys - 1) / kTileKeys;
       if (attn_cost(p, s, rt) != t) ++bad;
-      u += t;
+      u += t + p.extra;
     }
     if (attn_seq_units(p, s) != u * p.kv_heads) ++bad;
     total += u * p.kv_heads;
@@ -56,7 +56,7 @@ static long check(AttnPlan p) {
     AttnSegment s;
     bool was_last = false;
     int n = 0;
-    int64_t units = 0;
+    int64_t units = 0, left = total - u0 < per ? total - u0 : per;
     while (c.next(p, s)) {
       if (was_last) ++bad;                       // a piece that does not end is a worker's last
       auto key = std::make_tuple(s.b, s.h, s.rt);
@@ -68,15 +68,15 @@ static long check(AttnPlan p) {
         was_last = true;
         if (s.begins()) opened[key] = attn_pieces(s, per) - 1;
       } else if (!s.begins() && opened[key] != 0) ++bad;
-      if (p.whole && !(s.begins() && s.ends())) ++bad;
       AttnSeq q = attn_seq(p, s.b);
       if (s.token0 != q.q0 + s.rt * p.tokens || s.ntok < 1 || s.ntok > p.tokens ||
           s.token0 + s.ntok > q.q0 + q.n) ++bad;
       if (s.keys > std::max(0, q.m) || s.first_keys > s.keys) ++bad;
-      units += s.tile1 - s.tile0;
+      units += s.tile1 - s.tile0 + (s.begins() ? p.extra : 0);
       ++n;
     }
-    if (!p.whole && units != std::min<int64_t>(per, total - u0)) ++bad;
+    // at most the extra units of the items at its two ends are not this worker's own
+    if (units < left - p.extra || units > left + p.extra) ++bad;
   }
   for (int b = 0; b < p.n_seqs; ++b) {
     AttnSeq s = attn_seq(p, b);
@@ -111,17 +111,17 @@ int main() {
     p.tokens = toks[rand() % 10];
     p.workers = 1 + rand() % 152;
     p.min_units = 1 + rand() % 4;
-    p.whole = rand() % 4 == 0;
+    p.extra = rand() % 4;
     bad += check(p);
     ++cases;
   }
   // a very long cache: the sums pass 32 bits
   int cu[2] = {0, 1 << 20}, kv[1] = {1 << 29};
-  AttnPlan p{cu, kv, 1, 1 << 20, 1 << 29, 128, 2, 152, 1, 0};
+  AttnPlan p{cu, kv, 1, 1 << 20, 1 << 29, 128, 2, 152, 1, 3};
   const int64_t u = attn_seq_units(p, attn_seq(p, 0));
   long double want = 0;
   for (long r = 0; r < (1 << 19); ++r)
-    want += ((1L << 29) - (1L << 20) + (r + 1) * 2 + 127) / 128 * 128.0L;
+    want += ((1L << 29) - (1L << 20) + (r + 1) * 2 + 127) / 128 * 128.0L + 3 * 128.0L;
   if ((long double)u != want) ++bad;
   printf("cases=%ld bad=%ld\n", cases, bad);
   return bad != 0;
