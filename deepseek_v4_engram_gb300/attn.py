@@ -14,10 +14,11 @@ import torch
 
 from . import _lib
 from ._lib import EngramAttnDesc, EngramAttnView, EngramKvCache
-from .api import _check, _stream, lib
+from .api import _check, lib
 
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
 _TORCH = {_lib.BF16: torch.bfloat16, _lib.F16: torch.float16}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def make_attn_desc(n_heads: int, n_kv_heads: int, head_dim: int, dtype=torch.bfloat16,
@@ -30,81 +31,88 @@ def make_attn_desc(n_heads: int, n_kv_heads: int, head_dim: int, dtype=torch.bfl
     return EngramAttnDesc(n_heads, n_kv_heads, head_dim, _DTYPES[dtype], scale)
 
 
-def _tensor(t, name: str, ndim: int, dtype):
+# A decoding step's calls are shorter on the GPU than a chain of careful helpers on the host, so
+# each check below is one expression of cheap tensor attributes; what is wrong with an argument
+# that fails it is worked out only then.
+
+def _refuse(t, name: str, shape: str, dtype):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor (the library takes device pointers)")
-    if t.dtype != dtype or t.dim() != ndim:
-        raise ValueError(f"{name}: expected a {ndim}-dimensional {dtype} tensor, got "
-                         f"{t.dim()}-dimensional {t.dtype}")
+    raise ValueError(f"{name}: expected a {dtype} tensor {shape}, got {t.dtype} {list(t.shape)} "
+                     f"with strides {t.stride()}")
 
 
-def _view(t, name: str, heads: int, desc: EngramAttnDesc, tokens: int | None = None):
-    _tensor(t, name, 3, _TORCH[desc.dtype])
-    n, h, d = t.shape
-    if h != heads or d != desc.head_dim or (tokens is not None and n != tokens):
-        want = "tokens" if tokens is None else tokens
-        raise ValueError(f"{name}: expected shape [{want}, {heads}, {desc.head_dim}], got "
-                         f"{[n, h, d]}")
-    s = t.stride()
-    if s[2] != 1:
-        raise ValueError(f"{name}: the last dimension must be dense")
-    return EngramAttnView(t.data_ptr(), s[0], s[1])
+def _view(t, name: str, heads: int, dim: int, dtype, tokens: int = -1):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype:
+        shape = t.shape
+        if len(shape) == 3 and shape[1] == heads and shape[2] == dim and (
+                tokens < 0 or shape[0] == tokens):
+            s = t.stride()
+            if s[2] == 1:
+                return EngramAttnView(t.data_ptr(), s[0], s[1])
+    n = "tokens" if tokens < 0 else tokens
+    _refuse(t, name, f"[{n}, {heads}, {dim}] whose last dimension is dense", dtype)
 
 
-def _ints(t, name: str, count: int | None = None):
-    _tensor(t, name, 1, torch.int32)
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
-    if count is not None and t.shape[0] != count:
-        raise ValueError(f"{name}: expected {count} elements, got {t.shape[0]}")
-    return t.data_ptr()
+def _ints(t, name: str, count: int = -1):
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.int32:
+        shape = t.shape
+        if len(shape) == 1 and (count < 0 or shape[0] == count) and t.is_contiguous():
+            return t.data_ptr()
+    _refuse(t, name, f"[{'n' if count < 0 else count}], contiguous", torch.int32)
 
 
 def _sequences(cu_seqlens) -> int:
-    n = cu_seqlens.shape[0] - 1 if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dim() else 0
+    n = cu_seqlens.shape[0] - 1
     if n < 0:
         raise ValueError("cu_seqlens: expected one element more than there are sequences")
     return n
 
 
-def _cache(desc: EngramAttnDesc, k_cache, v_cache, block_table, n_seqs: int):
-    dtype = _TORCH[desc.dtype]
-    _tensor(k_cache, "k_cache", 4, dtype)
-    _tensor(v_cache, "v_cache", 4, dtype)
-    _tensor(block_table, "block_table", 2, torch.int32)
-    pages, page_size, heads, d = k_cache.shape
-    if heads != desc.n_kv_heads or d != desc.head_dim or v_cache.shape != k_cache.shape:
-        raise ValueError(f"k_cache and v_cache: expected [pages, page_size, {desc.n_kv_heads}, "
-                         f"{desc.head_dim}], got {list(k_cache.shape)} and {list(v_cache.shape)}")
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if ks[3] != 1 or vs[3] != 1:
-        raise ValueError("k_cache and v_cache: the last dimension must be dense")
-    if block_table.shape[0] != n_seqs or not block_table.is_contiguous():
-        raise ValueError(f"block_table: expected a contiguous [{n_seqs}, width] tensor")
-    return EngramKvCache(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1],
-                         vs[2], pages, page_size, block_table.data_ptr(), block_table.shape[1])
+def _cache(desc: EngramAttnDesc, dtype, k_cache, v_cache, block_table, n_seqs: int):
+    if (isinstance(k_cache, torch.Tensor) and isinstance(v_cache, torch.Tensor)
+            and isinstance(block_table, torch.Tensor) and k_cache.is_cuda and v_cache.is_cuda
+            and block_table.is_cuda and k_cache.dtype is dtype and v_cache.dtype is dtype
+            and block_table.dtype is torch.int32):
+        shape, table = k_cache.shape, block_table.shape
+        if (len(shape) == 4 and shape[2] == desc.n_kv_heads and shape[3] == desc.head_dim
+                and v_cache.shape == shape and len(table) == 2 and table[0] == n_seqs
+                and block_table.is_contiguous()):
+            k0, k1, k2, k3 = k_cache.stride()
+            v0, v1, v2, v3 = v_cache.stride()
+            if k3 == 1 and v3 == 1:
+                return EngramKvCache(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2,
+                                     shape[0], shape[1], block_table.data_ptr(), table[1])
+    want = (f"[pages, page_size, {desc.n_kv_heads}, {desc.head_dim}] whose last dimension is "
+            f"dense, keys and values alike, with a contiguous int32 block_table [{n_seqs}, width]")
+    _refuse(k_cache, "k_cache, v_cache and block_table", want, dtype)
 
 
 def _scratch(desc: EngramAttnDesc, workspace, device):
     """The given workspace, or a fresh one."""
     if workspace is None:
-        workspace = torch.empty(engram_attn_workspace_size(desc), dtype=torch.uint8, device=device)
-    else:
-        _tensor(workspace, "workspace", 1, torch.uint8)
-        if not workspace.is_contiguous():
-            raise ValueError("workspace: must be contiguous")
+        return torch.empty(engram_attn_workspace_size(desc), dtype=torch.uint8, device=device)
+    if not (isinstance(workspace, torch.Tensor) and workspace.is_cuda
+            and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
+        _refuse(workspace, "workspace", "[bytes], contiguous", torch.uint8)
     return workspace
 
 
 def _lse(lse_out, tokens: int, desc: EngramAttnDesc):
     if lse_out is None:
         return None
-    _tensor(lse_out, "lse_out", 2, torch.float32)
-    if lse_out.shape != (tokens, desc.n_heads) or not lse_out.is_contiguous():
-        raise ValueError(f"lse_out: expected a contiguous [{tokens}, {desc.n_heads}] tensor")
+    if not (isinstance(lse_out, torch.Tensor) and lse_out.is_cuda
+            and lse_out.dtype is torch.float32 and lse_out.shape == (tokens, desc.n_heads)
+            and lse_out.is_contiguous()):
+        _refuse(lse_out, "lse_out", f"[{tokens}, {desc.n_heads}], contiguous", torch.float32)
     return lse_out.data_ptr()
+
+
+def _stream(stream, like):
+    """The given stream, or the current one of the tensors' device."""
+    return _raw_stream(like.get_device()) if stream is None else stream.cuda_stream
 
 
 def engram_attn_workspace_size(desc: EngramAttnDesc) -> int:
@@ -115,42 +123,48 @@ def engram_attn_prompt(desc: EngramAttnDesc, q, k, v, cu_seqlens, out, workspace
                        lse_out=None, stream=None):
     """Causal attention over the packed sequences cu_seqlens (int32 [sequences + 1]) of q, k and
     v. `workspace` (uint8, engram_attn_workspace_size bytes) defaults to a fresh one."""
-    qv = _view(q, "q", desc.n_heads, desc)
+    dtype, heads, kv_heads, dim = _TORCH[desc.dtype], desc.n_heads, desc.n_kv_heads, desc.head_dim
+    qv = _view(q, "q", heads, dim, dtype)
     total = q.shape[0]
-    kv = _view(k, "k", desc.n_kv_heads, desc, total)
-    vv = _view(v, "v", desc.n_kv_heads, desc, total)
-    ov = _view(out, "out", desc.n_heads, desc, total)
+    kv = _view(k, "k", kv_heads, dim, dtype, total)
+    vv = _view(v, "v", kv_heads, dim, dtype, total)
+    ov = _view(out, "out", heads, dim, dtype, total)
+    cu = _ints(cu_seqlens, "cu_seqlens")
     workspace = _scratch(desc, workspace, q.device)
     _check(lib().engram_attn_prompt(
-        ctypes.byref(desc), ctypes.byref(qv), ctypes.byref(kv), ctypes.byref(vv),
-        _ints(cu_seqlens, "cu_seqlens"), _sequences(cu_seqlens), total, ctypes.byref(ov),
-        _lse(lse_out, total, desc), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        ctypes.byref(desc), ctypes.byref(qv), ctypes.byref(kv), ctypes.byref(vv), cu,
+        _sequences(cu_seqlens), total, ctypes.byref(ov), _lse(lse_out, total, desc),
+        workspace.data_ptr(), workspace.numel(), _stream(stream, q)))
 
 
 def engram_attn_paged(desc: EngramAttnDesc, q, cu_seqlens, kv_len, block_table, k_cache, v_cache,
                       out, max_q: int, workspace=None, lse_out=None, stream=None):
     """Attention of the chunks cu_seqlens of q over the caches: kv_len (int32 [sequences]) counts
     the chunks' own positions. `max_q` is the longest chunk."""
-    qv = _view(q, "q", desc.n_heads, desc)
+    dtype, heads, dim = _TORCH[desc.dtype], desc.n_heads, desc.head_dim
+    qv = _view(q, "q", heads, dim, dtype)
     total = q.shape[0]
-    ov = _view(out, "out", desc.n_heads, desc, total)
+    ov = _view(out, "out", heads, dim, dtype, total)
+    cu = _ints(cu_seqlens, "cu_seqlens")
     n = _sequences(cu_seqlens)
-    cache = _cache(desc, k_cache, v_cache, block_table, n)
+    cache = _cache(desc, dtype, k_cache, v_cache, block_table, n)
     workspace = _scratch(desc, workspace, q.device)
     _check(lib().engram_attn_paged(
-        ctypes.byref(desc), ctypes.byref(qv), _ints(cu_seqlens, "cu_seqlens"), n, total, max_q,
-        _ints(kv_len, "kv_len", n), ctypes.byref(cache), ctypes.byref(ov),
-        _lse(lse_out, total, desc), workspace.data_ptr(), workspace.numel(), _stream(stream)))
+        ctypes.byref(desc), ctypes.byref(qv), cu, n, total, max_q, _ints(kv_len, "kv_len", n),
+        ctypes.byref(cache), ctypes.byref(ov), _lse(lse_out, total, desc), workspace.data_ptr(),
+        workspace.numel(), _stream(stream, q)))
 
 
 def engram_kv_append(desc: EngramAttnDesc, k, v, cu_seqlens, kv_len, block_table, k_cache, v_cache,
                      stream=None):
     """Write the chunks' keys and values into the caches' pages; kv_len already counts them."""
-    kv = _view(k, "k", desc.n_kv_heads, desc)
+    dtype, kv_heads, dim = _TORCH[desc.dtype], desc.n_kv_heads, desc.head_dim
+    kv = _view(k, "k", kv_heads, dim, dtype)
     total = k.shape[0]
-    vv = _view(v, "v", desc.n_kv_heads, desc, total)
+    vv = _view(v, "v", kv_heads, dim, dtype, total)
+    cu = _ints(cu_seqlens, "cu_seqlens")
     n = _sequences(cu_seqlens)
-    cache = _cache(desc, k_cache, v_cache, block_table, n)
+    cache = _cache(desc, dtype, k_cache, v_cache, block_table, n)
     _check(lib().engram_kv_append(
-        ctypes.byref(desc), ctypes.byref(kv), ctypes.byref(vv), _ints(cu_seqlens, "cu_seqlens"),
-        n, total, _ints(kv_len, "kv_len", n), ctypes.byref(cache), _stream(stream)))
+        ctypes.byref(desc), ctypes.byref(kv), ctypes.byref(vv), cu, n, total,
+        _ints(kv_len, "kv_len", n), ctypes.byref(cache), _stream(stream, k)))

@@ -66,9 +66,10 @@ inline AttnPieces attn_pieces_at(void* workspace, int32_t workers, int32_t rows)
 // Width of a row in the kernels: 64 or 128 columns, those past head_dim zero.
 constexpr int32_t attn_width(int32_t head_dim) { return head_dim <= 64 ? 64 : 128; }
 
-// Items of up to 16 rows (attn_rows_sm103.cu): decoding.
-constexpr int32_t kAttnRows = 16;
-cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t st);
+// Items of up to kAttnFewRows rows (attn_rows_sm103.cu): decoding and short chunks. `rows`: of the
+// longest chunk, at least the heads that share a key-value head.
+constexpr int32_t kAttnFewRows = 64;
+cudaError_t launch_attn_rows(const AttnArgs& a, int32_t rows, cudaStream_t st);
 
 // Items of up to 256 rows on tcgen05 (attn_tiles_sm103.cu): prompts and long chunks.
 constexpr int32_t kAttnItemRows = 256;

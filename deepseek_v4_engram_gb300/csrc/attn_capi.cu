@@ -255,8 +255,10 @@ ENGRAM_API int engram_attn_paged(const engram_attn_desc_t* desc, const engram_at
   a.n_pages = cache->n_pages;
   a.granule = granule_of(cache->page_size);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool few = int64_t(max_q) * a.group <= kAttnRows;
-  return report(few ? launch_attn_rows(a, st) : launch_attn_tiles(a, st), "engram_attn_paged");
+  const int64_t rows = int64_t(max_q > 1 ? max_q : 1) * a.group;
+  return report(rows <= kAttnFewRows ? launch_attn_rows(a, static_cast<int32_t>(rows), st)
+                                     : launch_attn_tiles(a, st),
+                "engram_attn_paged");
 }
 
 ENGRAM_API int engram_kv_append(const engram_attn_desc_t* desc, const engram_attn_view_t* k,

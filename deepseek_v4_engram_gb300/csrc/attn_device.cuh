@@ -97,7 +97,7 @@ __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volati
 // cursor. One pass over the lengths; all kThreads threads call it. A worker without work gets a
 // cursor that has nothing left. Worker 0 reports lengths beyond the page table.
 struct AttnStart {
-  int64_t sums[33];
+  int64_t sums[16];   // per warp
   int64_t per;
   AttnCursor cursor;
 };
@@ -105,6 +105,7 @@ struct AttnStart {
 template <int kThreads>
 __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worker,
                                                 AttnStart* sh, uint32_t* err) {
+  static_assert(kThreads <= 16 * 32, "sums");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t run = (p.n_seqs + kThreads - 1) / kThreads;
   const int32_t b0 = tid * run;

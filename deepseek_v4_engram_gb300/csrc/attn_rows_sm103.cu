@@ -1,19 +1,20 @@
-// Attention for items of at most 16 query rows: decoding, a few drafted tokens, any chunk of a
-// sequence whose rows (tokens x heads that share a key-value head) are few.
+// Attention for items of at most 16, 32 or 64 query rows: decoding, a few drafted tokens, any chunk
+// of a sequence whose rows (tokens x heads that share a key-value head) are few.
 //
 //   o_r = sum_j 2^(x_rj - M_r) v_j / sum_j 2^(x_rj - M_r),   x_rj = scale log2(e) q_r . k_j
 //
 // in one pass over the keys with a running maximum M and sum. What bounds it is the cache's bytes:
-// 16 rows make 16 multiply-adds of each key or value element, far below what the tensor cores do in
-// the time that the element takes to arrive. So the work is shared out by key tiles alone
+// 64 rows make 64 multiply-adds of each key or value element, below what the tensor cores do in the
+// time that the element takes to arrive. So the work is shared out by key tiles alone
 // (attn_plan.cuh), one CTA per SM streams its tiles through a ring of three 64 KB stages (six of
 // 32 KB where heads have up to 64 columns), which keeps more bytes in flight per SM than the memory's
 // latency needs, and the ring runs on across the ends of items.
 //
-// Roles (288 threads): warp 8 requests the tiles by TMA, one page granule per lane; warps 0-7 take
-// 16 of a tile's 128 keys each, so every warp has its own maximum, sum and output and no step of
-// the loop waits for another warp. The products run on mma.sync m16n8k16: its 16 rows are the whole
-// item, its fragments stay in registers (scores come out in the layout in which they go back in as
+// Roles (288 threads): warp 8 requests the tiles by TMA, one page granule per lane; warps 0-7 each
+// take 16 rows and some of a tile's keys (with kGroups groups of rows, 16 kGroups of the 128), 16 at
+// a time, so every warp has its own maximum, sum and output and no step of the loop waits for
+// another warp. The products run on mma.sync m16n8k16: its 16 rows are the whole item of a decoding
+// step, its fragments stay in registers (scores come out in the layout in which they go back in as
 // probabilities), and a tcgen05 tile would be seven eighths padding.
 #include "attn_device.cuh"
 #include "kernels.h"
@@ -40,7 +41,7 @@ struct Shared {
   uint64_t full[Geo<DH>::kStages];
   uint64_t empty[Geo<DH>::kStages];
   AttnStart start;
-  float ml[kConsumers][kAttnRows][2];
+  float ml[kConsumers][16][2];
   int abort;
 };
 
@@ -88,12 +89,13 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int c) {
                                (((c & 7) ^ (row & 7)) << 4));
 }
 
-template <int DH, bool kBf16>
+template <int DH, int kGroups, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const AttnArgs a,
                      const AttnPieces pieces) {
   using G = Geo<DH>;
+  constexpr int kRows = 16 * kGroups;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
   float* join = reinterpret_cast<float*>(smem + G::kStages * 2 * G::kTensorBytes);
@@ -151,15 +153,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ------------------------------------------------------------- consumers
     const int gid = lane >> 2, tid = lane & 3;
+    const int group = warp % kGroups;                       // of rows
+    const int keys_at = warp / kGroups * (16 * kGroups);    // first of this warp's keys in a tile
     uint32_t stage = 0, phase = 0;
     AttnMeta meta{0, 0, 0, 0};
     while (cur.next(a.plan, seg)) {
-      // Rows gid and gid + 8: token row / G of the item, head h * G + row % G.
+      // Rows gid and gid + 8 of the group: token row / G of the item, head h * G + row % G.
       int32_t limit[2];
       uint32_t qf[DH / 16][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int32_t r = gid + 8 * i, tok = r / a.group;
+        const int32_t r = group * 16 + gid + 8 * i, tok = r / a.group;
         const bool valid = tok < seg.ntok;
         const int32_t lim = seg.seq.m - seg.seq.n + (seg.token0 - seg.seq.q0) + tok + 1;
         limit[i] = valid && lim > 0 ? lim : 0;
@@ -183,12 +187,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             0xFFFFFFFFu, !attn_wait(&sh->full[stage], phase, abort, a.err));
         const uint32_t sk = smem_u32(smem + stage * 2 * G::kTensorBytes);
         const uint32_t sv = sk + G::kTensorBytes;
-        const int32_t key0 = t * kTileKeys + warp * 16;   // this warp's keys
-        if (here && key0 < seg.keys) {
+#pragma unroll 1
+        for (int at = keys_at; at < keys_at + 16 * kGroups; at += 16) {
+          const int32_t key0 = t * kTileKeys + at;
+          if (!here || key0 >= seg.keys) break;
           // scores of 16 rows by 16 keys
           float s[2][4] = {};
           {
-            const int row = warp * 16 + ((lane >> 4) << 3) + (lane & 7);
+            const int row = at + ((lane >> 4) << 3) + (lane & 7);
 #pragma unroll
             for (int kk = 0; kk < DH / 16; ++kk) {
               uint32_t b[4];
@@ -229,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               o[n][2 * i + 1] *= f;
             }
           }
-          const int row = warp * 16 + (lane & 15);
+          const int row = at + (lane & 15);
           const int32_t seen = seg.keys - key0;   // keys past it hold whatever the memory held
           if (!edge) {
 #pragma unroll
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                   uint32_t w;
                   asm volatile("ld.shared.u32 %0, [%1];"
                                : "=r"(w)
-                               : "r"(sv + tile_offset(warp * 16 + j, n) + tid * 4)
+                               : "r"(sv + tile_offset(at + j, n) + tid * 4)
                                : "memory");
 #pragma unroll
                   for (int i = 0; i < 2; ++i)
@@ -299,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
       }
 
-      // ---- the eight warps' maxima, sums and outputs become one
+      // ---- the maxima, sums and outputs of a row group's warps become one
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
@@ -314,10 +320,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float m = -INFINITY;
-        for (int w = 0; w < kConsumers; ++w) m = fmaxf(m, sh->ml[w][gid + 8 * i][0]);
+        for (int w = group; w < kConsumers; w += kGroups) m = fmaxf(m, sh->ml[w][gid + 8 * i][0]);
         const float base = m == -INFINITY ? 0.f : m;
         float l = 0.f;
-        for (int w = 0; w < kConsumers; ++w)
+        for (int w = group; w < kConsumers; w += kGroups)
           l += sh->ml[w][gid + 8 * i][1] * exp2_fast(sh->ml[w][gid + 8 * i][0] - base);
         m_all[i] = m;
         l_all[i] = l;
@@ -328,8 +334,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           o[n][2 * i + 1] *= f;
         }
       }
-      // warps 4-7 hand theirs to 0-3, then 2-3 to 0-1, then 1 to 0: each lane to the same lane
-      for (int give = 4; give >= 1; give >>= 1) {
+      // warps 4-7 hand theirs to 0-3, then 2-3 to 0-1, then 1 to 0, as far as a row group has more
+      // than one: each lane to the same lane
+#pragma unroll
+      for (int give = 4; give >= kGroups; give >>= 1) {
         if (warp >= give && warp < 2 * give) {
 #pragma unroll
           for (int n = 0; n < DH / 8; ++n)
@@ -348,14 +356,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             o[n][3] += v.w;
           }
         }
-        if (give > 1) named_bar_sync(1, kConsumers * 32);
+        if (give > kGroups) named_bar_sync(1, kConsumers * 32);
       }
-      if (warp == 0) {
+      if (warp < kGroups) {
         const bool whole = seg.begins() && seg.ends();
         const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg.begins() ? 1 : 0);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int32_t r = gid + 8 * i, tok = r / a.group;
+          const int32_t r = group * 16 + gid + 8 * i, tok = r / a.group;
           if (tok >= seg.ntok) continue;
           const int32_t head = seg.h * a.group + (r - tok * a.group);
           if (whole) {
@@ -371,13 +379,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               a.lse[static_cast<int64_t>(seg.token0 + tok) * a.heads + head] =
                   (m_all[i] + log2f(l_all[i])) * 0.69314718055994531f;
           } else {
-            float* po = pieces.o + (slot * kAttnRows + r) * DH;
+            float* po = pieces.o + (slot * kRows + r) * DH;
 #pragma unroll
             for (int n = 0; n < DH / 8; ++n)
               *reinterpret_cast<float2*>(po + n * 8 + tid * 2) =
                   make_float2(o[n][2 * i], o[n][2 * i + 1]);
             if (tid == 0)
-              *reinterpret_cast<float2*>(pieces.ml + (slot * kAttnRows + r) * 2) =
+              *reinterpret_cast<float2*>(pieces.ml + (slot * kRows + r) * 2) =
                   make_float2(m_all[i], l_all[i]);
           }
         }
@@ -391,22 +399,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   cta_sync_all();
 }
 
-template <int DH, bool kBf16>
+template <int DH, int kGroups, bool kBf16>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& tmK, const CUtensorMap& tmV,
                    cudaStream_t st) {
   const cudaError_t e = ensure_dynamic_smem(
-      reinterpret_cast<const void*>(attn_rows_kernel<DH, kBf16>), smem_bytes<DH>());
+      reinterpret_cast<const void*>(attn_rows_kernel<DH, kGroups, kBf16>), smem_bytes<DH>());
   if (e != cudaSuccess) return e;
-  return launch_ex(attn_rows_kernel<DH, kBf16>, dim3(a.plan.workers), dim3(kThreads),
+  return launch_ex(attn_rows_kernel<DH, kGroups, kBf16>, dim3(a.plan.workers), dim3(kThreads),
                    smem_bytes<DH>(), st, true, tmK, tmV, a,
-                   attn_pieces_at(a.workspace, a.plan.workers, kAttnRows));
+                   attn_pieces_at(a.workspace, a.plan.workers, 16 * kGroups));
 }
 
-}  // namespace
-
-cudaError_t launch_attn_rows(const AttnArgs& in, cudaStream_t st) {
-  AttnArgs a = in;
-  a.plan.tokens = kAttnRows / a.group;
+template <int kGroups>
+cudaError_t launch_any(AttnArgs a, cudaStream_t st) {
+  a.plan.tokens = 16 * kGroups / a.group;
   a.plan.workers = device_sm_count();
   a.plan.min_units = 1;
   a.plan.extra = kExtraUnits;
@@ -414,11 +420,19 @@ cudaError_t launch_attn_rows(const AttnArgs& in, cudaStream_t st) {
   if (!attn_tensor_maps(a, &tmK, &tmV)) return cudaErrorInvalidValue;
   cudaError_t e;
   if (attn_width(a.head_dim) == 64)
-    e = a.bf16 ? launch<64, true>(a, tmK, tmV, st) : launch<64, false>(a, tmK, tmV, st);
+    e = a.bf16 ? launch<64, kGroups, true>(a, tmK, tmV, st)
+               : launch<64, kGroups, false>(a, tmK, tmV, st);
   else
-    e = a.bf16 ? launch<128, true>(a, tmK, tmV, st) : launch<128, false>(a, tmK, tmV, st);
-  if (e != cudaSuccess) return e;
-  return launch_attn_combine(a, kAttnRows, st);
+    e = a.bf16 ? launch<128, kGroups, true>(a, tmK, tmV, st)
+               : launch<128, kGroups, false>(a, tmK, tmV, st);
+  return e != cudaSuccess ? e : launch_attn_combine(a, 16 * kGroups, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_rows(const AttnArgs& a, int32_t rows, cudaStream_t st) {
+  if (rows <= 16) return launch_any<1>(a, st);
+  return rows <= 32 ? launch_any<2>(a, st) : launch_any<4>(a, st);
 }
 
 }  // namespace engram

@@ -57,7 +57,7 @@ struct Shared {
   uint64_t drain;
   AttnStart start;
   AttnCursor cur[kThreads / 32];   // each warp's own
-  AttnSegment seg[kThreads / 32];
+  AttnSegment seg[kThreads / 32 + kSoftmaxWarps];   // each warp's, and the softmax warps' next
   int poison[2][kPoisonSlots];   // of warps 10 and 11, by segment
   uint32_t tmem_base;
   int abort;
@@ -250,11 +250,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &sh->abort;
   // Every warp walks the segments for itself; one lane does, and the others read what it left.
   AttnCursor& cur = sh->cur[warp];
-  const AttnSegment& seg = sh->seg[warp];
-  auto next_segment = [&]() {
+  auto next_segment = [&](int at = 0) {   // `at` 1: into the warp's second place
     __syncwarp();
     bool more = false;
-    if (lane == 0) more = cur.next(a.plan, sh->seg[warp]);
+    if (lane == 0) more = cur.next(a.plan, sh->seg[at ? kThreads / 32 + warp : warp]);
     return __shfl_sync(0xFFFFFFFFu, more, 0);
   };
   if (lane == 0) cur = sh->start.cursor;
@@ -270,13 +269,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t tok = row / a.group, sub = row - tok * a.group;
     uint32_t s_phase = 0, o_phase = 0, count = 0;
     AttnMeta meta{0, 0, 0, 0};
-    while (next_segment()) {
+    int at = 0;
+    for (bool more = next_segment(0), next; more; more = next, at ^= 1) {
+      const AttnSegment& seg = sh->seg[at ? kThreads / 32 + warp : warp];
       if (threadIdx.x == 0 && seg.begins() && !seg.ends())
         meta = AttnMeta{seg.b, seg.h, seg.rt, attn_pieces(seg, sh->start.per)};
       const bool tiles = seg.keys > 0;
       const uint32_t slot8 = count % kPoisonSlots;
       if (tiles) ++count;
-      if (t * kTileRows >= seg.ntok * a.group) continue;   // this row tile is empty
+      if (t * kTileRows >= seg.ntok * a.group) {   // this row tile is empty
+        next = next_segment(at ^ 1);
+        continue;
+      }
       const bool valid = tok < seg.ntok;
       const int32_t lim = seg.seq.m - seg.seq.n + (seg.token0 - seg.seq.q0) + tok + 1;
       const int32_t limit = valid && lim > 0 ? lim : 0;
@@ -351,9 +355,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           unpair(add2(sum[0], sum[1]), x, y);
           l += x + y;
         }
+        next = next_segment(at ^ 1);   // while the last product runs
         attn_wait(&sh->ofull[t], o_phase, abort, a.err);
         o_phase ^= 1u;
         tc_fence_after();
+      } else {
+        next = next_segment(at ^ 1);
       }
       const bool whole = seg.begins() && seg.ends();
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
@@ -373,20 +380,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int e = 0; e < 4; ++e)
         to[e] = __shfl_sync(0xFFFFFFFFu, place, (lane & ~3) + e);
       const int own = lane & 3;
+      if (poison) {   // rare: what warps 10-11 took out goes back to the rows that see it
+        const int32_t k0 = seg.first_keys > seg.tile0 * kTileKeys ? seg.first_keys
+                                                                  : seg.tile0 * kTileKeys;
+        const int32_t k1 = limit < seg.tile1 * kTileKeys ? limit : seg.tile1 * kTileKeys;
 #pragma unroll 1
-      for (int i = 0; i < DH / 32; ++i) {
-        uint32_t o[32];
-        if (tiles) {
+        for (int i = 0; i < DH / 32; ++i) {
+          uint32_t o[32];
           tc_ld_32x32b_x32(tO + i * 32, o);
           tc_wait_ld(o);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0;
-        }
-        if (poison) {
-          const int32_t k0 = seg.first_keys > seg.tile0 * kTileKeys ? seg.first_keys
-                                                                    : seg.tile0 * kTileKeys;
-          const int32_t k1 = limit < seg.tile1 * kTileKeys ? limit : seg.tile1 * kTileKeys;
           for (int32_t k = k0; k < k1; ++k) {
             const uint16_t* v = value_row(a, seg, k);
 #pragma unroll
@@ -397,36 +399,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           __syncwarp();
+          tc_st_32x32b_x32(tO + i * 32, o);
         }
-        if (whole) {
+        tc_wait_st();
+      }
+      uint32_t o[DH / 32][32];
+      if (tiles) {
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i) tc_ld_32x32b_x32(tO + i * 32, o[i]);
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i) tc_wait_ld(o[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[i][e] = 0;
+      }
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < DH / 32; ++i) {
           uint32_t w[4][4];
 #pragma unroll
           for (int v = 0; v < 4; ++v)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              w[v][e] = pack16x2<kBf16>(__uint_as_float(o[8 * v + 2 * e]) * inv,
-                                        __uint_as_float(o[8 * v + 2 * e + 1]) * inv);
+              w[v][e] = pack16x2<kBf16>(__uint_as_float(o[i][8 * v + 2 * e]) * inv,
+                                        __uint_as_float(o[i][8 * v + 2 * e + 1]) * inv);
+          exchange4(w, own);
+          const int col = i * 32 + own * 8;
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            if (to[v] >= 0 && col < a.head_dim)
+              *reinterpret_cast<uint4*>(a.out + to[v] + col) =
+                  make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < DH / 16; ++i) {
+          uint32_t w[4][4];
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[v][e] = o[i >> 1][(i & 1) * 16 + 4 * v + e];
           exchange4(w, own);
 #pragma unroll
           for (int v = 0; v < 4; ++v)
-            if (to[v] >= 0 && i * 32 + own * 8 < a.head_dim)
-              *reinterpret_cast<uint4*>(a.out + to[v] + i * 32 + own * 8) =
+            if (to[v] >= 0)
+              *reinterpret_cast<uint4*>(pieces.o + to[v] + i * 16 + own * 4) =
                   make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
-        } else {
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint32_t w[4][4];
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) w[v][e] = o[hf * 16 + 4 * v + e];
-            exchange4(w, own);
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              if (to[v] >= 0)
-                *reinterpret_cast<uint4*>(pieces.o + to[v] + i * 32 + hf * 16 + own * 4) =
-                    make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
-          }
         }
       }
       tc_fence_before();   // the next product into O follows this thread's next P
@@ -442,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) pieces.meta[blockIdx.x] = meta;
   } else {
     set_max_regs_down<kOtherRegs>();
+    const AttnSegment& seg = sh->seg[warp];
     if (warp == 8) {
       // ----------------------------------------------------------- MMA issuer
       constexpr uint32_t kIdS = idesc<kBf16>(128, 128, false), kIdO = idesc<kBf16>(128, DH, true);
@@ -642,6 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
 }
+
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory");
 
 template <int DH, bool kBf16>
 cudaError_t launch(const AttnArgs& a, const CUtensorMap& tmQ, const CUtensorMap& tmK,
