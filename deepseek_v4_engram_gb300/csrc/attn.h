@@ -12,7 +12,7 @@
 namespace engram {
 
 struct AttnArgs {
-  AttnPlan plan;             // tokens, workers, min_units and whole are the launcher's
+  AttnPlan plan;             // tokens, workers and extra are the launcher's
   bool bf16;                 // else f16
   int32_t heads;             // query heads
   int32_t group;             // query heads per key-value head
@@ -34,10 +34,11 @@ struct AttnArgs {
   uint32_t* err;
 };
 
-// The pieces of cut items: per worker one AttnMeta (the item that it begins and does not end) and
+// The pieces of cut items: per worker an AttnMeta (the item that it begins and does not end) and
 // two slots of `rows` rows: slot 0 for the item that it continues, slot 1 for the one it begins.
 struct AttnMeta {
-  int32_t b, h, rt, pieces;  // pieces = 0: nothing to join
+  int32_t token0, ntok, h;
+  int32_t pieces;            // of workers this one, the next, ...; 0: nothing to join
 };
 struct AttnPieces {
   AttnMeta* meta;            // [workers]

@@ -20,12 +20,9 @@ __global__ void __launch_bounds__(kThreads)
   const int32_t w = blockIdx.x;
   const AttnMeta meta = pieces.meta[w];
   if (meta.pieces == 0) return;
-  const AttnSeq s = attn_seq(a.plan, meta.b);
-  const int32_t t0 = meta.rt * a.plan.tokens;
-  const int32_t ntok = s.n - t0 < a.plan.tokens ? s.n - t0 : a.plan.tokens;
   const int lane = threadIdx.x & 31;
   constexpr int kVec = DH / 32;   // columns per lane
-  for (int32_t r = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); r < ntok * a.group;
+  for (int32_t r = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); r < meta.ntok * a.group;
        r += gridDim.y * (kThreads / 32)) {
     float m = -INFINITY;
     for (int32_t i = 0; i < meta.pieces; ++i) {
@@ -47,7 +44,7 @@ __global__ void __launch_bounds__(kThreads)
         acc[c + 1] += f * v.y;
       }
     }
-    const int32_t tok = s.q0 + t0 + r / a.group;
+    const int32_t tok = meta.token0 + r / a.group;
     const int32_t head = meta.h * a.group + r % a.group;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     uint16_t* op = a.out + static_cast<int64_t>(tok) * a.o_token +

@@ -51,17 +51,16 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
-// Where the keys of the granule that starts at position `pos` of sequence b lie: z and w
+// Where the keys of the granule that starts at position `pos` of the segment's sequence lie: z and w
 // coordinates of the tensor maps. A page number that the cache does not have is reported and
 // addressed past the end, where a copy reads zeros.
 struct KvPlace {
   int32_t z, w;
 };
-__device__ __forceinline__ KvPlace kv_place(const AttnArgs& a, const AttnSeq& s, int32_t b,
-                                            int32_t pos) {
+__device__ __forceinline__ KvPlace kv_place(const AttnArgs& a, const AttnSegment& s, int32_t pos) {
   if (a.table == nullptr) return {s.q0 + pos, 0};
   const int32_t col = pos / a.page_size;
-  int32_t page = a.table[static_cast<int64_t>(b) * a.table_width + col];
+  int32_t page = a.table[static_cast<int64_t>(s.b) * a.table_width + col];
   if (page < 0 || page >= a.n_pages) {
     set_error(a.err, kErrPageRange);
     page = a.n_pages;
@@ -98,53 +97,61 @@ __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volati
 // cursor that has nothing left. Worker 0 reports lengths beyond the page table.
 struct AttnStart {
   int64_t sums[16];   // per warp
-  int64_t per;
   AttnCursor cursor;
 };
 
 template <int kThreads>
-__device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worker,
-                                                AttnStart* sh, uint32_t* err) {
+__device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worker, AttnStart* sh,
+                                                uint32_t* err) {
   static_assert(kThreads <= 16 * 32, "sums");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int32_t run = (p.n_seqs + kThreads - 1) / kThreads;
   const int32_t b0 = tid * run;
   const int32_t b1 = b0 + run < p.n_seqs ? b0 + run : p.n_seqs;
-  int64_t mine = 0;
-  for (int32_t b = b0; b < b1; ++b) {
-    mine += attn_seq_units(p, attn_seq(p, b));
-    if (worker == 0 && p.kv_len && p.kv_len[b] > p.kv_cap) set_error(err, kErrCacheCapacity);
-  }
-  int64_t scan = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
-    if (lane >= o) scan += v;
-  }
-  if (lane == 31) sh->sums[warp] = scan;
   if (tid == 0) {
     sh->cursor.left = 0;
     sh->cursor.b = p.n_seqs;
   }
-  __syncthreads();
-  int64_t before = 0, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sh->sums[w];
-    total += sh->sums[w];
-  }
-  const int64_t per = attn_share(p, total);
-  const int64_t u0 = per * worker;
-  int64_t at = before + scan - mine;
-  if (tid == 0) sh->per = per;
-  if (u0 < total && at <= u0 && u0 < at + mine) {
-    int32_t b = b0;
-    for (;; ++b) {
-      const int64_t u = attn_seq_units(p, attn_seq(p, b));
-      if (u0 < at + u) break;
-      at += u;
+  // Pass 0 sums the run; pass 1, in the thread whose run holds the range's first unit, walks it
+  // (one loop for both: the code is read from memory once per launch and SM).
+  int64_t mine = 0, at = 0, u0 = -1, per = 0, total = 0;
+  bool holds = true;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    if (holds) {
+#pragma unroll 1
+      for (int32_t b = b0; b < b1; ++b) {
+        const int64_t u = attn_seq_units(p, attn_seq(p, b));
+        if (pass == 1 && u0 < at + u) {
+          sh->cursor.start(p, worker, per, b, u0 - at, total - u0 < per ? total - u0 : per);
+          break;
+        }
+        at += u;
+      }
     }
-    sh->cursor.start(p, b, u0 - at, total - u0 < per ? total - u0 : per);
+    if (pass == 1) break;
+    mine = at;
+    int64_t scan = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xFFFFFFFFu, scan, o);
+      if (lane >= o) scan += v;
+    }
+    if (lane == 31) sh->sums[warp] = scan;
+    __syncthreads();
+    at = scan - mine;
+#pragma unroll 1
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) at += sh->sums[w];
+      total += sh->sums[w];
+    }
+    per = attn_share(p, total);
+    u0 = per * worker;
+    holds = u0 < total && at <= u0 && u0 < at + mine;
   }
+  if (worker == 0 && p.kv_len)
+    for (int32_t b = b0; b < b1; ++b)
+      if (p.kv_len[b] > p.kv_cap) set_error(err, kErrCacheCapacity);
   __syncthreads();
 }
 

@@ -10,11 +10,13 @@
 // same keys.
 //
 // All the items' units laid end to end are units 0 .. W-1, and worker w (a CTA) takes the units
-// [w * per, (w + 1) * per) with per = ceil(W / workers), at least `min_units`. Prompts of any
-// lengths, causal triangles and long caches with few rows are so balanced by one rule that needs
-// no lengths on the host: every worker evaluates it for itself from the lengths in device memory.
-// An item that a boundary cuts is computed in pieces, each with its own running maximum and sum;
-// the pieces are joined afterwards (attn_combine.cu), always in the same order.
+// [w * per, (w + 1) * per) with per = ceil(W / workers). Prompts of any lengths, causal triangles
+// and long caches with few rows are so balanced by one rule that needs no lengths on the host:
+// every worker evaluates it for itself from the lengths in device memory. An item that a boundary
+// cuts is computed in pieces, each with its own running maximum and sum, that are joined afterwards
+// (attn_combine.cu), always in the same order. Where an item is small beside a worker's
+// share, the boundary moves to the item's nearer end instead: up to a quarter of a share of
+// imbalance costs less than the pieces' way through memory.
 //
 // A worker holds at most two pieces: one of an item that an earlier worker began (its first
 // segment), and one of an item that it begins and a later worker finishes (its last segment).
@@ -25,6 +27,7 @@
 namespace engram {
 
 constexpr int32_t kTileKeys = 128;   // keys per unit
+constexpr int32_t kWholeUnits = 8;   // items up to this size may be left whole
 
 struct AttnPlan {
   const int32_t* cu;       // [n_seqs + 1] first token of each sequence, and the end
@@ -35,7 +38,6 @@ struct AttnPlan {
   int32_t kv_heads;
   int32_t tokens;          // query tokens per item
   int32_t workers;
-  int32_t min_units;       // smallest share of a worker
   int32_t extra;           // units of an item beside its tiles
 };
 
@@ -113,19 +115,25 @@ __host__ __device__ inline int64_t attn_seq_units(const AttnPlan& p, const AttnS
 }
 
 __host__ __device__ inline int64_t attn_share(const AttnPlan& p, int64_t units) {
-  const int64_t per = (units + p.workers - 1) / p.workers;
-  return per > p.min_units ? per : p.min_units;
+  return (units + p.workers - 1) / p.workers;
+}
+
+// Whether an item of `units` units is left whole where the share is `per`.
+__host__ __device__ inline bool attn_whole(int32_t units, int64_t per) {
+  return units <= kWholeUnits && 2 * units <= per;
 }
 
 // A stretch of one item's key tiles, [tile0, tile1) of `cost`.
 struct AttnSegment {
-  AttnSeq seq;
-  int32_t b, h, rt;
+  int32_t b, h;
   int32_t tile0, tile1, cost;
-  int32_t keys;        // that the item's last token sees
+  int32_t q0;          // first token of its sequence
   int32_t token0;      // first token of the item in q
   int32_t ntok;        // its tokens
-  int32_t first_keys;  // keys that its first token sees (at least 0)
+  int32_t keys;        // that the item's last token sees
+  int32_t first;       // that its first token sees: token i sees first + i; none if that is <= 0
+  int32_t owner;       // the worker that begins it
+  int32_t pieces;      // workers that hold a piece of it: owner, owner + 1, ...
   __host__ __device__ bool begins() const { return tile0 == 0; }
   __host__ __device__ bool ends() const { return tile1 == cost; }
 };
@@ -135,25 +143,36 @@ struct AttnSegment {
 struct AttnCursor {
   AttnSeq seq;
   int32_t b, h, rt, unit;
+  int32_t worker;
+  int32_t per;    // the share, cut at 2^30 (an item is far smaller)
   int64_t left;
 
   __host__ __device__ bool next(const AttnPlan& p, AttnSegment& out) {
     if (left <= 0 || b >= p.n_seqs) return false;
-    out.seq = seq;
     out.b = b;
     out.h = h;
-    out.rt = rt;
     out.cost = attn_cost(p, seq, rt);
     const int32_t units = out.cost + p.extra;
-    const int32_t end = left >= units - unit ? units : unit + static_cast<int32_t>(left);
+    int32_t end = left >= units - unit ? units : unit + static_cast<int32_t>(left);
+    if (end < units && attn_whole(units, per)) {   // the boundary moves to the nearer end
+      if (2 * end <= units) {
+        left = 0;
+        return false;
+      }
+      left = units - unit;
+      end = units;
+    }
     out.tile0 = unit > p.extra ? unit - p.extra : 0;
     out.tile1 = end > p.extra ? end - p.extra : 0;
     out.keys = attn_keys(p, seq, rt);
     const int32_t t0 = rt * p.tokens;
+    out.q0 = seq.q0;
     out.token0 = seq.q0 + t0;
     out.ntok = seq.n - t0 < p.tokens ? seq.n - t0 : p.tokens;
-    const int32_t f = seq.m - seq.n + t0 + 1;
-    out.first_keys = f > 0 ? f : 0;
+    out.first = seq.m - seq.n + t0 + 1;
+    const int32_t before = unit > p.extra ? (unit - p.extra + per - 1) / per : 0;
+    out.owner = worker - before;
+    out.pieces = before + 1 + (units - end + per - 1) / per;
     left -= end - unit;
     if (end == units) step(p);
     return out.tile1 > out.tile0;   // a range may end before the item's first tile
@@ -172,8 +191,11 @@ struct AttnCursor {
     } while (seq.n == 0);
   }
 
-  // The worker's range begins inside sequence b, `pos` units into it, and holds `units`.
-  __host__ __device__ void start(const AttnPlan& p, int32_t b_, int64_t pos, int64_t units) {
+  // The range of worker `w` begins inside sequence b, `pos` units into it, and holds `units`.
+  __host__ __device__ void start(const AttnPlan& p, int32_t w, int64_t share, int32_t b_,
+                                 int64_t pos, int64_t units) {
+    worker = w;
+    per = share < (1 << 30) ? static_cast<int32_t>(share) : 1 << 30;
     b = b_;
     seq = attn_seq(p, b);
     left = units;
@@ -188,13 +210,17 @@ struct AttnCursor {
     }
     rt = lo;
     unit = static_cast<int32_t>(in - attn_units_before(p, seq, lo));
+    const int32_t all = attn_cost(p, seq, rt) + p.extra;
+    if (unit > 0 && attn_whole(all, per)) {   // as the worker before has it
+      if (2 * unit <= all) {
+        left += unit;
+        unit = 0;
+      } else {
+        left -= all - unit;
+        step(p);
+      }
+    }
   }
 };
-
-// Workers that hold a piece of the item that `s`, a worker's last segment, begins but does not
-// end: this one and the ones that follow.
-__host__ __device__ inline int32_t attn_pieces(const AttnSegment& s, int64_t per) {
-  return 1 + static_cast<int32_t>((s.cost - s.tile1 + per - 1) / per);
-}
 
 }  // namespace engram

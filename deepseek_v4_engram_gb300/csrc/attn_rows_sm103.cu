@@ -92,8 +92,8 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int c) {
 template <int DH, int kGroups, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_rows_kernel(const __grid_constant__ CUtensorMap tmK,
-                     const __grid_constant__ CUtensorMap tmV, const AttnArgs a,
-                     const AttnPieces pieces) {
+                     const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ AttnArgs a, const AttnPieces pieces) {
   using G = Geo<DH>;
   constexpr int kRows = 16 * kGroups;
   extern __shared__ uint8_t smem_raw[];
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t n = seg.keys - k0 < kTileKeys ? seg.keys - k0 : kTileKeys;
         const int32_t grans = (n + a.granule - 1) / a.granule;
         KvPlace at{0, 0};
-        if (gran < grans) at = kv_place(a, seg.seq, seg.b, k0 + gran * a.granule);
+        if (gran < grans) at = kv_place(a, seg, k0 + gran * a.granule);
         stop = __any_sync(0xFFFFFFFFu, !ring.acquire(sh->empty, abort, a.err));
         if (stop) break;
         uint8_t* dst = smem + (ring.stage * 2 + (lane < 16 ? 0 : 1)) * G::kTensorBytes;
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int i = 0; i < 2; ++i) {
         const int32_t r = group * 16 + gid + 8 * i, tok = r / a.group;
         const bool valid = tok < seg.ntok;
-        const int32_t lim = seg.seq.m - seg.seq.n + (seg.token0 - seg.seq.q0) + tok + 1;
+        const int32_t lim = seg.first + tok;
         limit[i] = valid && lim > 0 ? lim : 0;
         const uint16_t* qp = a.q + static_cast<int64_t>(seg.token0 + tok) * a.q_token +
                              static_cast<int64_t>(seg.h * a.group + (r - tok * a.group)) * a.q_head;
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_16816<kBf16>(s[1], qf[kk], b[2], b[3]);
             }
           }
-          const bool edge = key0 + 16 > seg.first_keys;   // some row does not see all of them
+          const bool edge = key0 + 16 > seg.first;   // some row does not see all of them
 #pragma unroll
           for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -389,9 +389,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   make_float2(m_all[i], l_all[i]);
           }
         }
-        if (seg.begins() && !seg.ends())
-          meta = AttnMeta{seg.b, seg.h, seg.rt, attn_pieces(seg, sh->start.per)};
       }
+      if (seg.begins() && !seg.ends()) meta = AttnMeta{seg.token0, seg.ntok, seg.h, seg.pieces};
     }
     if (threadIdx.x == 0) pieces.meta[blockIdx.x] = meta;
   }
@@ -414,7 +413,6 @@ template <int kGroups>
 cudaError_t launch_any(AttnArgs a, cudaStream_t st) {
   a.plan.tokens = 16 * kGroups / a.group;
   a.plan.workers = device_sm_count();
-  a.plan.min_units = 1;
   a.plan.extra = kExtraUnits;
   alignas(64) CUtensorMap tmK, tmV;
   if (!attn_tensor_maps(a, &tmK, &tmV)) return cudaErrorInvalidValue;

@@ -196,7 +196,7 @@ __device__ __forceinline__ void exchange4(uint32_t (&w)[4][4], int own) {
 // Value row of position `pos` (for the rare rows that see an infinity or NaN).
 __device__ __forceinline__ const uint16_t* value_row(const AttnArgs& a, const AttnSegment& s,
                                                      int32_t pos) {
-  if (a.table == nullptr) return a.v + (int64_t(s.seq.q0) + pos) * a.v_token + s.h * a.v_head;
+  if (a.table == nullptr) return a.v + (int64_t(s.q0) + pos) * a.v_token + s.h * a.v_head;
   const int32_t col = pos / a.page_size;
   const int32_t page = a.table[int64_t(s.b) * a.table_width + col];
   if (page < 0 || page >= a.n_pages) return nullptr;   // read as zeros
@@ -207,8 +207,8 @@ template <int DH, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tiles_kernel(const __grid_constant__ CUtensorMap tmQ,
                       const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV, const AttnArgs a,
-                      const AttnPieces pieces) {
+                      const __grid_constant__ CUtensorMap tmV,
+                      const __grid_constant__ AttnArgs a, const AttnPieces pieces) {
   using G = Geo<DH>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto next_segment = [&](int at = 0) {   // `at` 1: into the warp's second place
     __syncwarp();
     bool more = false;
-    if (lane == 0) more = cur.next(a.plan, sh->seg[at ? kThreads / 32 + warp : warp]);
+    if (lane == 0)  more = cur.next(a.plan, sh->seg[at ? kThreads / 32 + warp : warp]);
     return __shfl_sync(0xFFFFFFFFu, more, 0);
   };
   if (lane == 0) cur = sh->start.cursor;
@@ -269,20 +269,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t tok = row / a.group, sub = row - tok * a.group;
     uint32_t s_phase = 0, o_phase = 0, count = 0;
     AttnMeta meta{0, 0, 0, 0};
-    int at = 0;
-    for (bool more = next_segment(0), next; more; more = next, at ^= 1) {
+    int at = 1;
+    for (bool more = false, next;; more = next) {
+      at ^= 1;
+      next = next_segment(at ^ 1);   // one ahead, while this one's first scores are on their way
+      if (!more) {
+        if (!next) break;
+        continue;
+      }
       const AttnSegment& seg = sh->seg[at ? kThreads / 32 + warp : warp];
-      if (threadIdx.x == 0 && seg.begins() && !seg.ends())
-        meta = AttnMeta{seg.b, seg.h, seg.rt, attn_pieces(seg, sh->start.per)};
+      if (seg.begins() && !seg.ends()) meta = AttnMeta{seg.token0, seg.ntok, seg.h, seg.pieces};
       const bool tiles = seg.keys > 0;
       const uint32_t slot8 = count % kPoisonSlots;
       if (tiles) ++count;
-      if (t * kTileRows >= seg.ntok * a.group) {   // this row tile is empty
-        next = next_segment(at ^ 1);
-        continue;
-      }
+      if (t * kTileRows >= seg.ntok * a.group) continue;   // this row tile is empty
       const bool valid = tok < seg.ntok;
-      const int32_t lim = seg.seq.m - seg.seq.n + (seg.token0 - seg.seq.q0) + tok + 1;
+      const int32_t lim = seg.first + tok;
       const int32_t limit = valid && lim > 0 ? lim : 0;
       float m = -INFINITY, l = 0.f;
       if (tiles) {
@@ -355,12 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           unpair(add2(sum[0], sum[1]), x, y);
           l += x + y;
         }
-        next = next_segment(at ^ 1);   // while the last product runs
         attn_wait(&sh->ofull[t], o_phase, abort, a.err);
         o_phase ^= 1u;
         tc_fence_after();
-      } else {
-        next = next_segment(at ^ 1);
       }
       const bool whole = seg.begins() && seg.ends();
       const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
@@ -381,7 +380,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         to[e] = __shfl_sync(0xFFFFFFFFu, place, (lane & ~3) + e);
       const int own = lane & 3;
       if (poison) {   // rare: what warps 10-11 took out goes back to the rows that see it
-        const int32_t k0 = seg.first_keys > seg.tile0 * kTileKeys ? seg.first_keys
+        const int32_t k0 = seg.first > seg.tile0 * kTileKeys ? seg.first
                                                                   : seg.tile0 * kTileKeys;
         const int32_t k1 = limit < seg.tile1 * kTileKeys ? limit : seg.tile1 * kTileKeys;
 #pragma unroll 1
@@ -403,50 +402,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_wait_st();
       }
-      uint32_t o[DH / 32][32];
-      if (tiles) {
+#pragma unroll 1
+      for (int i = 0; i < DH / 32; ++i) {
+        uint32_t o[32];
+        if (tiles) {
+          tc_ld_32x32b_x32(tO + i * 32, o);
+          tc_wait_ld(o);
+        } else {
 #pragma unroll
-        for (int i = 0; i < DH / 32; ++i) tc_ld_32x32b_x32(tO + i * 32, o[i]);
-#pragma unroll
-        for (int i = 0; i < DH / 32; ++i) tc_wait_ld(o[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < DH / 32; ++i)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[i][e] = 0;
-      }
-      if (whole) {
-#pragma unroll
-        for (int i = 0; i < DH / 32; ++i) {
+          for (int e = 0; e < 32; ++e) o[e] = 0;
+        }
+        // whole: 32 columns of the result; else: 16 sums, twice
+#pragma unroll 1
+        for (int hf = 0; hf < (whole ? 1 : 2); ++hf) {
           uint32_t w[4][4];
 #pragma unroll
           for (int v = 0; v < 4; ++v)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              w[v][e] = pack16x2<kBf16>(__uint_as_float(o[i][8 * v + 2 * e]) * inv,
-                                        __uint_as_float(o[i][8 * v + 2 * e + 1]) * inv);
+              w[v][e] = whole ? pack16x2<kBf16>(__uint_as_float(o[8 * v + 2 * e]) * inv,
+                                                __uint_as_float(o[8 * v + 2 * e + 1]) * inv)
+                              : o[4 * v + e];
           exchange4(w, own);
-          const int col = i * 32 + own * 8;
+          if (whole) {
+            const int col = i * 32 + own * 8;
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (to[v] >= 0 && col < a.head_dim)
-              *reinterpret_cast<uint4*>(a.out + to[v] + col) =
-                  make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
-        }
-      } else {
+            for (int v = 0; v < 4; ++v)
+              if (to[v] >= 0 && col < a.head_dim)
+                *reinterpret_cast<uint4*>(a.out + to[v] + col) =
+                    make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
+          } else {
 #pragma unroll
-        for (int i = 0; i < DH / 16; ++i) {
-          uint32_t w[4][4];
+            for (int v = 0; v < 4; ++v) {
+              if (to[v] >= 0)
+                *reinterpret_cast<uint4*>(pieces.o + to[v] + i * 32 + hf * 16 + own * 4) =
+                    make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[v][e] = o[i >> 1][(i & 1) * 16 + 4 * v + e];
-          exchange4(w, own);
-#pragma unroll
-          for (int v = 0; v < 4; ++v)
-            if (to[v] >= 0)
-              *reinterpret_cast<uint4*>(pieces.o + to[v] + i * 16 + own * 4) =
-                  make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
+              for (int e = 0; e < 4; ++e) o[4 * v + e] = o[16 + 4 * v + e];
+            }
+          }
         }
       }
       tc_fence_before();   // the next product into O follows this thread's next P
@@ -497,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (seg.keys == 0) continue;
         const bool two = uniform(seg.ntok * a.group > kTileRows) != 0;
         const int32_t n = uniform(seg.tile1 - seg.tile0);
-        const int32_t j_guard = uniform(seg.first_keys / kTileKeys - seg.tile0);   // from here on: vok
+        const int32_t j_guard = uniform((seg.first > 0 ? seg.first : 0) / kTileKeys - seg.tile0);   // from here on: vok
         // scores of the first tile
         if (!wait(&sh->full[stage], phase) || !wait(&sh->qfull, q_phase)) break;
         q_phase ^= 1u;
@@ -561,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int32_t n = seg.keys - k0 < kTileKeys ? seg.keys - k0 : kTileKeys;
           const int32_t grans = (n + a.granule - 1) / a.granule;
           KvPlace at{0, 0};
-          if (lane < grans) at = kv_place(a, seg.seq, seg.b, k0 + lane * a.granule);
+          if (lane < grans) at = kv_place(a, seg, k0 + lane * a.granule);
           for (int kv = 0; kv < 2; ++kv) {
             stop = __any_sync(0xFFFFFFFFu, !ring.acquire(sh->empty, abort, a.err));
             if (stop) break;
@@ -609,14 +603,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kv = 0; kv < 2; ++kv) {
             attn_wait(&sh->full[stage], phase, abort, a.err);
             __syncwarp();
-            if (kv == 1 && (j + 1) * kTileKeys > seg.first_keys) {
+            if (kv == 1 && (j + 1) * kTileKeys > seg.first) {
               // Each lane takes one 16-byte chunk column and every kStep-th row.
               constexpr int kChunks = DH / 8, kStep = 2 * (32 / kChunks);
               const int ch = lane % kChunks;
               const uint32_t v = smem_u32(sKV + stage * G::kTileBytes) +
                                  (ch >> 3) * (kTileKeys * 128);
               auto at = [&](int32_t r) { return v + r * 128 + (((ch & 7) ^ (r & 7)) << 4); };
-              const int32_t f = seg.first_keys - j * kTileKeys, e = seg.keys - j * kTileKeys;
+              const int32_t f = seg.first - j * kTileKeys, e = seg.keys - j * kTileKeys;
               const int32_t r1 = e < kTileKeys ? e : kTileKeys;   // rows from here on: nobody's
               int32_t r = (f > 0 ? f : 0) + part * (32 / kChunks) + lane / kChunks;
               uint32_t any = 0;
@@ -683,7 +677,6 @@ cudaError_t launch_attn_tiles(const AttnArgs& in, cudaStream_t st) {
   AttnArgs a = in;
   a.plan.tokens = kItemRows / a.group;
   a.plan.workers = device_sm_count();
-  a.plan.min_units = 1;
   a.plan.extra = kExtraUnits;
   alignas(64) CUtensorMap tmQ, tmK, tmV;
   if (!attn_tensor_maps(a, &tmK, &tmV) ||
@@ -696,8 +689,9 @@ cudaError_t launch_attn_tiles(const AttnArgs& in, cudaStream_t st) {
   else
     e = a.bf16 ? launch<128, true>(a, tmQ, tmK, tmV, st)
                : launch<128, false>(a, tmQ, tmK, tmV, st);
-  if (e != cudaSuccess) return e;
-  return launch_attn_combine(a, kItemRows, st);
+  // prompts of at most one key tile are never cut
+  const bool cut = a.table != nullptr || a.plan.total > kTileKeys;
+  return e != cudaSuccess || !cut ? e : launch_attn_combine(a, kItemRows, st);
 }
 
 }  // namespace engram

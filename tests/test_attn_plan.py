@@ -1,8 +1,8 @@
 """Host check of how the attention kernels share out their work (no GPU): the header is compiled
 with g++ into a program that walks every worker's segments for many batches and checks that they
-tile every item's key tiles exactly once and in order, that a worker holds at most one piece it
-continues and one it begins, that the pieces counted for a cut item are the workers that hold it,
-and that the closed forms equal plain sums."""
+tile every item's key tiles exactly once and in order, that small items are whole, that a worker
+holds at most one piece it continues and one it begins, that all pieces of a cut item name the same
+first worker and the same number of pieces, and that the closed forms equal plain sums."""
 import os
 import shutil
 import subprocess
@@ -43,40 +43,48 @@ static long check(AttnPlan p) {
     total += u * p.kv_heads;
   }
   const int64_t per = attn_share(p, total);
-  if (per * p.workers < total || per < p.min_units) ++bad;
+  if (per * p.workers < total) ++bad;
   std::map<std::tuple<int, int, int>, int> done;     // item -> tiles done
-  std::map<std::tuple<int, int, int>, int> opened;   // cut item -> pieces still to come
+  std::map<std::tuple<int, int, int>, std::pair<int, int>> cut;   // cut item -> owner, pieces so far
+  std::map<std::tuple<int, int, int>, int> pieces;
   for (int w = 0; w < p.workers; ++w) {
     const int64_t u0 = per * w;
     if (u0 >= total) break;
     int b = p.n_seqs - 1;
     while (first[b] > u0 || attn_seq_units(p, attn_seq(p, b)) == 0) --b;
     AttnCursor c;
-    c.start(p, b, u0 - first[b], total - u0 < per ? total - u0 : per);
+    c.start(p, w, per, b, u0 - first[b], total - u0 < per ? total - u0 : per);
     AttnSegment s;
     bool was_last = false;
     int n = 0;
-    int64_t units = 0, left = total - u0 < per ? total - u0 : per;
+    int64_t units = 0;
     while (c.next(p, s)) {
       if (was_last) ++bad;                       // a piece that does not end is a worker's last
-      auto key = std::make_tuple(s.b, s.h, s.rt);
+      AttnSeq q = attn_seq(p, s.b);
+      auto key = std::make_tuple(s.b, s.h, (s.token0 - q.q0) / p.tokens);
       if (done[key] != s.tile0 || s.tile1 <= s.tile0 || s.tile1 > s.cost) ++bad;
       done[key] = s.tile1;
       if (!s.begins() && n != 0) ++bad;          // one that an earlier worker began is its first
-      if (!s.begins() && --opened[key] < 0) ++bad;
-      if (!s.ends()) {
-        was_last = true;
-        if (s.begins()) opened[key] = attn_pieces(s, per) - 1;
-      } else if (!s.begins() && opened[key] != 0) ++bad;
-      AttnSeq q = attn_seq(p, s.b);
-      if (s.token0 != q.q0 + s.rt * p.tokens || s.ntok < 1 || s.ntok > p.tokens ||
-          s.token0 + s.ntok > q.q0 + q.n) ++bad;
-      if (s.keys > std::max(0, q.m) || s.first_keys > s.keys) ++bad;
+      if (!(s.begins() && s.ends())) {
+        // an item that counts as small is whole; the others agree on who holds their pieces
+        if (attn_whole(s.cost + p.extra, per)) ++bad;
+        if (s.begins()) cut[key] = {w, 0};
+        if (s.owner != cut[key].first || s.owner + cut[key].second != w) ++bad;
+        ++cut[key].second;
+        if (s.begins()) pieces[key] = s.pieces;
+        if (s.pieces != pieces[key]) ++bad;
+        if (s.ends() != (cut[key].second == s.pieces)) ++bad;
+      }
+      was_last = !s.ends();
+      const int t0 = s.token0 - q.q0;
+      if (t0 % p.tokens || s.q0 != q.q0 || s.ntok < 1 || s.ntok > p.tokens || t0 + s.ntok > q.n ||
+          (s.ntok < p.tokens && t0 + s.ntok != q.n)) ++bad;
+      if (s.first != q.m - q.n + t0 + 1 || s.keys != std::max(0, s.first + s.ntok - 1)) ++bad;
       units += s.tile1 - s.tile0 + (s.begins() ? p.extra : 0);
       ++n;
     }
-    // at most the extra units of the items at its two ends are not this worker's own
-    if (units < left - p.extra || units > left + p.extra) ++bad;
+    // beyond its share, a worker has at most half a small item at each end
+    if (units > per + std::min<int64_t>(kWholeUnits, per / 2) + p.extra) ++bad;
   }
   for (int b = 0; b < p.n_seqs; ++b) {
     AttnSeq s = attn_seq(p, b);
@@ -84,7 +92,7 @@ static long check(AttnPlan p) {
       for (int rt = 0; rt < attn_items(p, s); ++rt)
         if (done[std::make_tuple(b, h, rt)] != attn_cost(p, s, rt)) ++bad;
   }
-  for (auto& o : opened) if (o.second != 0) ++bad;
+  for (auto& o : cut) if (o.second.second != pieces[o.first]) ++bad;
   return bad;
 }
 
@@ -110,14 +118,13 @@ int main() {
     const int toks[] = {1, 2, 3, 16, 36, 51, 64, 85, 128, 256};
     p.tokens = toks[rand() % 10];
     p.workers = 1 + rand() % 152;
-    p.min_units = 1 + rand() % 4;
     p.extra = rand() % 4;
     bad += check(p);
     ++cases;
   }
   // a very long cache: the sums pass 32 bits
   int cu[2] = {0, 1 << 20}, kv[1] = {1 << 29};
-  AttnPlan p{cu, kv, 1, 1 << 20, 1 << 29, 128, 2, 152, 1, 3};
+  AttnPlan p{cu, kv, 1, 1 << 20, 1 << 29, 128, 2, 152, 3};
   const int64_t u = attn_seq_units(p, attn_seq(p, 0));
   long double want = 0;
   for (long r = 0; r < (1 << 19); ++r)
