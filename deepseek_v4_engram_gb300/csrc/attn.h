@@ -69,7 +69,7 @@ constexpr int32_t attn_width(int32_t head_dim) { return head_dim <= 64 ? 64 : 12
 
 // Items of up to kAttnFewRows rows (attn_rows_sm103.cu): decoding and short chunks. `rows`: of the
 // longest chunk, at least the heads that share a key-value head.
-constexpr int32_t kAttnFewRows = 64;
+constexpr int32_t kAttnFewRows = 32;
 cudaError_t launch_attn_rows(const AttnArgs& a, int32_t rows, cudaStream_t st);
 
 // Items of up to 256 rows on tcgen05 (attn_tiles_sm103.cu): prompts and long chunks.

@@ -11,6 +11,7 @@ namespace engram {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kAtOnce = 4;   // pieces
 
 template <int DH, bool kBf16>
 __global__ void __launch_bounds__(kThreads)
@@ -24,24 +25,37 @@ __global__ void __launch_bounds__(kThreads)
   constexpr int kVec = DH / 32;   // columns per lane
   for (int32_t r = blockIdx.y * (kThreads / 32) + (threadIdx.x >> 5); r < meta.ntok * a.group;
        r += gridDim.y * (kThreads / 32)) {
-    float m = -INFINITY;
-    for (int32_t i = 0; i < meta.pieces; ++i) {
-      const int64_t slot = (static_cast<int64_t>(w) + i) * 2 + (i == 0);
-      m = fmaxf(m, pieces.ml[(slot * rows + r) * 2]);
-    }
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, acc[kVec] = {};
-    for (int32_t i = 0; i < meta.pieces; ++i) {
-      const int64_t slot = (static_cast<int64_t>(w) + i) * 2 + (i == 0);
-      const float2 ml = *reinterpret_cast<const float2*>(pieces.ml + (slot * rows + r) * 2);
-      const float f = exp2_fast(ml.x - base);
-      l += f * ml.y;
-      const float* o = pieces.o + (slot * rows + r) * DH + lane * kVec;
+    // a running maximum over groups of pieces whose loads are in flight together
+    float m = -INFINITY, l = 0.f, acc[kVec] = {};
+    for (int32_t i0 = 0; i0 < meta.pieces; i0 += kAtOnce) {
+      float2 ml[kAtOnce], v[kAtOnce][kVec / 2];
 #pragma unroll
-      for (int c = 0; c < kVec; c += 2) {
-        const float2 v = *reinterpret_cast<const float2*>(o + c);
-        acc[c] += f * v.x;
-        acc[c + 1] += f * v.y;
+      for (int i = 0; i < kAtOnce; ++i) {
+        const int32_t k = i0 + i < meta.pieces ? i0 + i : i0;
+        const int64_t at = ((static_cast<int64_t>(w) + k) * 2 + (k == 0)) * rows + r;
+        ml[i] = *reinterpret_cast<const float2*>(pieces.ml + at * 2);
+        const float* o = pieces.o + at * DH + lane * kVec;
+#pragma unroll
+        for (int c = 0; c < kVec; c += 2) v[i][c / 2] = *reinterpret_cast<const float2*>(o + c);
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) top = fmaxf(top, ml[i].x);
+      const float base = top == -INFINITY ? 0.f : top, f0 = exp2_fast(m - base);
+      m = top;
+      l *= f0;
+#pragma unroll
+      for (int c = 0; c < kVec; ++c) acc[c] *= f0;
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (i0 + i >= meta.pieces) continue;
+        const float f = exp2_fast(ml[i].x - base);
+        l += f * ml[i].y;
+#pragma unroll
+        for (int c = 0; c < kVec; c += 2) {
+          acc[c] += f * v[i][c / 2].x;
+          acc[c + 1] += f * v[i][c / 2].y;
+        }
       }
     }
     const int32_t tok = meta.token0 + r / a.group;

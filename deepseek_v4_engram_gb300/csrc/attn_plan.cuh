@@ -74,25 +74,33 @@ __host__ __device__ inline int32_t attn_cost(const AttnPlan& p, const AttnSeq& s
   return t > 0 ? t : 1;
 }
 
-// sum_{i < n} floor((a i + b) / m), by the Euclidean reduction of the lattice-point count:
-// exchange the roles of a and m once both a and b are below m. a n + b stays below 2^32 here
-// (a < 2^8 after the first step, n < 2^24).
-__host__ __device__ inline uint64_t attn_floor_sum(uint32_t n, uint32_t m, uint32_t a,
-                                                   uint32_t b) {
-  uint64_t sum = 0;
-  while (n > 0) {
+// sum_{i < n} floor((a i + b) / kTileKeys), by the Euclidean reduction of the lattice-point count:
+// take out what both a and b hold of the divisor, then exchange the roles of a and the divisor.
+// a n + b stays below 2^32 (a < 2^8 after the first step, n < 2^24). One turn of the loop where a
+// divides kTileKeys, none where it is a multiple.
+__host__ __device__ inline uint64_t attn_floor_sum(uint32_t n, uint32_t a, uint32_t b) {
+  uint32_t m = kTileKeys;
+  uint64_t sum = (static_cast<uint64_t>(n) * (n - 1) / 2) * (a / kTileKeys) +
+                 static_cast<uint64_t>(n) * (b / kTileKeys);
+  a %= kTileKeys;
+  b %= kTileKeys;
+  for (uint32_t y = a * n + b; y >= m && n > 0; y = a * n + b) {
+    n = y / m;
+    b = y % m;
+    const uint32_t t = a;
+    a = m;
+    m = t;
     sum += (static_cast<uint64_t>(n) * (n - 1) / 2) * (a / m) + static_cast<uint64_t>(n) * (b / m);
     a %= m;
     b %= m;
-    const uint32_t y = a * n + b;
-    if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const uint32_t t = m;
-    m = a;
-    a = t;
   }
   return sum;
+}
+
+// a / b for a >= 0, b > 0, in 32 bits where they are enough.
+__host__ __device__ inline int64_t attn_div(int64_t a, int64_t b) {
+  if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
 }
 
 // Units of the token tiles 0 .. k-1 of one key-value head (k <= attn_items).
@@ -100,22 +108,24 @@ __host__ __device__ inline int64_t attn_units_before(const AttnPlan& p, const At
                                                      int32_t k) {
   if (k <= 0) return 0;
   int64_t u = static_cast<int64_t>(k) * p.extra;
-  if (k == attn_items(p, s)) u += attn_cost(p, s, --k);   // the last one may hold fewer tokens
+  if (static_cast<int64_t>(k) * p.tokens >= s.n) u += attn_cost(p, s, --k);   // the last one may hold fewer tokens
+  if (k == 0) return u;
   const int32_t a = s.m - s.n;
   int32_t z = a < 0 ? -a / p.tokens : 0;   // tiles that see nothing: one unit each
   if (z > k) z = k;
   u += z;
+  if (k == z) return u;
   return u + static_cast<int64_t>(attn_floor_sum(
-                 static_cast<uint32_t>(k - z), kTileKeys, p.tokens,
+                 static_cast<uint32_t>(k - z), p.tokens,
                  static_cast<uint32_t>(a + (z + 1) * p.tokens + kTileKeys - 1)));
 }
 
 __host__ __device__ inline int64_t attn_seq_units(const AttnPlan& p, const AttnSeq& s) {
-  return s.n == 0 ? 0 : attn_units_before(p, s, attn_items(p, s)) * p.kv_heads;
+  return attn_units_before(p, s, attn_items(p, s)) * p.kv_heads;
 }
 
 __host__ __device__ inline int64_t attn_share(const AttnPlan& p, int64_t units) {
-  return (units + p.workers - 1) / p.workers;
+  return attn_div(units + p.workers - 1, p.workers);
 }
 
 // Whether an item of `units` units is left whole where the share is `per`.
@@ -200,7 +210,7 @@ struct AttnCursor {
     seq = attn_seq(p, b);
     left = units;
     const int64_t head = attn_units_before(p, seq, attn_items(p, seq));
-    h = static_cast<int32_t>(pos / head);
+    h = static_cast<int32_t>(attn_div(pos, head));
     const int64_t in = pos - h * head;
     int32_t lo = 0, hi = attn_items(p, seq);   // units_before(lo) <= in < units_before(hi)
     while (hi - lo > 1) {

@@ -1,10 +1,10 @@
-// Attention for items of at most 16, 32 or 64 query rows: decoding, a few drafted tokens, any chunk
+// Attention for items of at most 16 or 32 query rows: decoding, a few drafted tokens, any chunk
 // of a sequence whose rows (tokens x heads that share a key-value head) are few.
 //
 //   o_r = sum_j 2^(x_rj - M_r) v_j / sum_j 2^(x_rj - M_r),   x_rj = scale log2(e) q_r . k_j
 //
 // in one pass over the keys with a running maximum M and sum. What bounds it is the cache's bytes:
-// 64 rows make 64 multiply-adds of each key or value element, below what the tensor cores do in the
+// 32 rows make 32 multiply-adds of each key or value element, below what the tensor cores do in the
 // time that the element takes to arrive. So the work is shared out by key tiles alone
 // (attn_plan.cuh), one CTA per SM streams its tiles through a ring of three 64 KB stages (six of
 // 32 KB where heads have up to 64 columns), which keeps more bytes in flight per SM than the memory's
@@ -429,8 +429,7 @@ cudaError_t launch_any(AttnArgs a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_attn_rows(const AttnArgs& a, int32_t rows, cudaStream_t st) {
-  if (rows <= 16) return launch_any<1>(a, st);
-  return rows <= 32 ? launch_any<2>(a, st) : launch_any<4>(a, st);
+  return rows <= 16 ? launch_any<1>(a, st) : launch_any<2>(a, st);
 }
 
 }  // namespace engram
