@@ -402,43 +402,60 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_wait_st();
       }
+      // 64 columns at a time; 16 bytes of a row are 8 results or 4 sums
 #pragma unroll 1
-      for (int i = 0; i < DH / 32; ++i) {
-        uint32_t o[32];
-        if (tiles) {
-          tc_ld_32x32b_x32(tO + i * 32, o);
-          tc_wait_ld(o);
-        } else {
+      for (int i = 0; i < DH; i += 64) {
+        uint32_t o[2][32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0;
-        }
-        // whole: 32 columns of the result; else: 16 sums, twice
-#pragma unroll 1
-        for (int hf = 0; hf < (whole ? 1 : 2); ++hf) {
-          uint32_t w[4][4];
+        for (int h = 0; h < 2; ++h)
+          if (tiles) {
+            tc_ld_32x32b_x32(tO + i + h * 32, o[h]);
+          } else {
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
+            for (int e = 0; e < 32; ++e) o[h][e] = 0;
+          }
+        tc_wait_ld(o[0]);
+        tc_wait_ld(o[1]);
+        if (whole) {
+          uint32_t w[2][4][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[v][e] = whole ? pack16x2<kBf16>(__uint_as_float(o[8 * v + 2 * e]) * inv,
-                                                __uint_as_float(o[8 * v + 2 * e + 1]) * inv)
-                              : o[4 * v + e];
-          exchange4(w, own);
-          if (whole) {
-            const int col = i * 32 + own * 8;
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[h][v][e] = pack16x2<kBf16>(__uint_as_float(o[h][8 * v + 2 * e]) * inv,
+                                             __uint_as_float(o[h][8 * v + 2 * e + 1]) * inv);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) exchange4(w[h], own);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = i + h * 32 + own * 8;
 #pragma unroll
             for (int v = 0; v < 4; ++v)
               if (to[v] >= 0 && col < a.head_dim)
                 *reinterpret_cast<uint4*>(a.out + to[v] + col) =
-                    make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
-          } else {
+                    make_uint4(w[h][v][0], w[h][v][1], w[h][v][2], w[h][v][3]);
+          }
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[4][4];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
+            for (int v = 0; v < 4; ++v)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) w[v][e] = o[0][4 * v + e];
+            exchange4(w, own);
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
               if (to[v] >= 0)
-                *reinterpret_cast<uint4*>(pieces.o + to[v] + i * 32 + hf * 16 + own * 4) =
+                *reinterpret_cast<uint4*>(pieces.o + to[v] + i + q * 16 + own * 4) =
                     make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) o[4 * v + e] = o[16 + 4 * v + e];
+            for (int e = 0; e < 16; ++e) {   // the next 16 sums
+              o[0][e] = o[0][e + 16];
+              o[0][e + 16] = o[1][e];
+              o[1][e] = o[1][e + 16];
             }
           }
         }
@@ -465,17 +482,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t q_phase = 0, p_phase[2] = {0, 0};
       const uint32_t td = uniform(tmem);
       const uint32_t q_lo = uniform(kmajor_lo(smem_u32(sQ))), kv = uniform(smem_u32(sKV));
-      bool ok = true;
+      // After a wait that gave up, the warp still runs to its end, on whatever shared memory holds.
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        ok = ok && __all_sync(0xFFFFFFFFu, attn_wait(bar, parity, abort, a.err));
+        attn_wait(bar, parity, abort, a.err);
         tc_fence_after();
-        return ok;
       };
       auto commit = [&](uint64_t* bar) {
         if (elect_one()) tc_commit(bar);
         __syncwarp();
       };
-      auto scores = [&](int t, uint32_t ks) {
+      auto scores = [&](int t, uint32_t ks, bool done, bool last) {
         const uint32_t k_lo = kmajor_lo(kv + ks * G::kTileBytes);
         if (elect_one()) {
 #pragma unroll
@@ -484,21 +500,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                  desc_of(q_lo + ((t * kTileRows + (kk >> 2) * kItemRows) * 128 >> 4) + 2 * (kk & 3)),
                  desc_of(k_lo + ((kk >> 2) * kTileKeys * 128 >> 4) + 2 * (kk & 3)), kIdS, kk != 0);
         tc_commit(&sh->sfull[t]);
+        if (done) tc_commit(&sh->empty[ks]);
+        if (done && last) tc_commit(&sh->qempty);
         }
         __syncwarp();
       };
-      while (ok && next_segment()) {
+      while (next_segment()) {
         if (seg.keys == 0) continue;
         const bool two = uniform(seg.ntok * a.group > kTileRows) != 0;
         const int32_t n = uniform(seg.tile1 - seg.tile0);
         const int32_t j_guard = uniform((seg.first > 0 ? seg.first : 0) / kTileKeys - seg.tile0);   // from here on: vok
         // scores of the first tile
-        if (!wait(&sh->full[stage], phase) || !wait(&sh->qfull, q_phase)) break;
+        wait(&sh->full[stage], phase);
+        wait(&sh->qfull, q_phase);
         q_phase ^= 1u;
-        scores(0, stage);
-        if (two) scores(1, stage);
-        if (n == 1) commit(&sh->qempty);
-        commit(&sh->empty[stage]);
+        scores(0, stage, !two, n == 1);
+        if (two) scores(1, stage, true, n == 1);
         if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
         for (int32_t j = 0; j < n; ++j) {
           const uint32_t vs = stage, vph = phase;
@@ -508,35 +525,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t v_lo = mnmajor_lo(kv + vs * G::kTileBytes);
           // what was requested long ago first, so that nothing else stands between P and its MMAs
           if (j >= j_guard) {
-            if (!wait(&sh->vok[vs], (vphase >> vs) & 1u)) break;
+            wait(&sh->vok[vs], (vphase >> vs) & 1u);
             vphase ^= 1u << vs;
-          } else if (!wait(&sh->full[vs], vph)) {
-            break;
+          } else {
+            wait(&sh->full[vs], vph);
           }
           auto tile = [&](int t) {
-            if (!wait(&sh->pfull[t], p_phase[t])) return;
+            wait(&sh->pfull[t], p_phase[t]);
             p_phase[t] ^= 1u;
             if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kTileKeys / 16; ++kk)
-              mma_ts(td + G::kO + t * DH, td + t * 128 + kk * 8,
-                     desc_of(v_lo + (kk * 16 * 128 >> 4)), kIdO, (j | kk) != 0);
+              for (int kk = 0; kk < kTileKeys / 16; ++kk)
+                mma_ts(td + G::kO + t * DH, td + t * 128 + kk * 8,
+                       desc_of(v_lo + (kk * 16 * 128 >> 4)), kIdO, (j | kk) != 0);
+              if (!more) tc_commit(&sh->ofull[t]);
+              if (t == 1 || !two) tc_commit(&sh->empty[vs]);
             }
             __syncwarp();
-            if (!more) {
-              commit(&sh->ofull[t]);
-            } else {
-              if (t == 0 && !wait(&sh->full[ks], kph)) return;
-              scores(t, ks);
+            if (more) {
+              if (t == 0) wait(&sh->full[ks], kph);
+              scores(t, ks, t == 1 || !two, j + 2 == n);
             }
           };
           tile(0);
-          if (two && ok) tile(1);
-          if (!ok) break;
-          commit(&sh->empty[vs]);
+          if (two) tile(1);
           if (more) {
-            if (j + 2 == n) commit(&sh->qempty);
-            commit(&sh->empty[ks]);
             if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
           }
         }
