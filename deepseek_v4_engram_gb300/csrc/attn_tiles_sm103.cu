@@ -11,9 +11,10 @@
 // units, which are the nearer bound for heads of 64. So the two row tiles take turns: while the
 // tensor cores work on one, the other's softmax runs. Both read the same key and value tiles.
 //
-// The maximum that a row subtracts lags: it is only raised when a tile exceeds it by more than
-// 2^8, because raising it means rescaling O in TMEM. Probabilities are then up to 2^8 instead of
-// 1, which f32 sums and both 16-bit types hold as exactly, and the result is the same quotient.
+// The maximum that a row subtracts lags: it is only raised when a tile's probabilities against it
+// sum to more than kMostSum, because finding it costs a pass over the scores and raising it means
+// rescaling O in TMEM. Probabilities are then up to 512 instead of 1, which f32 sums and both 16-bit
+// types hold as exactly, and the result is the same quotient.
 //
 // Roles (384 threads): warps 0-3 and 4-7 softmax and output of row tile 0 and 1 (thread = row =
 // TMEM lane); warp 8 issues the MMAs; warp 9 requests key and value tiles by TMA (one page granule
@@ -40,6 +41,7 @@ constexpr int kTileRows = 128;
 constexpr int kItemRows = kAttnItemRows;   // two row tiles
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 256 * 208 + 128 * 88 = 384 * 168
 constexpr int kPoisonSlots = 8;
+constexpr float kMostSum = 512.f;   // of a tile's probabilities against an older maximum
 constexpr int kExtraUnits = 2;
 
 template <int DH>
@@ -305,57 +307,69 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 32; ++e)
                 if (i * 32 + e >= left) s[i][e] = 0xFF800000u;   // -infinity
           }
-          float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          // The maximum of a row's first tile is found first. Later tiles rarely raise it: their
+          // exponentials are taken against the one that is there, and only if their sum says that
+          // some were far above it (or nothing had been seen), the maximum is found after all, O
+          // and l are scaled down to it and the exponentials taken again.
+          bool fresh = j == seg.tile0;
+          float sums;
+          for (;;) {
+            if (fresh) {
+              float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int e = 0; e < 32; e += 2)
+              for (int e = 0; e < 32; e += 2)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              mt[i] = max3(mt[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
-          const float top = fmaxf(m, fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])));
-          if (j == seg.tile0) {
-            m = top;
-          } else if (__any_sync(0xFFFFFFFFu, (top - m) * c > 8.f)) {
-            // The score MMA that this tile waited for came after the last product with V, so O
-            // is at rest.
-            const float f = m == -INFINITY ? 0.f : exp2_fast((m - top) * c);
-            m = top;
-            l *= f;
+                for (int i = 0; i < 4; ++i)
+                  mt[i] = max3(mt[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
+              const float top = fmaxf(m, fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])));
+              if (j > seg.tile0) {
+                // The score MMA that this tile waited for came after the last product with V, so
+                // O is at rest.
+                const float f = m == -INFINITY ? 0.f : exp2_fast((m - top) * c);
+                l *= f;
 #pragma unroll 1
-            for (int i = 0; i < DH / 32; ++i) {
-              uint32_t o[32];
-              tc_ld_32x32b_x32(tO + i * 32, o);
-              tc_wait_ld(o);
+                for (int i = 0; i < DH / 32; ++i) {
+                  uint32_t o[32];
+                  tc_ld_32x32b_x32(tO + i * 32, o);
+                  tc_wait_ld(o);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tc_st_32x32b_x32(tO + i * 32, o);
+                  for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tc_st_32x32b_x32(tO + i * 32, o);
+                }
+              }
+              m = top;
             }
-          }
-          const float base = m == -INFINITY ? 0.f : -m * c;
-          const uint64_t c2 = pair(c, c), b2 = pair(base, base);
-          uint64_t sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+            const float base = m == -INFINITY ? 0.f : -m * c;
+            const uint64_t c2 = pair(c, c), b2 = pair(base, base);
+            uint64_t sum[4] = {};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t p[16];
+            for (int i = 0; i < 4; ++i) {
+              uint32_t p[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float x, y;
-              unpair(fma2(pair(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])), c2,
-                          b2),
-                     x, y);
-              x = exp2_fast(x);
-              y = exp2_fast(y);
-              sum[e & 1] = add2(sum[e & 1], pair(x, y));
-              p[e] = pack16x2<kBf16>(x, y);
+              for (int e = 0; e < 16; ++e) {
+                float x, y;
+                unpair(fma2(pair(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1])),
+                            c2, b2),
+                       x, y);
+                x = exp2_fast(x);
+                y = exp2_fast(y);
+                sum[e & 3] = add2(sum[e & 3], pair(x, y));
+                p[e] = pack16x2<kBf16>(x, y);
+              }
+              tc_st_32x32b_x16(tS + i * 16, p);
             }
-            tc_st_32x32b_x16(tS + i * 16, p);
+            float x, y;
+            unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
+            sums = x + y;
+            if (fresh || !__any_sync(0xFFFFFFFFu, sums > kMostSum || (m == -INFINITY && left > 0)))
+              break;
+            fresh = true;
           }
           tc_wait_st();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh->pfull[t]);
-          float x, y;
-          unpair(add2(sum[0], sum[1]), x, y);
-          l += x + y;
+          l += sums;
         }
         attn_wait(&sh->ofull[t], o_phase, abort, a.err);
         o_phase ^= 1u;
