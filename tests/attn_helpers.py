@@ -44,7 +44,7 @@ def assert_attn_close(got, lse, ref, dtype, head_dim, scale):
         n = f64(lse)
         empty = np.isneginf(ref[1])
         assert (np.isneginf(n) == empty).all(), "lse is -inf exactly where a row sees nothing"
-        d = np.abs(n - ref[1], where=~empty, out=np.zeros_like(n))
+        d = np.abs(np.where(empty, 0.0, n) - np.where(empty, 0.0, ref[1]))
         assert (d <= t_lse).all(), f"lse off by {d.max():.3g}"
 
 
