@@ -34,14 +34,17 @@ struct AttnArgs {
   uint32_t* err;
 };
 
-// The pieces of cut items: per worker an AttnMeta (the item that it begins and does not end) and
-// two slots of `rows` rows: slot 0 for the item that it continues, slot 1 for the one it begins.
+// The pieces of cut items. A worker continues at most one item that another began and begins at
+// most one that another ends: for each of the two, in this order, it has an AttnMeta and a slot of
+// `rows` rows.
 struct AttnMeta {
   int32_t token0, ntok, h;
-  int32_t pieces;            // of workers this one, the next, ...; 0: nothing to join
+  int32_t pieces;            // of workers owner, owner + 1, ...; 0: the worker has no such item
+  int32_t owner;             // the worker that begins it
+  int32_t unused[3];
 };
 struct AttnPieces {
-  AttnMeta* meta;            // [workers]
+  AttnMeta* meta;            // [workers * 2]
   float* ml;                 // [workers * 2, rows, 2]: running maximum (of log2 scores) and sum
   float* o;                  // [workers * 2, rows, width]: sum of 2^(x - max) v
 };
@@ -49,7 +52,7 @@ struct AttnPieces {
 constexpr size_t attn_round256(size_t n) { return (n + 255) & ~size_t(255); }
 
 inline size_t attn_pieces_bytes(int32_t workers, int32_t rows, int32_t width) {
-  return attn_round256(size_t(workers) * sizeof(AttnMeta)) +
+  return attn_round256(size_t(workers) * 2 * sizeof(AttnMeta)) +
          attn_round256(size_t(workers) * 2 * rows * 2 * 4) + size_t(workers) * 2 * rows * width * 4;
 }
 
@@ -57,7 +60,7 @@ inline AttnPieces attn_pieces_at(void* workspace, int32_t workers, int32_t rows)
   uint8_t* p = static_cast<uint8_t*>(workspace);
   AttnPieces r;
   r.meta = reinterpret_cast<AttnMeta*>(p);
-  p += attn_round256(size_t(workers) * sizeof(AttnMeta));
+  p += attn_round256(size_t(workers) * 2 * sizeof(AttnMeta));
   r.ml = reinterpret_cast<float*>(p);
   p += attn_round256(size_t(workers) * 2 * rows * 2 * 4);
   r.o = reinterpret_cast<float*>(p);

@@ -155,4 +155,16 @@ __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worke
   __syncthreads();
 }
 
+// What the joining kernel has to know of a segment that is a piece, written by one thread; the two
+// entries of a worker are first cleared by attn_no_pieces.
+__device__ __forceinline__ void attn_no_pieces(const AttnPieces& p) {
+  p.meta[blockIdx.x * 2].pieces = 0;
+  p.meta[blockIdx.x * 2 + 1].pieces = 0;
+}
+__device__ __forceinline__ void attn_piece(const AttnPieces& p, const AttnSegment& s) {
+  if (s.begins() && s.ends()) return;
+  p.meta[blockIdx.x * 2 + (s.begins() ? 1 : 0)] =
+      AttnMeta{s.token0, s.ntok, s.h, s.pieces, s.owner, {0, 0, 0}};
+}
+
 }  // namespace engram

@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int group = warp % kGroups;                       // of rows
     const int keys_at = warp / kGroups * (16 * kGroups);    // first of this warp's keys in a tile
     uint32_t stage = 0, phase = 0;
-    AttnMeta meta{0, 0, 0, 0};
+    if (threadIdx.x == 0) attn_no_pieces(pieces);
     while (cur.next(a.plan, seg)) {
       // Rows gid and gid + 8 of the group: token row / G of the item, head h * G + row % G.
       int32_t limit[2];
@@ -390,9 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (seg.begins() && !seg.ends()) meta = AttnMeta{seg.token0, seg.ntok, seg.h, seg.pieces};
+      if (threadIdx.x == 0) attn_piece(pieces, seg);
     }
-    if (threadIdx.x == 0) pieces.meta[blockIdx.x] = meta;
   }
   __syncwarp();
   cta_sync_all();

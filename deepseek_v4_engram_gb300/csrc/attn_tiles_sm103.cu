@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float c = a.scale_log2;
     const int32_t tok = row / a.group, sub = row - tok * a.group;
     uint32_t s_phase = 0, o_phase = 0, count = 0;
-    AttnMeta meta{0, 0, 0, 0};
+    if (threadIdx.x == 0) attn_no_pieces(pieces);
     int at = 1;
     for (bool more = false, next;; more = next) {
       at ^= 1;
@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       const AttnSegment& seg = sh->seg[at ? kThreads / 32 + warp : warp];
-      if (seg.begins() && !seg.ends()) meta = AttnMeta{seg.token0, seg.ntok, seg.h, seg.pieces};
+      if (threadIdx.x == 0) attn_piece(pieces, seg);
       const bool tiles = seg.keys > 0;
       const uint32_t slot8 = count % kPoisonSlots;
       if (tiles) ++count;
@@ -484,7 +484,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     }
-    if (threadIdx.x == 0) pieces.meta[blockIdx.x] = meta;
   } else {
     set_max_regs_down<kOtherRegs>();
     const AttnSegment& seg = sh->seg[warp];
