@@ -92,11 +92,14 @@ __device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volati
 }
 
 // Finds the calling CTA's range: every thread sums a run of sequences, a scan over the CTA finds
-// the run that holds the range's first unit, and that run's thread walks it and places the
-// cursor. One pass over the lengths; all kThreads threads call it. A worker without work gets a
-// cursor that has nothing left. Worker 0 reports lengths beyond the page table.
+// the run that holds the range's first unit, that run's thread walks it, and the first warp finds
+// the place in the sequence, 32 token tiles at a time. One pass over the lengths; all kThreads
+// threads call it. A worker without work gets a cursor that has nothing left. Worker 0 reports
+// lengths beyond the page table.
 struct AttnStart {
   int64_t sums[16];   // per warp
+  int64_t pos, units, per;
+  int32_t b;
   AttnCursor cursor;
 };
 
@@ -105,13 +108,10 @@ __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worke
                                                 uint32_t* err) {
   static_assert(kThreads <= 16 * 32, "sums");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int32_t run = (p.n_seqs + kThreads - 1) / kThreads;
+  const int32_t run = p.n_seqs <= kThreads ? 1 : (p.n_seqs + kThreads - 1) / kThreads;
   const int32_t b0 = tid * run;
   const int32_t b1 = b0 + run < p.n_seqs ? b0 + run : p.n_seqs;
-  if (tid == 0) {
-    sh->cursor.left = 0;
-    sh->cursor.b = p.n_seqs;
-  }
+  if (tid == 0) sh->units = 0;
   // Pass 0 sums the run; pass 1, in the thread whose run holds the range's first unit, walks it
   // (one loop for both: the code is read from memory once per launch and SM).
   int64_t mine = 0, at = 0, u0 = -1, per = 0, total = 0;
@@ -121,9 +121,12 @@ __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worke
     if (holds) {
 #pragma unroll 1
       for (int32_t b = b0; b < b1; ++b) {
-        const int64_t u = attn_seq_units(p, attn_seq(p, b));
+        const int64_t u = pass == 1 && run == 1 ? mine : attn_seq_units(p, attn_seq(p, b));
         if (pass == 1 && u0 < at + u) {
-          sh->cursor.start(p, worker, per, b, u0 - at, total - u0 < per ? total - u0 : per);
+          sh->b = b;
+          sh->pos = u0 - at;
+          sh->units = total - u0 < per ? total - u0 : per;
+          sh->per = per;
           break;
         }
         at += u;
@@ -140,7 +143,7 @@ __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worke
     if (lane == 31) sh->sums[warp] = scan;
     __syncthreads();
     at = scan - mine;
-#pragma unroll 1
+#pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) at += sh->sums[w];
       total += sh->sums[w];
@@ -152,6 +155,32 @@ __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worke
   if (worker == 0 && p.kv_len)
     for (int32_t b = b0; b < b1; ++b)
       if (p.kv_len[b] > p.kv_cap) set_error(err, kErrCacheCapacity);
+  __syncthreads();
+  if (warp == 0) {
+    const int64_t units = sh->units;
+    if (units > 0) {
+      const AttnSeq s = attn_seq(p, sh->b);
+      int32_t lo = 0, hi = attn_items(p, s);   // the place is in token tile lo .. hi - 1
+      const int64_t head = attn_units_before(p, s, hi);
+      const int64_t pos = sh->pos;
+      const int32_t h = static_cast<int32_t>(attn_div(pos, head));
+      const int64_t in = pos - h * head;
+      int64_t begins = 0;                      // units before lo
+      while (hi - lo > 1) {
+        const int32_t step = (hi - lo + 31) / 32, k = lo + step * lane;
+        const int64_t u = lane == 0 ? begins : k < hi ? attn_units_before(p, s, k) : in + 1;
+        const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, u <= in));   // lane 0 always is
+        begins = __shfl_sync(0xFFFFFFFFu, u, last);
+        lo += step * last;
+        hi = lo + step < hi ? lo + step : hi;
+      }
+      if (lane == 0)
+        sh->cursor.start(p, worker, sh->per, sh->b, h, lo, static_cast<int32_t>(in - begins), units);
+    } else if (lane == 0) {
+      sh->cursor.left = 0;
+      sh->cursor.b = p.n_seqs;
+    }
+  }
   __syncthreads();
 }
 

@@ -152,6 +152,7 @@ struct AttnSegment {
 // units in it.
 struct AttnCursor {
   AttnSeq seq;
+  int32_t items;  // token tiles of the sequence
   int32_t b, h, rt, unit;
   int32_t worker;
   int32_t per;    // the share, cut at 2^30 (an item is far smaller)
@@ -180,9 +181,14 @@ struct AttnCursor {
     out.token0 = seq.q0 + t0;
     out.ntok = seq.n - t0 < p.tokens ? seq.n - t0 : p.tokens;
     out.first = seq.m - seq.n + t0 + 1;
-    const int32_t before = unit > p.extra ? (unit - p.extra + per - 1) / per : 0;
-    out.owner = worker - before;
-    out.pieces = before + 1 + (units - end + per - 1) / per;
+    out.owner = worker;
+    out.pieces = 1;
+    if (unit > p.extra) {
+      const int32_t before = (unit - p.extra + per - 1) / per;
+      out.owner -= before;
+      out.pieces += before;
+    }
+    if (end < units) out.pieces += (units - end + per - 1) / per;
     left -= end - unit;
     if (end == units) step(p);
     return out.tile1 > out.tile0;   // a range may end before the item's first tile
@@ -191,7 +197,7 @@ struct AttnCursor {
   // To the next item.
   __host__ __device__ void step(const AttnPlan& p) {
     unit = 0;
-    if (++rt < attn_items(p, seq)) return;
+    if (++rt < items) return;
     rt = 0;
     if (++h < p.kv_heads) return;
     h = 0;
@@ -199,27 +205,22 @@ struct AttnCursor {
       if (++b >= p.n_seqs) return;
       seq = attn_seq(p, b);
     } while (seq.n == 0);
+    items = attn_items(p, seq);
   }
 
-  // The range of worker `w` begins inside sequence b, `pos` units into it, and holds `units`.
-  __host__ __device__ void start(const AttnPlan& p, int32_t w, int64_t share, int32_t b_,
-                                 int64_t pos, int64_t units) {
+  // The range of worker `w` begins inside sequence b, in token tile `rt` of key-value head h, which
+  // begins `in` units before it, and holds `units`.
+  __host__ __device__ void start(const AttnPlan& p, int32_t w, int64_t share, int32_t b_, int32_t h_,
+                                 int32_t rt_, int32_t in, int64_t units) {
     worker = w;
     per = share < (1 << 30) ? static_cast<int32_t>(share) : 1 << 30;
     b = b_;
-    seq = attn_seq(p, b);
+    h = h_;
+    rt = rt_;
+    unit = in;
     left = units;
-    const int64_t head = attn_units_before(p, seq, attn_items(p, seq));
-    h = static_cast<int32_t>(attn_div(pos, head));
-    const int64_t in = pos - h * head;
-    int32_t lo = 0, hi = attn_items(p, seq);   // units_before(lo) <= in < units_before(hi)
-    while (hi - lo > 1) {
-      const int32_t mid = lo + (hi - lo) / 2;
-      if (attn_units_before(p, seq, mid) <= in) lo = mid;
-      else hi = mid;
-    }
-    rt = lo;
-    unit = static_cast<int32_t>(in - attn_units_before(p, seq, lo));
+    seq = attn_seq(p, b);
+    items = attn_items(p, seq);
     const int32_t all = attn_cost(p, seq, rt) + p.extra;
     if (unit > 0 && attn_whole(all, per)) {   // as the worker before has it
       if (2 * unit <= all) {

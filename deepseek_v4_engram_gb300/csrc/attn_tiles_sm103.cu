@@ -271,26 +271,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t tok = row / a.group, sub = row - tok * a.group;
     uint32_t s_phase = 0, o_phase = 0, count = 0;
     if (threadIdx.x == 0) attn_no_pieces(pieces);
-    int at = 1;
-    for (bool more = false, next;; more = next) {
-      at ^= 1;
-      next = next_segment(at ^ 1);   // one ahead, while this one's first scores are on their way
-      if (!more) {
-        if (!next) break;
-        continue;
-      }
+    int at = 0;
+    for (bool more = next_segment(0), next; more; more = next, at ^= 1) {
       const AttnSegment& seg = sh->seg[at ? kThreads / 32 + warp : warp];
       if (threadIdx.x == 0) attn_piece(pieces, seg);
       const bool tiles = seg.keys > 0;
       const uint32_t slot8 = count % kPoisonSlots;
       if (tiles) ++count;
-      if (t * kTileRows >= seg.ntok * a.group) continue;   // this row tile is empty
+      const bool empty = t * kTileRows >= seg.ntok * a.group;   // this row tile has no rows
       const bool valid = tok < seg.ntok;
       const int32_t lim = seg.first + tok;
       const int32_t limit = valid && lim > 0 ? lim : 0;
       float m = -INFINITY, l = 0.f;
-      if (tiles) {
-        for (int32_t j = seg.tile0; j < seg.tile1; ++j) {
+      for (int32_t j = seg.tile0;; ++j) {
+        if (tiles && !empty) {
           attn_wait(&sh->sfull[t], s_phase, abort, a.err);
           s_phase ^= 1u;
           tc_fence_after();
@@ -371,6 +365,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&sh->pfull[t]);
           l += sums;
         }
+        if (!tiles || empty || j + 1 == seg.tile1) {
+          next = next_segment(at ^ 1);   // while the last product runs
+          break;
+        }
+      }
+      if (empty) continue;
+      if (tiles) {
         attn_wait(&sh->ofull[t], o_phase, abort, a.err);
         o_phase ^= 1u;
         tc_fence_after();

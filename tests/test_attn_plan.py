@@ -53,7 +53,12 @@ static long check(AttnPlan p) {
     int b = p.n_seqs - 1;
     while (first[b] > u0 || attn_seq_units(p, attn_seq(p, b)) == 0) --b;
     AttnCursor c;
-    c.start(p, w, per, b, u0 - first[b], total - u0 < per ? total - u0 : per);
+    const AttnSeq at = attn_seq(p, b);
+    const int64_t head = attn_units_before(p, at, attn_items(p, at)), pos = u0 - first[b];
+    int rt = 0;
+    while (rt + 1 < attn_items(p, at) && attn_units_before(p, at, rt + 1) <= pos % head) ++rt;
+    c.start(p, w, per, b, pos / head, rt, pos % head - attn_units_before(p, at, rt),
+            total - u0 < per ? total - u0 : per);
     AttnSegment s;
     bool was_last = false;
     int n = 0;
