@@ -160,19 +160,24 @@ __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worke
     const int64_t units = sh->units;
     if (units > 0) {
       const AttnSeq s = attn_seq(p, sh->b);
-      int32_t lo = 0, hi = attn_items(p, s);   // the place is in token tile lo .. hi - 1
-      const int64_t head = attn_units_before(p, s, hi);
       const int64_t pos = sh->pos;
-      const int32_t h = static_cast<int32_t>(attn_div(pos, head));
-      const int64_t in = pos - h * head;
-      int64_t begins = 0;                      // units before lo
-      while (hi - lo > 1) {
-        const int32_t step = (hi - lo + 31) / 32, k = lo + step * lane;
-        const int64_t u = lane == 0 ? begins : k < hi ? attn_units_before(p, s, k) : in + 1;
-        const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, u <= in));   // lane 0 always is
-        begins = __shfl_sync(0xFFFFFFFFu, u, last);
-        lo += step * last;
-        hi = lo + step < hi ? lo + step : hi;
+      int32_t lo = 0, hi = attn_items(p, s), step = 0, h = 0;   // the place is in tile lo .. hi - 1
+      int64_t in = 0, begins = 0;   // units into the key-value head, and before lo
+#pragma unroll 1
+      for (int round = 0; round == 0 || hi - lo > 1; ++round) {
+        const int32_t k = round == 0 ? hi : lo + step * lane;
+        int64_t u = k <= hi ? attn_units_before(p, s, k) : in + 1;
+        if (round == 0) {           // of a whole head
+          h = static_cast<int32_t>(attn_div(pos, u));
+          in = pos - h * u;
+        } else {
+          if (lane == 0) u = begins;
+          const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, u <= in));   // lane 0 always is
+          begins = __shfl_sync(0xFFFFFFFFu, u, last);
+          lo += step * last;
+          hi = lo + step < hi ? lo + step : hi;
+        }
+        step = (hi - lo + 31) / 32;
       }
       if (lane == 0)
         sh->cursor.start(p, worker, sh->per, sh->b, h, lo, static_cast<int32_t>(in - begins), units);

@@ -97,10 +97,20 @@ __host__ __device__ inline uint64_t attn_floor_sum(uint32_t n, uint32_t a, uint3
   return sum;
 }
 
-// a / b for a >= 0, b > 0, in 32 bits where they are enough.
+// a / b for a >= 0, b > 0: in 32 bits where they are enough, else bit by bit (few instructions count
+// for more than a case that does not come up).
 __host__ __device__ inline int64_t attn_div(int64_t a, int64_t b) {
   if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
+  uint64_t q = 0, r = 0;
+  for (int i = 62; i >= 0; --i) {
+    r = r << 1 | (static_cast<uint64_t>(a) >> i & 1u);
+    q <<= 1;
+    if (r >= static_cast<uint64_t>(b)) {
+      r -= b;
+      q |= 1u;
+    }
+  }
+  return static_cast<int64_t>(q);
 }
 
 // Units of the token tiles 0 .. k-1 of one key-value head (k <= attn_items).
@@ -143,7 +153,7 @@ struct AttnSegment {
   int32_t keys;        // that the item's last token sees
   int32_t first;       // that its first token sees: token i sees first + i; none if that is <= 0
   int32_t owner;       // the worker that begins it
-  int32_t pieces;      // workers that hold a piece of it: owner, owner + 1, ...
+  int32_t pieces;      // workers that hold a piece of it: owner, owner + 1, ... (at least 1)
   __host__ __device__ bool begins() const { return tile0 == 0; }
   __host__ __device__ bool ends() const { return tile1 == cost; }
 };

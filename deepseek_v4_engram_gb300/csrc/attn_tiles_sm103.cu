@@ -40,6 +40,8 @@ constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
 constexpr int kTileRows = 128;
 constexpr int kItemRows = kAttnItemRows;   // two row tiles
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 256 * 208 + 128 * 88 = 384 * 168
+constexpr int kSegments = 4;                 // in the ring from warp 9 to the others
+constexpr int kSegmentReaders = kSoftmaxWarps + 3;
 constexpr int kPoisonSlots = 8;
 constexpr float kMostSum = 512.f;   // of a tile's probabilities against an older maximum
 constexpr int kExtraUnits = 2;
@@ -57,9 +59,9 @@ struct Shared {
   uint64_t full[Geo<DH>::kStages], empty[Geo<DH>::kStages], vok[Geo<DH>::kStages];
   uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2];
   uint64_t drain;
+  uint64_t seg_full[kSegments], seg_empty[kSegments];
+  AttnSegment seg[kSegments];
   AttnStart start;
-  AttnCursor cur[kThreads / 32];   // each warp's own
-  AttnSegment seg[kThreads / 32 + kSoftmaxWarps];   // each warp's, and the softmax warps' next
   int poison[2][kPoisonSlots];   // of warps 10 and 11, by segment
   uint32_t tmem_base;
   int abort;
@@ -137,6 +139,20 @@ __device__ __forceinline__ void tc_st_32x32b_x32(uint32_t taddr, const uint32_t 
       "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
       "r"(r[30]), "r"(r[31]), "r"(taddr)
       : "memory");
+}
+// One column: a value per lane.
+__device__ __forceinline__ uint32_t tc_ld_32x32b_x1(uint32_t taddr) {
+  uint32_t r;
+  __syncwarp();
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r)
+      : "r"(taddr)
+      : "memory");
+  return r;
+}
+__device__ __forceinline__ void tc_st_32x32b_x1(uint32_t taddr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(v) : "memory");
 }
 __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -233,6 +249,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->ofull[t], 1);
     }
     mbar_init(&sh->drain, 1);
+    for (int i = 0; i < kSegments; ++i) {
+      mbar_init(&sh->seg_full[i], 1);
+      mbar_init(&sh->seg_empty[i], kSegmentReaders);
+    }
     sh->abort = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
@@ -250,15 +270,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   volatile int* abort = &sh->abort;
-  // Every warp walks the segments for itself; one lane does, and the others read what it left.
-  AttnCursor& cur = sh->cur[warp];
-  auto next_segment = [&](int at = 0) {   // `at` 1: into the warp's second place
-    __syncwarp();
-    bool more = false;
-    if (lane == 0)  more = cur.next(a.plan, sh->seg[at ? kThreads / 32 + warp : warp]);
-    return __shfl_sync(0xFFFFFFFFu, more, 0);
+  // Warp 9 walks the worker's segments and passes them on through a ring (each role walking them for
+  // itself is more code than the instruction cache has room for); one without pieces ends them.
+  uint32_t seg_at = 0, seg_phase = 0;
+  auto next_segment = [&]() {
+    const bool ok = attn_wait(&sh->seg_full[seg_at], seg_phase, abort, a.err);
+    return !__any_sync(0xFFFFFFFFu, !ok) && sh->seg[seg_at].pieces != 0;
   };
-  if (lane == 0) cur = sh->start.cursor;
+  auto segment_done = [&]() {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh->seg_empty[seg_at]);
+    if (++seg_at == kSegments) {
+      seg_at = 0;
+      seg_phase ^= 1u;
+    }
+  };
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax and output
@@ -271,20 +297,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t tok = row / a.group, sub = row - tok * a.group;
     uint32_t s_phase = 0, o_phase = 0, count = 0;
     if (threadIdx.x == 0) attn_no_pieces(pieces);
-    int at = 0;
-    for (bool more = next_segment(0), next; more; more = next, at ^= 1) {
-      const AttnSegment& seg = sh->seg[at ? kThreads / 32 + warp : warp];
+    for (; next_segment(); segment_done()) {
+      const AttnSegment& seg = sh->seg[seg_at];
       if (threadIdx.x == 0) attn_piece(pieces, seg);
       const bool tiles = seg.keys > 0;
       const uint32_t slot8 = count % kPoisonSlots;
       if (tiles) ++count;
-      const bool empty = t * kTileRows >= seg.ntok * a.group;   // this row tile has no rows
+      if (t * kTileRows >= seg.ntok * a.group) continue;   // this row tile is empty
       const bool valid = tok < seg.ntok;
       const int32_t lim = seg.first + tok;
       const int32_t limit = valid && lim > 0 ? lim : 0;
       float m = -INFINITY, l = 0.f;
-      for (int32_t j = seg.tile0;; ++j) {
-        if (tiles && !empty) {
+      if (tiles) {
+        for (int32_t j = seg.tile0; j < seg.tile1; ++j) {
           attn_wait(&sh->sfull[t], s_phase, abort, a.err);
           s_phase ^= 1u;
           tc_fence_after();
@@ -365,13 +390,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&sh->pfull[t]);
           l += sums;
         }
-        if (!tiles || empty || j + 1 == seg.tile1) {
-          next = next_segment(at ^ 1);   // while the last product runs
-          break;
-        }
-      }
-      if (empty) continue;
-      if (tiles) {
         attn_wait(&sh->ofull[t], o_phase, abort, a.err);
         o_phase ^= 1u;
         tc_fence_after();
@@ -399,21 +417,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                   : seg.tile0 * kTileKeys;
         const int32_t k1 = limit < seg.tile1 * kTileKeys ? limit : seg.tile1 * kTileKeys;
 #pragma unroll 1
-        for (int i = 0; i < DH / 32; ++i) {
-          uint32_t o[32];
-          tc_ld_32x32b_x32(tO + i * 32, o);
-          tc_wait_ld(o);
+        for (int col = 0; col < a.head_dim; ++col) {
+          uint32_t o = tc_ld_32x32b_x1(tO + col);
+#pragma unroll 1
           for (int32_t k = k0; k < k1; ++k) {
             const uint16_t* v = value_row(a, seg, k);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              if (v == nullptr || i * 32 + e >= a.head_dim) continue;
-              const float x = to_f32<kBf16>(v[i * 32 + e]);
-              if (!(fabsf(x) < INFINITY)) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
-            }
+            const float x = v == nullptr ? 0.f : to_f32<kBf16>(v[col]);
+            if (!(fabsf(x) < INFINITY)) o = __float_as_uint(__uint_as_float(o) + x);
           }
           __syncwarp();
-          tc_st_32x32b_x32(tO + i * 32, o);
+          tc_st_32x32b_x1(tO + col, o);
         }
         tc_wait_st();
       }
@@ -487,7 +500,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     set_max_regs_down<kOtherRegs>();
-    const AttnSegment& seg = sh->seg[warp];
     if (warp == 8) {
       // ----------------------------------------------------------- MMA issuer
       constexpr uint32_t kIdS = idesc<kBf16>(128, 128, false), kIdO = idesc<kBf16>(128, DH, true);
@@ -500,10 +512,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto wait = [&](uint64_t* bar, uint32_t parity) {
         attn_wait(bar, parity, abort, a.err);
         tc_fence_after();
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (elect_one()) tc_commit(bar);
-        __syncwarp();
       };
       auto scores = [&](int t, uint32_t ks, bool done, bool last) {
         const uint32_t k_lo = kmajor_lo(kv + ks * G::kTileBytes);
@@ -519,45 +527,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      while (next_segment()) {
+      for (; next_segment(); segment_done()) {
+        const AttnSegment& seg = sh->seg[seg_at];
         if (seg.keys == 0) continue;
         const bool two = uniform(seg.ntok * a.group > kTileRows) != 0;
         const int32_t n = uniform(seg.tile1 - seg.tile0);
         const int32_t j_guard = uniform((seg.first > 0 ? seg.first : 0) / kTileKeys - seg.tile0);   // from here on: vok
-        // scores of the first tile
-        wait(&sh->full[stage], phase);
         wait(&sh->qfull, q_phase);
         q_phase ^= 1u;
-        scores(0, stage, !two, n == 1);
-        if (two) scores(1, stage, true, n == 1);
-        if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
-        for (int32_t j = 0; j < n; ++j) {
-          const uint32_t vs = stage, vph = phase;
-          if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
-          const uint32_t ks = stage, kph = phase;
+#pragma unroll 1
+        for (int32_t j = -1; j < n; ++j) {   // -1: the first tile's scores alone
+          const uint32_t vs = stage;
+          if (j >= 0) {
+            // what was requested long ago first, so that nothing else stands between P and its MMAs
+            if (j >= j_guard) {
+              wait(&sh->vok[vs], (vphase >> vs) & 1u);
+              vphase ^= 1u << vs;
+            } else {
+              wait(&sh->full[vs], phase);
+            }
+            if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+          }
+          const uint32_t ks = stage;
           const bool more = j + 1 < n;
           const uint32_t v_lo = mnmajor_lo(kv + vs * G::kTileBytes);
-          // what was requested long ago first, so that nothing else stands between P and its MMAs
-          if (j >= j_guard) {
-            wait(&sh->vok[vs], (vphase >> vs) & 1u);
-            vphase ^= 1u << vs;
-          } else {
-            wait(&sh->full[vs], vph);
-          }
           auto tile = [&](int t) {
-            wait(&sh->pfull[t], p_phase[t]);
-            p_phase[t] ^= 1u;
-            if (elect_one()) {
+            if (j >= 0) {
+              wait(&sh->pfull[t], p_phase[t]);
+              p_phase[t] ^= 1u;
+              if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < kTileKeys / 16; ++kk)
-                mma_ts(td + G::kO + t * DH, td + t * 128 + kk * 8,
-                       desc_of(v_lo + (kk * 16 * 128 >> 4)), kIdO, (j | kk) != 0);
-              if (!more) tc_commit(&sh->ofull[t]);
-              if (t == 1 || !two) tc_commit(&sh->empty[vs]);
+                for (int kk = 0; kk < kTileKeys / 16; ++kk)
+                  mma_ts(td + G::kO + t * DH, td + t * 128 + kk * 8,
+                         desc_of(v_lo + (kk * 16 * 128 >> 4)), kIdO, (j | kk) != 0);
+                if (!more) tc_commit(&sh->ofull[t]);
+                if (t == 1 || !two) tc_commit(&sh->empty[vs]);
+              }
+              __syncwarp();
             }
-            __syncwarp();
             if (more) {
-              if (t == 0) wait(&sh->full[ks], kph);
+              if (t == 0) wait(&sh->full[ks], phase);
               scores(t, ks, t == 1 || !two, j + 2 == n);
             }
           };
@@ -569,13 +578,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       // Every MMA this warp issued has finished before TMEM is released.
-      commit(&sh->drain);
+      if (elect_one()) tc_commit(&sh->drain);
+      __syncwarp();
       mbar_wait_drain(&sh->drain, 0);
     } else if (warp == 9) {
       // ----------------------------------------------------------- TMA producer
       TmaRingT<G::kStages> ring;
       bool stop = false;
-      while (!stop && next_segment()) {
+      AttnCursor cur = sh->start.cursor;
+      for (; !stop; seg_phase ^= ++seg_at == kSegments, seg_at %= kSegments) {
+        stop = __any_sync(0xFFFFFFFFu,
+                          !attn_wait(&sh->seg_empty[seg_at], seg_phase ^ 1u, abort, a.err));
+        if (stop) break;
+        AttnSegment& seg = sh->seg[seg_at];
+        if (lane == 0) {
+          if (!cur.next(a.plan, seg)) seg.pieces = 0;
+          mbar_arrive(&sh->seg_full[seg_at]);
+        }
+        __syncwarp();
+        if (seg.pieces == 0) break;
         if (seg.keys == 0) continue;
         for (int32_t j = seg.tile0; j < seg.tile1 && !stop; ++j) {
           const int32_t k0 = j * kTileKeys;
@@ -607,7 +628,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------- values nobody may see
       const int part = warp - kSoftmaxWarps - 2;   // of the rows
       uint32_t stage = 0, phase = 0, count = 0, q_phase = 0, q_loads = 0;
-      while (next_segment()) {
+      for (; next_segment(); segment_done()) {
+        const AttnSegment& seg = sh->seg[seg_at];
         if (seg.keys == 0) continue;
         const uint32_t slot8 = count++ % kPoisonSlots;
         if (part == 0) {   // the item's rows, once the MMAs have read the last ones
