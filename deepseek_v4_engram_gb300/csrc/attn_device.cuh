@@ -68,27 +68,30 @@ __device__ __forceinline__ KvPlace kv_place(const AttnArgs& a, const AttnSegment
   return {pos - col * a.page_size, page};
 }
 
-// Wait for the phase of `bar` with the given parity: mbar_wait of device.cuh with nothing but the
-// wait itself on the way of a phase that is about to complete (the clock and the abort flag are
-// only read after a number of tries). Gives up like it, after kWaitLimitNs or once another role
-// has: the roles then run to their end without waiting, and without touching memory that was
-// never filled in earnest.
-__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          uint32_t* err) {
+// Wait for the phase of `bar` with the given parity, in few instructions: it stands in many places,
+// and code that does not fit the instruction cache costs these kernels more than anything else
+// where items are short. Looks at the clock every 32 tries; gives up (false) after kWaitLimitNs or
+// once another role has: the roles then run to their end without touching memory that was never
+// filled in earnest, and the CTA reports it (attn_report).
+__device__ __forceinline__ bool attn_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
   const uint32_t at = smem_u32(bar);
-  uint64_t t0 = 0;
+  uint32_t since = 0;   // in units of 2^20 ns
+#pragma unroll 1
   for (uint32_t i = 1; !mbar_try_wait(at, parity); ++i) {
     if ((i & 31u) != 0) continue;
-    if (*abort) return false;
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitLimitNs) {
+    const uint32_t now = static_cast<uint32_t>(globaltimer_ns() >> 20) | 1u;
+    if (since == 0) since = now;
+    if (*abort != 0 || now - since > static_cast<uint32_t>(kWaitLimitNs >> 20)) {
       *abort = 1;
-      set_error(err, kErrWaitTimeout);
       return false;
     }
   }
   return true;
+}
+
+// At the end of a kernel, by one thread: whether a wait has given up.
+__device__ __forceinline__ void attn_report(volatile int* abort, uint32_t* err) {
+  if (*abort) set_error(err, kErrWaitTimeout);
 }
 
 // Finds the calling CTA's range: every thread sums a run of sequences, a scan over the CTA finds
@@ -143,7 +146,7 @@ __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worke
     if (lane == 31) sh->sums[warp] = scan;
     __syncthreads();
     at = scan - mine;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) at += sh->sums[w];
       total += sh->sums[w];
@@ -153,6 +156,7 @@ __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worke
     holds = u0 < total && at <= u0 && u0 < at + mine;
   }
   if (worker == 0 && p.kv_len)
+#pragma unroll 1
     for (int32_t b = b0; b < b1; ++b)
       if (p.kv_len[b] > p.kv_cap) set_error(err, kErrCacheCapacity);
   __syncthreads();

@@ -84,6 +84,7 @@ __host__ __device__ inline uint64_t attn_floor_sum(uint32_t n, uint32_t a, uint3
                  static_cast<uint64_t>(n) * (b / kTileKeys);
   a %= kTileKeys;
   b %= kTileKeys;
+#pragma unroll 1
   for (uint32_t y = a * n + b; y >= m && n > 0; y = a * n + b) {
     n = y / m;
     b = y % m;
@@ -102,6 +103,7 @@ __host__ __device__ inline uint64_t attn_floor_sum(uint32_t n, uint32_t a, uint3
 __host__ __device__ inline int64_t attn_div(int64_t a, int64_t b) {
   if (((a | b) >> 31) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
   uint64_t q = 0, r = 0;
+#pragma unroll 1
   for (int i = 62; i >= 0; --i) {
     r = r << 1 | (static_cast<uint64_t>(a) >> i & 1u);
     q <<= 1;
@@ -211,6 +213,7 @@ struct AttnCursor {
     rt = 0;
     if (++h < p.kv_heads) return;
     h = 0;
+#pragma unroll 1
     do {
       if (++b >= p.n_seqs) return;
       seq = attn_seq(p, b);

@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t grans = (n + a.granule - 1) / a.granule;
         KvPlace at{0, 0};
         if (gran < grans) at = kv_place(a, seg, k0 + gran * a.granule);
-        stop = __any_sync(0xFFFFFFFFu, !ring.acquire(sh->empty, abort, a.err));
+        stop = __any_sync(0xFFFFFFFFu, !attn_wait(&sh->empty[ring.stage], ring.phase ^ 1u, abort));
         if (stop) break;
         uint8_t* dst = smem + (ring.stage * 2 + (lane < 16 ? 0 : 1)) * G::kTensorBytes;
         if (lane == 0)
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       for (int32_t t = seg.tile0; t < seg.tile1 && t * kTileKeys < seg.keys; ++t) {
         const bool here = !__any_sync(
-            0xFFFFFFFFu, !attn_wait(&sh->full[stage], phase, abort, a.err));
+            0xFFFFFFFFu, !attn_wait(&sh->full[stage], phase, abort));
         const uint32_t sk = smem_u32(smem + stage * 2 * G::kTensorBytes);
         const uint32_t sv = sk + G::kTensorBytes;
 #pragma unroll 1
@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   cta_sync_all();
+  if (threadIdx.x == 0) attn_report(abort, a.err);
 }
 
 template <int DH, int kGroups, bool kBf16>

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // itself is more code than the instruction cache has room for); one without pieces ends them.
   uint32_t seg_at = 0, seg_phase = 0;
   auto next_segment = [&]() {
-    const bool ok = attn_wait(&sh->seg_full[seg_at], seg_phase, abort, a.err);
+    const bool ok = attn_wait(&sh->seg_full[seg_at], seg_phase, abort);
     return !__any_sync(0xFFFFFFFFu, !ok) && sh->seg[seg_at].pieces != 0;
   };
   auto segment_done = [&]() {
@@ -297,6 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t tok = row / a.group, sub = row - tok * a.group;
     uint32_t s_phase = 0, o_phase = 0, count = 0;
     if (threadIdx.x == 0) attn_no_pieces(pieces);
+#pragma unroll 1
     for (; next_segment(); segment_done()) {
       const AttnSegment& seg = sh->seg[seg_at];
       if (threadIdx.x == 0) attn_piece(pieces, seg);
@@ -309,8 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t limit = valid && lim > 0 ? lim : 0;
       float m = -INFINITY, l = 0.f;
       if (tiles) {
+#pragma unroll 1
         for (int32_t j = seg.tile0; j < seg.tile1; ++j) {
-          attn_wait(&sh->sfull[t], s_phase, abort, a.err);
+          attn_wait(&sh->sfull[t], s_phase, abort);
           s_phase ^= 1u;
           tc_fence_after();
           uint32_t s[4][32];
@@ -332,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // and l are scaled down to it and the exponentials taken again.
           bool fresh = j == seg.tile0;
           float sums;
+#pragma unroll 1
           for (;;) {
             if (fresh) {
               float mt[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -390,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive(&sh->pfull[t]);
           l += sums;
         }
-        attn_wait(&sh->ofull[t], o_phase, abort, a.err);
+        attn_wait(&sh->ofull[t], o_phase, abort);
         o_phase ^= 1u;
         tc_fence_after();
       }
@@ -430,49 +433,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_wait_st();
       }
-      // 64 columns at a time; 16 bytes of a row are 8 results or 4 sums
+      // 32 columns at a time; 16 bytes of a row are 8 results or 4 sums
 #pragma unroll 1
-      for (int i = 0; i < DH; i += 64) {
-        uint32_t o[2][32];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (tiles) {
-            tc_ld_32x32b_x32(tO + i + h * 32, o[h]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[h][e] = 0;
-          }
-        tc_wait_ld(o[0]);
-        tc_wait_ld(o[1]);
+      for (int i = 0; i < DH; i += 32) {
+        uint32_t o[32];
+        tc_ld_32x32b_x32(tO + i, o);
+        tc_wait_ld(o);
         if (whole) {
-          uint32_t w[2][4][4];
+          uint32_t w[4][4];
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int v = 0; v < 4; ++v)
 #pragma unroll
-            for (int v = 0; v < 4; ++v)
+            for (int e = 0; e < 4; ++e)
+              w[v][e] = tiles ? pack16x2<kBf16>(__uint_as_float(o[8 * v + 2 * e]) * inv,
+                                                __uint_as_float(o[8 * v + 2 * e + 1]) * inv)
+                              : 0u;
+          exchange4(w, own);
+          const int col = i + own * 8;
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[h][v][e] = pack16x2<kBf16>(__uint_as_float(o[h][8 * v + 2 * e]) * inv,
-                                             __uint_as_float(o[h][8 * v + 2 * e + 1]) * inv);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) exchange4(w[h], own);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int col = i + h * 32 + own * 8;
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-              if (to[v] >= 0 && col < a.head_dim)
-                *reinterpret_cast<uint4*>(a.out + to[v] + col) =
-                    make_uint4(w[h][v][0], w[h][v][1], w[h][v][2], w[h][v][3]);
-          }
+          for (int v = 0; v < 4; ++v)
+            if (to[v] >= 0 && col < a.head_dim)
+              *reinterpret_cast<uint4*>(a.out + to[v] + col) =
+                  make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
         } else {
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < 2; ++q) {
             uint32_t w[4][4];
 #pragma unroll
             for (int v = 0; v < 4; ++v)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) w[v][e] = o[0][4 * v + e];
+              for (int e = 0; e < 4; ++e) w[v][e] = o[4 * v + e];
             exchange4(w, own);
 #pragma unroll
             for (int v = 0; v < 4; ++v)
@@ -480,11 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 *reinterpret_cast<uint4*>(pieces.o + to[v] + i + q * 16 + own * 4) =
                     make_uint4(w[v][0], w[v][1], w[v][2], w[v][3]);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {   // the next 16 sums
-              o[0][e] = o[0][e + 16];
-              o[0][e + 16] = o[1][e];
-              o[1][e] = o[1][e + 16];
-            }
+            for (int e = 0; e < 16; ++e) o[e] = o[e + 16];   // the other 16 sums
           }
         }
       }
@@ -510,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t q_lo = uniform(kmajor_lo(smem_u32(sQ))), kv = uniform(smem_u32(sKV));
       // After a wait that gave up, the warp still runs to its end, on whatever shared memory holds.
       auto wait = [&](uint64_t* bar, uint32_t parity) {
-        attn_wait(bar, parity, abort, a.err);
+        attn_wait(bar, parity, abort);
         tc_fence_after();
       };
       auto scores = [&](int t, uint32_t ks, bool done, bool last) {
@@ -527,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      for (; next_segment(); segment_done()) {
+  #pragma unroll 1
+    for (; next_segment(); segment_done()) {
         const AttnSegment& seg = sh->seg[seg_at];
         if (seg.keys == 0) continue;
         const bool two = uniform(seg.ntok * a.group > kTileRows) != 0;
@@ -535,38 +522,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t j_guard = uniform((seg.first > 0 ? seg.first : 0) / kTileKeys - seg.tile0);   // from here on: vok
         wait(&sh->qfull, q_phase);
         q_phase ^= 1u;
+        wait(&sh->full[stage], phase);
+        scores(0, stage, !two, n == 1);
+        if (two) scores(1, stage, true, n == 1);
+        if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
 #pragma unroll 1
-        for (int32_t j = -1; j < n; ++j) {   // -1: the first tile's scores alone
-          const uint32_t vs = stage;
-          if (j >= 0) {
-            // what was requested long ago first, so that nothing else stands between P and its MMAs
-            if (j >= j_guard) {
-              wait(&sh->vok[vs], (vphase >> vs) & 1u);
-              vphase ^= 1u << vs;
-            } else {
-              wait(&sh->full[vs], phase);
-            }
-            if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
-          }
-          const uint32_t ks = stage;
+        for (int32_t j = 0; j < n; ++j) {
+          const uint32_t vs = stage, vph = phase;
+          if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+          const uint32_t ks = stage, kph = phase;
           const bool more = j + 1 < n;
           const uint32_t v_lo = mnmajor_lo(kv + vs * G::kTileBytes);
+          // what was requested long ago first, so that nothing else stands between P and its MMAs
+          if (j >= j_guard) {
+            wait(&sh->vok[vs], (vphase >> vs) & 1u);
+            vphase ^= 1u << vs;
+          } else {
+            wait(&sh->full[vs], vph);
+          }
           auto tile = [&](int t) {
-            if (j >= 0) {
-              wait(&sh->pfull[t], p_phase[t]);
-              p_phase[t] ^= 1u;
-              if (elect_one()) {
+            wait(&sh->pfull[t], p_phase[t]);
+            p_phase[t] ^= 1u;
+            if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kTileKeys / 16; ++kk)
-                  mma_ts(td + G::kO + t * DH, td + t * 128 + kk * 8,
-                         desc_of(v_lo + (kk * 16 * 128 >> 4)), kIdO, (j | kk) != 0);
-                if (!more) tc_commit(&sh->ofull[t]);
-                if (t == 1 || !two) tc_commit(&sh->empty[vs]);
-              }
-              __syncwarp();
+              for (int kk = 0; kk < kTileKeys / 16; ++kk)
+                mma_ts(td + G::kO + t * DH, td + t * 128 + kk * 8,
+                       desc_of(v_lo + (kk * 16 * 128 >> 4)), kIdO, (j | kk) != 0);
+              if (!more) tc_commit(&sh->ofull[t]);
+              if (t == 1 || !two) tc_commit(&sh->empty[vs]);
             }
+            __syncwarp();
             if (more) {
-              if (t == 0) wait(&sh->full[ks], phase);
+              if (t == 0) wait(&sh->full[ks], kph);
               scores(t, ks, t == 1 || !two, j + 2 == n);
             }
           };
@@ -588,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       AttnCursor cur = sh->start.cursor;
       for (; !stop; seg_phase ^= ++seg_at == kSegments, seg_at %= kSegments) {
         stop = __any_sync(0xFFFFFFFFu,
-                          !attn_wait(&sh->seg_empty[seg_at], seg_phase ^ 1u, abort, a.err));
+                          !attn_wait(&sh->seg_empty[seg_at], seg_phase ^ 1u, abort));
         if (stop) break;
         AttnSegment& seg = sh->seg[seg_at];
         if (lane == 0) {
@@ -598,14 +585,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (seg.pieces == 0) break;
         if (seg.keys == 0) continue;
+#pragma unroll 1
         for (int32_t j = seg.tile0; j < seg.tile1 && !stop; ++j) {
           const int32_t k0 = j * kTileKeys;
           const int32_t n = seg.keys - k0 < kTileKeys ? seg.keys - k0 : kTileKeys;
           const int32_t grans = (n + a.granule - 1) / a.granule;
           KvPlace at{0, 0};
           if (lane < grans) at = kv_place(a, seg, k0 + lane * a.granule);
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
-            stop = __any_sync(0xFFFFFFFFu, !ring.acquire(sh->empty, abort, a.err));
+            stop = __any_sync(0xFFFFFFFFu, !attn_wait(&sh->empty[ring.stage], ring.phase ^ 1u, abort));
             if (stop) break;
             uint8_t* dst = sKV + ring.stage * G::kTileBytes;
             if (lane == 0)
@@ -628,12 +617,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------- values nobody may see
       const int part = warp - kSoftmaxWarps - 2;   // of the rows
       uint32_t stage = 0, phase = 0, count = 0, q_phase = 0, q_loads = 0;
-      for (; next_segment(); segment_done()) {
+  #pragma unroll 1
+    for (; next_segment(); segment_done()) {
         const AttnSegment& seg = sh->seg[seg_at];
         if (seg.keys == 0) continue;
         const uint32_t slot8 = count++ % kPoisonSlots;
         if (part == 0) {   // the item's rows, once the MMAs have read the last ones
-          const bool ok = !__any_sync(0xFFFFFFFFu, !attn_wait(&sh->qempty, q_phase ^ 1u, abort, a.err));
+          const bool ok = !__any_sync(0xFFFFFFFFu, !attn_wait(&sh->qempty, q_phase ^ 1u, abort));
           q_phase ^= 1u;
           if (ok && lane == 0) {
             ++q_loads;
@@ -648,9 +638,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 0) sh->poison[part][slot8] = 0;
         __syncwarp();
+#pragma unroll 1
         for (int32_t j = seg.tile0; j < seg.tile1; ++j) {
+#pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
-            attn_wait(&sh->full[stage], phase, abort, a.err);
+            attn_wait(&sh->full[stage], phase, abort);
             __syncwarp();
             if (kv == 1 && (j + 1) * kTileKeys > seg.first) {
               // Each lane takes one 16-byte chunk column and every kStep-th row.
@@ -677,12 +669,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (any != 0) {   // rare: replace what is not finite
                 *static_cast<volatile int*>(&sh->poison[part][slot8]) = 1;
+#pragma unroll 1
                 for (r = r_first; r < r1; r += kStep) {
                   const uint4 w = lds128(at(r));
                   sts128(at(r), make_uint4(finite_only<kBf16>(w.x), finite_only<kBf16>(w.y),
                                            finite_only<kBf16>(w.z), finite_only<kBf16>(w.w)));
                 }
               }
+#pragma unroll 1
               for (r = r1 + part * (32 / kChunks) + lane / kChunks; r < kTileKeys; r += kStep)
                 sts128(at(r), make_uint4(0, 0, 0, 0));
               fence_proxy_async_shared();
@@ -701,6 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncwarp();
   cta_sync_all();   // every role is done with TMEM (each thread counted on its own)
+  if (threadIdx.x == 0) attn_report(abort, a.err);
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
