@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libengram.so")
@@ -80,8 +81,10 @@ _DESC = ctypes.POINTER(EngramDesc)
 _TAB = ctypes.POINTER(EngramTables)
 _WTS = ctypes.POINTER(EngramWeights)
 _ADESC = ctypes.POINTER(EngramAttnDesc)
-_VIEW = ctypes.POINTER(EngramAttnView)
-_CACHE = ctypes.POINTER(EngramKvCache)
+# a view or a cache is passed as a reference to its Structure or as the packed bytes of one
+_VIEW = _CACHE = ctypes.c_void_p
+PACK_VIEW = struct.Struct("Pqq")
+PACK_CACHE = struct.Struct("PP6q2iPi0P")
 
 # name -> (restype, argtypes); the same names as include/engram.h
 SIGNATURES = {

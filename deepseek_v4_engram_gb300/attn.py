@@ -13,12 +13,13 @@ import math
 import torch
 
 from . import _lib
-from ._lib import EngramAttnDesc, EngramAttnView, EngramKvCache
+from ._lib import EngramAttnDesc
 from .api import _check, lib
 
 _DTYPES = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
 _TORCH = {_lib.BF16: torch.bfloat16, _lib.F16: torch.float16}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_pack_view, _pack_cache = _lib.PACK_VIEW.pack, _lib.PACK_CACHE.pack
 
 
 def make_attn_desc(n_heads: int, n_kv_heads: int, head_dim: int, dtype=torch.bfloat16,
@@ -33,7 +34,8 @@ def make_attn_desc(n_heads: int, n_kv_heads: int, head_dim: int, dtype=torch.bfl
 
 # A decoding step's calls are shorter on the GPU than a chain of careful helpers on the host, so
 # each check below is one expression of cheap tensor attributes; what is wrong with an argument
-# that fails it is worked out only then.
+# that fails it is worked out only then. Views and caches go to the library as packed bytes, which take
+# a quarter of the time of filling a ctypes Structure and a reference to it.
 
 def _refuse(t, name: str, shape: str, dtype):
     if not isinstance(t, torch.Tensor):
@@ -51,7 +53,7 @@ def _view(t, name: str, heads: int, dim: int, dtype, tokens: int = -1):
                 tokens < 0 or shape[0] == tokens):
             s = t.stride()
             if s[2] == 1:
-                return EngramAttnView(t.data_ptr(), s[0], s[1])
+                return _pack_view(t.data_ptr(), s[0], s[1])
     n = "tokens" if tokens < 0 else tokens
     _refuse(t, name, f"[{n}, {heads}, {dim}] whose last dimension is dense", dtype)
 
@@ -83,16 +85,20 @@ def _cache(desc: EngramAttnDesc, dtype, k_cache, v_cache, block_table, n_seqs: i
             k0, k1, k2, k3 = k_cache.stride()
             v0, v1, v2, v3 = v_cache.stride()
             if k3 == 1 and v3 == 1:
-                return EngramKvCache(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2,
-                                     shape[0], shape[1], block_table.data_ptr(), table[1])
+                return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2,
+                                   shape[0], shape[1], block_table.data_ptr(), table[1])
     want = (f"[pages, page_size, {desc.n_kv_heads}, {desc.head_dim}] whose last dimension is "
             f"dense, keys and values alike, with a contiguous int32 block_table [{n_seqs}, width]")
     _refuse(k_cache, "k_cache, v_cache and block_table", want, dtype)
 
 
-def _scratch(desc: EngramAttnDesc, workspace, device):
-    """The given workspace, or a fresh one."""
+def _scratch(desc: EngramAttnDesc, workspace, device, stream):
+    """The given workspace, or a fresh one. That belongs to the call's stream: the allocator may hand
+    its memory on as soon as the call returns, to the next user in the order of that stream."""
     if workspace is None:
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return _scratch(desc, None, device, None)
         return torch.empty(engram_attn_workspace_size(desc), dtype=torch.uint8, device=device)
     if not (isinstance(workspace, torch.Tensor) and workspace.is_cuda
             and workspace.dtype is torch.uint8 and workspace.is_contiguous()):
@@ -130,17 +136,17 @@ def engram_attn_prompt(desc: EngramAttnDesc, q, k, v, cu_seqlens, out, workspace
     vv = _view(v, "v", kv_heads, dim, dtype, total)
     ov = _view(out, "out", heads, dim, dtype, total)
     cu = _ints(cu_seqlens, "cu_seqlens")
-    workspace = _scratch(desc, workspace, q.device)
+    workspace = _scratch(desc, workspace, q.device, stream)
     _check(lib().engram_attn_prompt(
-        ctypes.byref(desc), ctypes.byref(qv), ctypes.byref(kv), ctypes.byref(vv), cu,
-        _sequences(cu_seqlens), total, ctypes.byref(ov), _lse(lse_out, total, desc),
+        ctypes.byref(desc), qv, kv, vv, cu, _sequences(cu_seqlens), total, ov,
+        _lse(lse_out, total, desc),
         workspace.data_ptr(), workspace.numel(), _stream(stream, q)))
 
 
 def engram_attn_paged(desc: EngramAttnDesc, q, cu_seqlens, kv_len, block_table, k_cache, v_cache,
                       out, max_q: int, workspace=None, lse_out=None, stream=None):
     """Attention of the chunks cu_seqlens of q over the caches: kv_len (int32 [sequences]) counts
-    the chunks' own positions. `max_q` is the longest chunk."""
+    the chunks' own positions. `max_q` is the longest chunk; it picks the kernel."""
     dtype, heads, dim = _TORCH[desc.dtype], desc.n_heads, desc.head_dim
     qv = _view(q, "q", heads, dim, dtype)
     total = q.shape[0]
@@ -148,10 +154,10 @@ def engram_attn_paged(desc: EngramAttnDesc, q, cu_seqlens, kv_len, block_table, 
     cu = _ints(cu_seqlens, "cu_seqlens")
     n = _sequences(cu_seqlens)
     cache = _cache(desc, dtype, k_cache, v_cache, block_table, n)
-    workspace = _scratch(desc, workspace, q.device)
+    workspace = _scratch(desc, workspace, q.device, stream)
     _check(lib().engram_attn_paged(
-        ctypes.byref(desc), ctypes.byref(qv), cu, n, total, max_q, _ints(kv_len, "kv_len", n),
-        ctypes.byref(cache), ctypes.byref(ov), _lse(lse_out, total, desc), workspace.data_ptr(),
+        ctypes.byref(desc), qv, cu, n, total, max_q, _ints(kv_len, "kv_len", n),
+        cache, ov, _lse(lse_out, total, desc), workspace.data_ptr(),
         workspace.numel(), _stream(stream, q)))
 
 
@@ -166,5 +172,5 @@ def engram_kv_append(desc: EngramAttnDesc, k, v, cu_seqlens, kv_len, block_table
     n = _sequences(cu_seqlens)
     cache = _cache(desc, dtype, k_cache, v_cache, block_table, n)
     _check(lib().engram_kv_append(
-        ctypes.byref(desc), ctypes.byref(kv), ctypes.byref(vv), cu, n, total,
-        _ints(kv_len, "kv_len", n), ctypes.byref(cache), _stream(stream, k)))
+        ctypes.byref(desc), kv, vv, cu, n, total,
+        _ints(kv_len, "kv_len", n), cache, _stream(stream, k)))

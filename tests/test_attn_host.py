@@ -131,3 +131,10 @@ def test_oracle_against_softmax():
     assert (out[:2] == 0).all() and np.isneginf(lse[:2]).all() and np.isfinite(lse[2:]).all()
     out, lse, *_ = attend(q, k[:0], v[:0], 0.3)
     assert (out == 0).all() and np.isneginf(lse).all()
+
+
+def test_packed_arguments_are_laid_out_as_the_structures():
+    view = _lib.EngramAttnView(1 << 40, 2, 3)
+    assert bytes(view) == _lib.PACK_VIEW.pack(1 << 40, 2, 3)
+    values = [1 << 40, 2 << 40, 3, 4, 5, 6, 7, 8, 9, 10, 3 << 40, 11]
+    assert bytes(_lib.EngramKvCache(*values)) == _lib.PACK_CACHE.pack(*values)

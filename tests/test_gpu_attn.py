@@ -325,6 +325,25 @@ def test_other_streams_and_a_reused_workspace():
         assert torch.equal(out, want_out) and torch.equal(lse, want_lse)   # and the same bits each time
 
 
+def test_a_default_workspace_on_another_stream():
+    # The call waits behind work on its stream; what is allocated and written on the current one in the
+    # meantime, of the workspace's very size, must not be its workspace.
+    cache = Paged([9000, 700], 64, 2, 128, BF16, 14)
+    desc = eg.make_attn_desc(8, 2, 128, BF16)
+    want = run_paged(cache, [40, 9], 8, 128, BF16, 4)[1:]
+    size, stream = eg.engram_attn_workspace_size(desc), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(20_000_000)
+    q, cu, out = randn((49, 8, 128), 4, BF16), cu_of([40, 9]), nan_like((49, 8, 128), BF16)
+    stream.wait_stream(torch.cuda.current_stream())
+    eg.engram_attn_paged(desc, q, cu, cache.kv_len, cache.table, cache.k, cache.v, out, 40, stream=stream)
+    for _ in range(3):
+        torch.empty(size, dtype=torch.uint8, device="cuda").zero_()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want[0])
+
+
 def test_inside_a_cuda_graph():
     cache = Paged([300, 77], 16, 2, 64, BF16, 15)
     desc = eg.make_attn_desc(4, 2, 64, BF16)
