@@ -1,7 +1,9 @@
 """GB300 (sm_103a) Engram forward path of DeepSeek V4.1 behind a C ABI (libengram.so).
 
 Importing the package loads nothing; the library is loaded on the first call and must have been
-built (``python -m deepseek_v4_engram_gb300.build``). There is no CPU fallback.
+built (``python -m deepseek_v4_engram_gb300.build``). There is no CPU fallback. Beside the block's
+own stages there is the causal attention of its decoder layer: over packed prompts, over a paged cache,
+and the writing of that cache (``attn.py``).
 """
 from .api import (DeviceLayerHash, DeviceTables, DeviceWeights, EngramError, EngramGraph,  # noqa: F401,E501
                   engram_check_errors, engram_embed_rows, engram_embed_rows_shard,

@@ -3,8 +3,10 @@
 // Every worker that holds a piece of an item joins its share of the item's rows, so that an item
 // that many workers share (one long cache) is joined by as many. A row is read by 1, 2, 4 or 8
 // warps, each with kAtOnce pieces in flight at a time, so that even the most pieces (one per SM) are
-// a handful of reads one after the other; the warps' parts meet in shared memory. Always in the same
-// order. What bounds it is the latency of those reads, from L2, and the launch: 2-4 us.
+// a handful of reads one after the other; the warps' parts meet in shared memory. Always in the
+// same order. What bounds it is the latency of those reads, from L2, and the launch: 2-4 us. (With
+// an item's rows all joined by one worker, a cache of 47 k positions with one key-value head took
+// 45 us instead of 25. Joining by the last worker to arrive, without this kernel, was slower too.)
 #include "attn_device.cuh"
 #include "kernels.h"
 

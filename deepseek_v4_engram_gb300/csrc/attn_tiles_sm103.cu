@@ -6,10 +6,24 @@
 //   P_t = 2^(c S_t - c M_t)       one thread per row, in registers; M_t the row's maximum
 //   O_t = O_t + P_t V             tcgen05.mma, P_t from TMEM (it takes the place of S_t), V as it
 //                                 lies: its rows are keys, so it enters transposed (MN-major)
-// with c = scale log2(e). Bound by the tensor cores for heads of 128 columns: a tile pair costs
-// 4 * 128 * 128 * D multiply-adds there and 2 * 128 * 128 exponentials on the special-function
-// units, which are the nearer bound for heads of 64. So the two row tiles take turns: while the
+// with c = scale log2(e). Bound by the tensor cores for heads of 128 columns: a pair of row tiles
+// costs 4 * 128 * 128 * D multiply-adds there (2048 cycles an SM at D = 128) and 2 * 128 * 128
+// exponentials on the special-function units (1024). So the two row tiles take turns: while the
 // tensor cores work on one, the other's softmax runs. Both read the same key and value tiles.
+//
+// Measured (bf16, queries, keys and values in one buffer): 16384 tokens with 16 heads of 128 over
+// 4 key-value heads 661 us, 1664 TFLOP/s, 87% of a large library matrix product's rate; 8192
+// tokens 194 us (1420), with heads of 64 columns 165 us (833, near the exponentials' bound). In the
+// long prompt a pair of row tiles keeps the tensor cores for 2048 of some 2900 cycles: the rest is
+// the chain from the scores through the softmax to the product, of which two row tiles in turn hide
+// most, and TMEM has no columns for a third. Short prompts wait for instructions (2.9 stalled warps
+// per issue against 0.4 in the long prompt): a worker with a handful of items runs through most of
+// the kernel a few times only, out of caches that do not hold all of it. So loops are rolled
+// where they do not carry the inner work, and one warp walks the work for all: that took a batch of
+// 14 prompts of 0-801 tokens from 66 to 45 us.
+// Tried and slower: two threads per row (the barrier between their maxima costs what the shorter
+// rows save); scores in blocks of 64 keys, so that a row tile always has the next ones; an MMA warp
+// per row tile; P apart from S where heads of 64 columns leave room for it.
 //
 // The maximum that a row subtracts lags: it is only raised when a tile's probabilities against it
 // sum to more than kMostSum, because finding it costs a pass over the scores and raising it means
@@ -43,14 +57,20 @@ constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 256 * 208 + 128 * 88 = 3
 constexpr int kSegments = 4;                 // in the ring from warp 9 to the others
 constexpr int kSegmentReaders = kSoftmaxWarps + 3;
 constexpr int kPoisonSlots = 8;
-constexpr float kMostSum = 512.f;   // of a tile's probabilities against an older maximum
+// Of a tile's probabilities against an older maximum. With 1, where nearly every tile looks for its
+// maximum, the prompt of 16384 tokens takes 1093 us instead of 661.
+constexpr float kMostSum = 512.f;
+// An item's fixed time in key tiles: fetching its queries, filling the pipeline, writing its rows.
+// With 1, 2, 3: a prompt of 8192 tokens 210, 194, 194 us, 14 prompts of 0-801 tokens 45.8, 44.5,
+// 46.3, chunks of 1024 and 300 tokens beside six single ones 151, 133, 137.
 constexpr int kExtraUnits = 2;
 
 template <int DH>
 struct Geo {
   static constexpr int kHalves = DH / 64;
   static constexpr int kTileBytes = 128 * DH * 2;            // a tile of Q, K or V
-  static constexpr int kStages = DH == 128 ? 5 : 10;         // of one K or V tile each
+  static constexpr int kStages = DH == 128 ? 5 : 10;         // of one K or V tile each: as many
+                                                             // as fit (3 / 6 are as fast)
   static constexpr uint32_t kO = 256;                        // TMEM columns: S0 S1 O0 O1
 };
 
@@ -81,9 +101,9 @@ constexpr uint32_t idesc(int M, int N, bool b_mn) {
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// The MMA warp runs converged, with one lane predicated on: descriptors that are the same in every
-// lane then come from uniform registers. (Issued from a branch that lane 0 takes alone, each MMA
-// first moved its descriptors there, and the issue, not the tensor cores, set the pace.)
+// The MMA warp runs converged and lets one lane issue, chosen by elect.sync: descriptors that are
+// the same in every lane then come from uniform registers. (Issued from a branch that lane 0 takes
+// alone, an MMA took 70 cycles to issue, and the issue, not the tensor cores, set the pace.)
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 
 // Low and high words of a shared-memory descriptor: the low one holds the address (in 16-byte
@@ -103,7 +123,8 @@ __device__ __forceinline__ uint32_t mnmajor_lo(uint32_t saddr) {
 
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(r));
   return r != 0;
 }
 
@@ -499,27 +520,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         attn_wait(bar, parity, abort);
         tc_fence_after();
       };
+      // Scores of a key tile. `done`: for its last reader; `last`: the item's last key tile.
       auto scores = [&](int t, uint32_t ks, bool done, bool last) {
         const uint32_t k_lo = kmajor_lo(kv + ks * G::kTileBytes);
         if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk)
-          tc_mma_bf16(td + t * 128,
-                 desc_of(q_lo + ((t * kTileRows + (kk >> 2) * kItemRows) * 128 >> 4) + 2 * (kk & 3)),
-                 desc_of(k_lo + ((kk >> 2) * kTileKeys * 128 >> 4) + 2 * (kk & 3)), kIdS, kk != 0);
-        tc_commit(&sh->sfull[t]);
-        if (done) tc_commit(&sh->empty[ks]);
-        if (done && last) tc_commit(&sh->qempty);
+          for (int kk = 0; kk < DH / 16; ++kk)
+            tc_mma_bf16(td + t * 128,
+                        desc_of(q_lo + ((t * kTileRows + (kk >> 2) * kItemRows) * 128 >> 4) +
+                                2 * (kk & 3)),
+                        desc_of(k_lo + ((kk >> 2) * kTileKeys * 128 >> 4) + 2 * (kk & 3)), kIdS,
+                        kk != 0);
+          tc_commit(&sh->sfull[t]);
+          if (done) tc_commit(&sh->empty[ks]);
+          if (done && last) tc_commit(&sh->qempty);
         }
         __syncwarp();
       };
-  #pragma unroll 1
-    for (; next_segment(); segment_done()) {
+#pragma unroll 1
+      for (; next_segment(); segment_done()) {
         const AttnSegment& seg = sh->seg[seg_at];
         if (seg.keys == 0) continue;
         const bool two = uniform(seg.ntok * a.group > kTileRows) != 0;
         const int32_t n = uniform(seg.tile1 - seg.tile0);
-        const int32_t j_guard = uniform((seg.first > 0 ? seg.first : 0) / kTileKeys - seg.tile0);   // from here on: vok
+        const int32_t j_guard =   // from this tile on, warps 10-11 look at the values first
+            uniform((seg.first > 0 ? seg.first : 0) / kTileKeys - seg.tile0);
         wait(&sh->qfull, q_phase);
         q_phase ^= 1u;
         wait(&sh->full[stage], phase);
@@ -594,7 +619,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < grans) at = kv_place(a, seg, k0 + lane * a.granule);
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
-            stop = __any_sync(0xFFFFFFFFu, !attn_wait(&sh->empty[ring.stage], ring.phase ^ 1u, abort));
+            stop = __any_sync(0xFFFFFFFFu,
+                              !attn_wait(&sh->empty[ring.stage], ring.phase ^ 1u, abort));
             if (stop) break;
             uint8_t* dst = sKV + ring.stage * G::kTileBytes;
             if (lane == 0)
@@ -617,8 +643,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ----------------------------------------------------------- values nobody may see
       const int part = warp - kSoftmaxWarps - 2;   // of the rows
       uint32_t stage = 0, phase = 0, count = 0, q_phase = 0, q_loads = 0;
-  #pragma unroll 1
-    for (; next_segment(); segment_done()) {
+#pragma unroll 1
+      for (; next_segment(); segment_done()) {
         const AttnSegment& seg = sh->seg[seg_at];
         if (seg.keys == 0) continue;
         const uint32_t slot8 = count++ % kPoisonSlots;

@@ -214,9 +214,6 @@ size_t forward_min_workspace_bytes(const engram_desc_t* desc, int64_t M);
 // Sets the message engram_last_error() returns on this thread; returns `code`.
 int set_last_error(int code, const char* msg);
 
-// Device address of the current device's error word, or null with the reason in *e.
-uint32_t* device_error_word(cudaError_t* e);
-
 // Tensor maps (capi.cu; cuTensorMapEncodeTiled is fetched from the driver on first use).
 bool tensor_map_2d_bf16(void* map_out, const void* base, uint64_t inner, uint64_t rows,
                         uint32_t box_inner, uint32_t box_rows);

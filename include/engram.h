@@ -500,8 +500,9 @@ ENGRAM_API int engram_attn_prompt(const engram_attn_desc_t* desc, const engram_a
  *   kv_len int32 [n_seqs]: cache_len as engram_forward leaves it after the same tokens. A length
  *   beyond table_width * page_size is cut there and sets ENGRAM_DEVERR_CACHE_FULL; a page number
  *   outside [0, n_pages) reads as zeros and sets ENGRAM_DEVERR_PAGE_RANGE.
- *   max_q: the longest chunk, which picks the kernel (up to 16 rows of a key-value head take the
- *   one made for decoding); a longer chunk than it says is computed all the same.
+ *   max_q: the longest chunk, which picks the kernel: where max_q * n_heads / n_kv_heads, the rows
+ *   that a key-value head serves, is at most 32, the one made for decoding. A longer chunk than it
+ *   says is computed all the same, only slower.
  * Everything else as engram_attn_prompt. out must not overlap q or the cache.
  */
 ENGRAM_API int engram_attn_paged(const engram_attn_desc_t* desc, const engram_attn_view_t* q,
