@@ -12,18 +12,21 @@
 // tensor cores work on one, the other's softmax runs. Both read the same key and value tiles.
 //
 // Measured (bf16, queries, keys and values in one buffer): 16384 tokens with 16 heads of 128 over
-// 4 key-value heads 661 us, 1664 TFLOP/s, 87% of a large library matrix product's rate; 8192
-// tokens 194 us (1420), with heads of 64 columns 165 us (833, near the exponentials' bound). In the
-// long prompt a pair of row tiles keeps the tensor cores for 2048 of some 2900 cycles: the rest is
-// the chain from the scores through the softmax to the product, of which two row tiles in turn hide
-// most, and TMEM has no columns for a third. Short prompts wait for instructions (2.9 stalled warps
+// 4 key-value heads 641 us, 1715 TFLOP/s, 89% of a large library matrix product's rate; 8192
+// tokens 188 us (1465), with heads of 64 columns 161-168 us (830-855). What bounds it there, at
+// either width, is the chain from a row tile's scores through its softmax to the product and the
+// next scores, of which two row tiles in turn hide most and for a third TMEM has no columns: at
+// 8192 tokens the tensor cores are busy 67% of the time (39% at 64 columns), the special-function
+// units 34% (39%), and the schedulers issue in 38% (42%) of the cycles. Short prompts wait for instructions (2.9 stalled warps
 // per issue against 0.4 in the long prompt): a worker with a handful of items runs through most of
 // the kernel a few times only, out of caches that do not hold all of it. So loops are rolled
 // where they do not carry the inner work, and one warp walks the work for all: that took a batch of
 // 14 prompts of 0-801 tokens from 66 to 45 us.
 // Tried and slower: two threads per row (the barrier between their maxima costs what the shorter
 // rows save); scores in blocks of 64 keys, so that a row tile always has the next ones; an MMA warp
-// per row tile; P apart from S where heads of 64 columns leave room for it.
+// per row tile; P apart from S where heads of 64 columns leave room for it; loading 32 scores while
+// the exponentials of the 32 before are taken, in one piece of code with what needs all of them at
+// once (9%: the compiler then schedules 32 columns at a time instead of 128) or in two (4%).
 //
 // The maximum that a row subtracts lags: it is only raised when a tile's probabilities against it
 // sum to more than kMostSum, because finding it costs a pass over the scores and raising it means
@@ -35,7 +38,7 @@
 // per lane), warp 10 each item's queries (a box of its tokens by the heads that share its key-value
 // head is the item's rows in order, whatever their number); warps 10-11 make the values that some
 // row of the item must not see harmless (below). Registers: the softmax warps hold a row of 128
-// scores, so they take 208 each and the other four 88.
+// scores, so they take 192 each and the other four 120.
 //
 // A probability of 0 does not undo an infinity or NaN that it multiplies. In the tiles that reach
 // past what the item's first row sees, warps 10-11 clear the value rows that no row sees (another
@@ -53,12 +56,14 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
 constexpr int kTileRows = 128;
 constexpr int kItemRows = kAttnItemRows;   // two row tiles
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;   // 256 * 208 + 128 * 88 = 384 * 168
+// 256 * 192 + 128 * 120 = 384 * 168. With 176 + 152 the softmax warps spill, with 208 + 88 the others
+// do: the prompt of 16384 tokens takes 676, 641, 658 us.
+constexpr int kSoftmaxRegs = 192, kOtherRegs = 120;
 constexpr int kSegments = 4;                 // in the ring from warp 9 to the others
 constexpr int kSegmentReaders = kSoftmaxWarps + 3;
 constexpr int kPoisonSlots = 8;
 // Of a tile's probabilities against an older maximum. With 1, where nearly every tile looks for its
-// maximum, the prompt of 16384 tokens takes 1093 us instead of 661.
+// maximum, the prompt of 16384 tokens took 1093 us instead of 661.
 constexpr float kMostSum = 512.f;
 // An item's fixed time in key tiles: fetching its queries, filling the pipeline, writing its rows.
 // With 1, 2, 3: a prompt of 8192 tokens 210, 194, 194 us, 14 prompts of 0-801 tokens 45.8, 44.5,
