@@ -44,12 +44,21 @@ __global__ void __launch_bounds__(kWarps * 32)
       float2 ml[kAtOnce], v[kAtOnce][kVec / 2];
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
-        const int32_t k = i0 + i < meta.pieces ? i0 + i : i0;
+        const int32_t k = i0 + i;
+        if (k >= meta.pieces) {
+          ml[i].x = -INFINITY;
+          continue;
+        }
         const int64_t at = ((static_cast<int64_t>(meta.owner) + k) * 2 + (k == 0)) * rows + r;
         ml[i] = *reinterpret_cast<const float2*>(pieces.ml + at * 2);
         const float* o = pieces.o + at * DH + lane * kVec;
-#pragma unroll
-        for (int c = 0; c < kVec; c += 2) v[i][c / 2] = *reinterpret_cast<const float2*>(o + c);
+        if constexpr (kVec == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(o);
+          v[i][0] = make_float2(x.x, x.y);
+          v[i][1] = make_float2(x.z, x.w);
+        } else {
+          v[i][0] = *reinterpret_cast<const float2*>(o);
+        }
       }
       float top = m;
 #pragma unroll

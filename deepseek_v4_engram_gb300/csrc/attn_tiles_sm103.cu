@@ -17,11 +17,11 @@
 // either width, is the chain from a row tile's scores through its softmax to the product and the
 // next scores, of which two row tiles in turn hide most and for a third TMEM has no columns: at
 // 8192 tokens the tensor cores are busy 67% of the time (39% at 64 columns), the special-function
-// units 34% (39%), and the schedulers issue in 38% (42%) of the cycles. Short prompts wait for instructions (2.9 stalled warps
-// per issue against 0.4 in the long prompt): a worker with a handful of items runs through most of
-// the kernel a few times only, out of caches that do not hold all of it. So loops are rolled
-// where they do not carry the inner work, and one warp walks the work for all: that took a batch of
-// 14 prompts of 0-801 tokens from 66 to 45 us.
+// units 34% (39%), and the schedulers issue in 38% (42%) of the cycles. Short prompts wait for
+// instructions (2.9 stalled warps per issue against 0.3 in a long one): a worker with a handful of
+// items runs through most of the kernel a few times only, out of caches that do not hold all of
+// it. So loops are rolled where they do not carry the inner work, and one warp walks the work for
+// all: that took a batch of 14 prompts of 0-801 tokens from 66 to 45 us.
 // Tried and slower: two threads per row (the barrier between their maxima costs what the shorter
 // rows save); scores in blocks of 64 keys, so that a row tile always has the next ones; an MMA warp
 // per row tile; P apart from S where heads of 64 columns leave room for it; loading 32 scores while
