@@ -6,9 +6,9 @@
 // in one pass over the keys with a running maximum M and sum. What bounds it is the cache's bytes:
 // 32 rows make 32 multiply-adds of each key or value element, below what the tensor cores do in the
 // time that the element takes to arrive. So the work is shared out by key tiles alone
-// (attn_plan.cuh), one CTA per SM streams its tiles through a ring of three 64 KB stages (six of
-// 32 KB where heads have up to 64 columns; two are as fast), and the ring runs on across the ends of
-// items.
+// (attn_plan.cuh), one CTA per SM streams its tiles through a ring of two 64 KB stages (five of 32 KB
+// where heads have up to 64 columns; three and six are no faster), and the ring runs on across the
+// ends of items.
 //
 // Roles (288 threads): warp 8 requests the tiles by TMA, one page granule per lane; warps 0-7 each
 // take 16 rows and some of a tile's keys (with kGroups groups of rows, 16 kGroups of the 128), 16
@@ -17,10 +17,13 @@
 // step, its fragments stay in registers (scores come out in the layout in which they go back in as
 // probabilities), and a tcgen05 tile would be seven eighths padding.
 //
-// Measured (8 key-value heads of 128): one token each over 64 caches of 1584-2048 positions 83 us,
-// 5.8 TB/s, and over 4 caches of 70001-131072 positions 258 us, 6.9 TB/s, which is the memory's
-// measured rate; one token over 511 positions 10 us. What every call pays, about 10 us, is a worker's look for its range (2.3), the latency of its first page entry, page and tile, the
-// meeting of the eight warps' results (2.4) and the joining kernel (3).
+// Measured (8 key-value heads of 128): one token each over 64 caches of 1584-2048 positions 80-82 us,
+// 5.9 TB/s, and over 4 caches of 70001-131072 positions 255-263 us, 6.7-6.9 TB/s, which is the
+// memory's measured rate; one token over 511 positions 9.3 us. What every call pays, about 9 us, is a
+// worker's look for its range (2.3), the latency of its first page entry, page and tile, the eight
+// warps' results becoming one and the joining kernel (3). The warps put their results down side by
+// side and each joins a part of the rows; handing them over pairwise, in three steps with less to
+// do in each, took 0.6-1.1 us more.
 #include "attn_device.cuh"
 #include "kernels.h"
 #include "wkv_tiles.cuh"
@@ -37,8 +40,9 @@ template <int DH>
 struct Geo {
   static constexpr int kHalves = DH / 64;                          // 64-column boxes per row
   static constexpr int kTensorBytes = kTileKeys * DH * 2;          // K or V of a stage
-  static constexpr int kStages = DH == 128 ? 3 : 6;
-  static constexpr int kJoinBytes = 4 * 16 * DH * 4;               // four warps' outputs
+  static constexpr int kStages = DH == 128 ? 2 : 5;
+  static constexpr int kJoinRow = DH + 8;                          // floats: eight rows, all banks
+  static constexpr int kJoinBytes = kConsumers * 16 * kJoinRow * 4;   // every warp's outputs
 };
 
 template <int DH>
@@ -46,7 +50,7 @@ struct Shared {
   uint64_t full[Geo<DH>::kStages];
   uint64_t empty[Geo<DH>::kStages];
   AttnStart start;
-  float ml[kConsumers][16][2];
+  float2 ml[kConsumers][16];   // running maxima and sums
   int abort;
 };
 
@@ -310,89 +314,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
       }
 
-      // ---- the maxima, sums and outputs of a row group's warps become one
+      // ---- the maxima, sums and outputs of a row group's warps become one: each warp puts its own
+      // down as they are, and then takes a part of the rows
+      named_bar_sync(1, kConsumers * 32);   // the segment before has been read
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
         sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
-        if (tid == 0) {
-          sh->ml[warp][gid + 8 * i][0] = mx[i];
-          sh->ml[warp][gid + 8 * i][1] = sum[i];
-        }
+        if (tid == 0) sh->ml[warp][gid + 8 * i] = make_float2(mx[i], sum[i]);
+        float* to = join + (warp * 16 + gid + 8 * i) * G::kJoinRow + tid * 2;
+#pragma unroll
+        for (int n = 0; n < DH / 8; ++n)
+          *reinterpret_cast<float2*>(to + n * 8) = make_float2(o[n][2 * i], o[n][2 * i + 1]);
       }
       named_bar_sync(1, kConsumers * 32);
-      float m_all[2], l_all[2];
+      const bool whole = seg.begins() && seg.ends();
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg.begins() ? 1 : 0);
+      constexpr int kLanes = DH / 4;   // of a row
+      const int col = lane % kLanes * 4;
+#pragma unroll 1
+      for (int n = 0; n < kRows * kLanes / (kConsumers * 32); ++n) {
+        const int r = (n * kConsumers + warp) * (32 / kLanes) + lane / kLanes, tok = r / a.group;
+        if (tok >= seg.ntok) continue;
+        float m = -INFINITY, l = 0.f, acc[4] = {};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float m = -INFINITY;
-        for (int w = group; w < kConsumers; w += kGroups) m = fmaxf(m, sh->ml[w][gid + 8 * i][0]);
+        for (int w = 0; w < kConsumers / kGroups; ++w)
+          m = fmaxf(m, sh->ml[w * kGroups + r / 16][r % 16].x);
         const float base = m == -INFINITY ? 0.f : m;
-        float l = 0.f;
-        for (int w = group; w < kConsumers; w += kGroups)
-          l += sh->ml[w][gid + 8 * i][1] * exp2_fast(sh->ml[w][gid + 8 * i][0] - base);
-        m_all[i] = m;
-        l_all[i] = l;
-        const float f = exp2_fast(mx[i] - base);
 #pragma unroll
-        for (int n = 0; n < DH / 8; ++n) {
-          o[n][2 * i] *= f;
-          o[n][2 * i + 1] *= f;
+        for (int w = 0; w < kConsumers / kGroups; ++w) {
+          const int from = w * kGroups + r / 16;
+          const float2 ml = sh->ml[from][r % 16];
+          const float4 v = *reinterpret_cast<const float4*>(
+              join + (from * 16 + r % 16) * G::kJoinRow + col);
+          const float f = exp2_fast(ml.x - base);
+          l += f * ml.y;
+          acc[0] += f * v.x;
+          acc[1] += f * v.y;
+          acc[2] += f * v.z;
+          acc[3] += f * v.w;
         }
-      }
-      // warps 4-7 hand theirs to 0-3, then 2-3 to 0-1, then 1 to 0, as far as a row group has more
-      // than one: each lane to the same lane
-#pragma unroll
-      for (int give = 4; give >= kGroups; give >>= 1) {
-        if (warp >= give && warp < 2 * give) {
-#pragma unroll
-          for (int n = 0; n < DH / 8; ++n)
-            *reinterpret_cast<float4*>(join + (((warp - give) * (DH / 8) + n) * 32 + lane) * 4) =
-                make_float4(o[n][0], o[n][1], o[n][2], o[n][3]);
-        }
-        named_bar_sync(1, kConsumers * 32);
-        if (warp < give) {
-#pragma unroll
-          for (int n = 0; n < DH / 8; ++n) {
-            const float4 v =
-                *reinterpret_cast<const float4*>(join + ((warp * (DH / 8) + n) * 32 + lane) * 4);
-            o[n][0] += v.x;
-            o[n][1] += v.y;
-            o[n][2] += v.z;
-            o[n][3] += v.w;
-          }
-        }
-        if (give > kGroups) named_bar_sync(1, kConsumers * 32);
-      }
-      if (warp < kGroups) {
-        const bool whole = seg.begins() && seg.ends();
-        const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg.begins() ? 1 : 0);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int32_t r = group * 16 + gid + 8 * i, tok = r / a.group;
-          if (tok >= seg.ntok) continue;
+        if (whole) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
           const int32_t head = seg.h * a.group + (r - tok * a.group);
-          if (whole) {
-            const float inv = l_all[i] == 0.f ? 0.f : 1.f / l_all[i];
-            uint16_t* op = a.out + static_cast<int64_t>(seg.token0 + tok) * a.o_token +
-                           static_cast<int64_t>(head) * a.o_head;
-#pragma unroll
-            for (int n = 0; n < DH / 8; ++n)
-              if (n * 8 < a.head_dim)
-                *reinterpret_cast<uint32_t*>(op + n * 8 + tid * 2) =
-                    pack16x2<kBf16>(o[n][2 * i] * inv, o[n][2 * i + 1] * inv);
-            if (a.lse != nullptr && tid == 0)
-              a.lse[static_cast<int64_t>(seg.token0 + tok) * a.heads + head] =
-                  (m_all[i] + log2f(l_all[i])) * 0.69314718055994531f;
-          } else {
-            float* po = pieces.o + (slot * kRows + r) * DH;
-#pragma unroll
-            for (int n = 0; n < DH / 8; ++n)
-              *reinterpret_cast<float2*>(po + n * 8 + tid * 2) =
-                  make_float2(o[n][2 * i], o[n][2 * i + 1]);
-            if (tid == 0)
-              *reinterpret_cast<float2*>(pieces.ml + (slot * kRows + r) * 2) =
-                  make_float2(m_all[i], l_all[i]);
-          }
+          const int64_t token = static_cast<int64_t>(seg.token0) + tok;
+          if (col < a.head_dim)
+            *reinterpret_cast<uint2*>(a.out + token * a.o_token +
+                                      static_cast<int64_t>(head) * a.o_head + col) =
+                make_uint2(pack16x2<kBf16>(acc[0] * inv, acc[1] * inv),
+                           pack16x2<kBf16>(acc[2] * inv, acc[3] * inv));
+          if (a.lse != nullptr && col == 0)
+            a.lse[token * a.heads + head] = (m + log2f(l)) * 0.69314718055994531f;
+        } else {
+          *reinterpret_cast<float4*>(pieces.o + (slot * kRows + r) * DH + col) =
+              make_float4(acc[0], acc[1], acc[2], acc[3]);
+          if (col == 0)
+            *reinterpret_cast<float2*>(pieces.ml + (slot * kRows + r) * 2) = make_float2(m, l);
         }
       }
       if (threadIdx.x == 0) attn_piece(pieces, seg);
