@@ -101,7 +101,7 @@ __device__ __forceinline__ void attn_report(volatile int* abort, uint32_t* err) 
 // lengths beyond the page table.
 struct AttnStart {
   int64_t sums[16];   // per warp
-  int64_t pos, units, per;
+  int64_t pos, units, per, head;
   int32_t b;
   AttnCursor cursor;
 };
@@ -117,19 +117,21 @@ __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worke
   if (tid == 0) sh->units = 0;
   // Pass 0 sums the run; pass 1, in the thread whose run holds the range's first unit, walks it
   // (one loop for both: the code is read from memory once per launch and SM).
-  int64_t mine = 0, at = 0, u0 = -1, per = 0, total = 0;
+  int64_t mine = 0, at = 0, u0 = -1, per = 0, total = 0, head = 0;   // head: of a key-value head
   bool holds = true;
 #pragma unroll 1
   for (int pass = 0; pass < 2; ++pass) {
     if (holds) {
 #pragma unroll 1
       for (int32_t b = b0; b < b1; ++b) {
-        const int64_t u = pass == 1 && run == 1 ? mine : attn_seq_units(p, attn_seq(p, b));
+        if (pass == 0 || run > 1) head = attn_head_units(p, attn_seq(p, b));
+        const int64_t u = head * p.kv_heads;
         if (pass == 1 && u0 < at + u) {
           sh->b = b;
           sh->pos = u0 - at;
           sh->units = total - u0 < per ? total - u0 : per;
           sh->per = per;
+          sh->head = head;
           break;
         }
         at += u;
@@ -147,7 +149,7 @@ __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worke
     __syncthreads();
     at = scan - mine;
 #pragma unroll 1
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = 0; w < kThreads / 32 && w * 32 * run < p.n_seqs; ++w) {
       if (w < warp) at += sh->sums[w];
       total += sh->sums[w];
     }
@@ -164,24 +166,19 @@ __device__ __forceinline__ void attn_find_start(const AttnPlan& p, int32_t worke
     const int64_t units = sh->units;
     if (units > 0) {
       const AttnSeq s = attn_seq(p, sh->b);
-      const int64_t pos = sh->pos;
-      int32_t lo = 0, hi = attn_items(p, s), step = 0, h = 0;   // the place is in tile lo .. hi - 1
-      int64_t in = 0, begins = 0;   // units into the key-value head, and before lo
+      const int32_t h = static_cast<int32_t>(attn_div(sh->pos, sh->head));
+      const int64_t in = sh->pos - h * sh->head;          // units into the key-value head
+      int32_t lo = 0, hi = attn_items(p, s);              // the place is in tile lo .. hi - 1
+      int64_t begins = 0;                                 // units before lo
 #pragma unroll 1
-      for (int round = 0; round == 0 || hi - lo > 1; ++round) {
-        const int32_t k = round == 0 ? hi : lo + step * lane;
+      while (hi - lo > 1) {
+        const int32_t step = (hi - lo + 31) / 32, k = lo + step * lane;
         int64_t u = k <= hi ? attn_units_before(p, s, k) : in + 1;
-        if (round == 0) {           // of a whole head
-          h = static_cast<int32_t>(attn_div(pos, u));
-          in = pos - h * u;
-        } else {
-          if (lane == 0) u = begins;
-          const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, u <= in));   // lane 0 always is
-          begins = __shfl_sync(0xFFFFFFFFu, u, last);
-          lo += step * last;
-          hi = lo + step < hi ? lo + step : hi;
-        }
-        step = (hi - lo + 31) / 32;
+        if (lane == 0) u = begins;
+        const int last = 31 - __clz(__ballot_sync(0xFFFFFFFFu, u <= in));   // lane 0 always is
+        begins = __shfl_sync(0xFFFFFFFFu, u, last);
+        lo += step * last;
+        hi = lo + step < hi ? lo + step : hi;
       }
       if (lane == 0)
         sh->cursor.start(p, worker, sh->per, sh->b, h, lo, static_cast<int32_t>(in - begins), units);

@@ -135,8 +135,9 @@ __host__ __device__ inline int64_t attn_units_before(const AttnPlan& p, const At
                  static_cast<uint32_t>(a + (z + 1) * p.tokens + kTileKeys - 1)));
 }
 
-__host__ __device__ inline int64_t attn_seq_units(const AttnPlan& p, const AttnSeq& s) {
-  return attn_units_before(p, s, attn_items(p, s)) * p.kv_heads;
+// Units of one of the sequence's key-value heads.
+__host__ __device__ inline int64_t attn_head_units(const AttnPlan& p, const AttnSeq& s) {
+  return attn_units_before(p, s, attn_items(p, s));
 }
 
 __host__ __device__ inline int64_t attn_share(const AttnPlan& p, int64_t units) {

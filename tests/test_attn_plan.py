@@ -39,7 +39,7 @@ static long check(AttnPlan p) {
       if (attn_cost(p, s, rt) != t) ++bad;
       u += t + p.extra;
     }
-    if (attn_seq_units(p, s) != u * p.kv_heads) ++bad;
+    if (attn_head_units(p, s) != u) ++bad;
     total += u * p.kv_heads;
   }
   const int64_t per = attn_share(p, total);
@@ -51,7 +51,7 @@ static long check(AttnPlan p) {
     const int64_t u0 = per * w;
     if (u0 >= total) break;
     int b = p.n_seqs - 1;
-    while (first[b] > u0 || attn_seq_units(p, attn_seq(p, b)) == 0) --b;
+    while (first[b] > u0 || attn_head_units(p, attn_seq(p, b)) == 0) --b;
     AttnCursor c;
     const AttnSeq at = attn_seq(p, b);
     const int64_t head = attn_units_before(p, at, attn_items(p, at)), pos = u0 - first[b];
@@ -130,7 +130,7 @@ int main() {
   // a very long cache: the sums pass 32 bits
   int cu[2] = {0, 1 << 20}, kv[1] = {1 << 29};
   AttnPlan p{cu, kv, 1, 1 << 20, 1 << 29, 128, 2, 152, 3};
-  const int64_t u = attn_seq_units(p, attn_seq(p, 0));
+  const int64_t u = attn_head_units(p, attn_seq(p, 0)) * p.kv_heads;
   long double want = 0;
   for (long r = 0; r < (1 << 19); ++r)
     want += ((1L << 29) - (1L << 20) + (r + 1) * 2 + 127) / 128 * 128.0L + 3 * 128.0L;
