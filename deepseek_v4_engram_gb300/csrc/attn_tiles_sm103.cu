@@ -12,8 +12,8 @@
 // tensor cores work on one, the other's softmax runs. Both read the same key and value tiles.
 //
 // Measured (bf16, queries, keys and values in one buffer): 16384 tokens with 16 heads of 128 over
-// 4 key-value heads 641 us, 1715 TFLOP/s, 89% of a large library matrix product's rate; 8192
-// tokens 188 us (1465), with heads of 64 columns 161-168 us (830-855). What bounds it there, at
+// 4 key-value heads 640-645 us, 1705-1720 TFLOP/s, 89-90% of a large library matrix product's rate;
+// 8192 tokens 186 us (1477), with heads of 64 columns 158-160 us (860-870). What bounds it there, at
 // either width, is the chain from a row tile's scores through its softmax to the product and the
 // next scores, of which two row tiles in turn hide most and for a third TMEM has no columns: at
 // 8192 tokens the tensor cores are busy 67% of the time (39% at 64 columns), the special-function
@@ -21,7 +21,8 @@
 // instructions (2.9 stalled warps per issue against 0.3 in a long one): a worker with a handful of
 // items runs through most of the kernel a few times only, out of caches that do not hold all of
 // it. So loops are rolled where they do not carry the inner work, and one warp walks the work for
-// all: with 90 KB of code instead of 137 a batch of 14 prompts of 0-801 tokens takes 45 us, not 55.
+// all: with 90 KB of code instead of 137 a batch of 14 prompts of 0-801 tokens took 45 us, not 55.
+// It takes 43 now: 5 before the first product, 1.3 per key tile, 2.5 per item (its output 1.2-1.8).
 // Tried and slower: two threads per row (the barrier between their maxima costs what the shorter
 // rows save); scores in blocks of 64 keys, so that a row tile always has the next ones; an MMA warp
 // per row tile; P apart from S where heads of 64 columns leave room for it; loading 32 scores while
