@@ -45,8 +45,8 @@ struct AttnMeta {
 };
 struct AttnPieces {
   AttnMeta* meta;            // [workers * 2]
-  float* ml;                 // [workers * 2, rows, 2]: running maximum (of log2 scores) and sum
-  float* o;                  // [workers * 2, rows, width]: sum of 2^(x - max) v
+  float* ml;                 // [workers * 2, rows, 2]: base of the exponentials (log2) and their sum
+  float* o;                  // [workers * 2, rows, width]: sum of 2^(x - base) v
 };
 
 constexpr size_t attn_round256(size_t n) { return (n + 255) & ~size_t(255); }

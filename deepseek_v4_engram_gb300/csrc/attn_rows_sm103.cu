@@ -36,6 +36,14 @@ constexpr int kConsumers = 8;
 constexpr int kExtraUnits = 1;   // an item's fixed time, in key tiles; with 0 to 3 within 2-5%
 constexpr int kThreads = (kConsumers + 1) * 32;
 
+// Probabilities are rounded to the values' type for the product with them, but summed as they are:
+// what rounding takes from a small one is lost. bf16 has the exponents of f32; f16 ends at 2^-24, and
+// a long cache may hold much weight in keys below that. So exponentials are taken against the
+// maximum less this, and f16 reaches from 2^15 for the largest, half its range, to 2^-39 of it. Maxima
+// below are all lower by it; the quotient of outputs and sum is the same.
+template <bool kBf16>
+constexpr float kLift = kBf16 ? 0.f : 15.f;
+
 template <int DH>
 struct Geo {
   static constexpr int kHalves = DH / 64;                          // 64-column boxes per row
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float m = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-            m = fmaxf(m, mx[i]);
+            m = fmaxf(m - kLift<kBf16>, mx[i]);
             const float base = m == -INFINITY ? 0.f : m;   // nothing seen yet: every term is 0
             const float f = exp2_fast(mx[i] - base);
             mx[i] = m;

@@ -32,7 +32,8 @@
 // The maximum that a row subtracts lags: it is only raised when a tile's probabilities against it
 // sum to more than kMostSum, because finding it costs a pass over the scores and raising it means
 // rescaling O in TMEM. Probabilities are then up to 512 instead of 1, which f32 sums and both 16-bit
-// types hold as exactly, and the result is the same quotient.
+// types hold as exactly, and the result is the same quotient. f16, whose values end at 2^-24, gets
+// them another 2^6 larger (kLift), which fills its range: 2^-30 of the largest one is still there.
 //
 // Roles (384 threads): warps 0-3 and 4-7 softmax and output of row tile 0 and 1 (thread = row =
 // TMEM lane); warp 8 issues the MMAs; warp 9 requests key and value tiles by TMA (one page granule
@@ -66,6 +67,14 @@ constexpr int kPoisonSlots = 8;
 // Of a tile's probabilities against an older maximum. With 1, where nearly every tile looks for its
 // maximum, the prompt of 16384 tokens took 1093 us instead of 661.
 constexpr float kMostSum = 512.f;
+// Probabilities are rounded to the values' type for the product with them, but summed as they are:
+// what rounding takes from a small one is lost, and a long cache may hold much weight in keys that
+// f16 has no value for beside 1. So they are 2^kLift times larger there, kMostSum of it below f16's
+// largest value. bf16 has the exponents of f32.
+template <bool kBf16>
+constexpr float kLift = kBf16 ? 0.f : 6.f;
+template <bool kBf16>
+constexpr float kMostLifted = kBf16 ? kMostSum : kMostSum * 64.f;
 // An item's fixed time in key tiles: fetching its queries, filling the pipeline, writing its rows.
 // With 1, 2, 3: a prompt of 8192 tokens 210, 194, 194 us, 14 prompts of 0-801 tokens 45.8, 44.5,
 // 46.3, chunks of 1024 and 300 tokens beside six single ones 151, 133, 137.
@@ -388,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               m = top;
             }
-            const float base = m == -INFINITY ? 0.f : -m * c;
+            const float base = m == -INFINITY ? 0.f : fmaf(-m, c, kLift<kBf16>);
             const uint64_t c2 = pair(c, c), b2 = pair(base, base);
             uint64_t sum[4] = {};
 #pragma unroll
@@ -410,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float x, y;
             unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
             sums = x + y;
-            if (fresh || !__any_sync(0xFFFFFFFFu, sums > kMostSum || (m == -INFINITY && left > 0)))
+            if (fresh || !__any_sync(0xFFFFFFFFu, sums > kMostLifted<kBf16> || (m == -INFINITY && left > 0)))
               break;
             fresh = true;
           }
@@ -503,11 +512,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();   // the next product into O follows this thread's next P
       if (valid) {
+        const float base = fmaf(m, c, -kLift<kBf16>);   // of the exponentials
         if (!whole)
-          *reinterpret_cast<float2*>(pieces.ml + slot * 2) = make_float2(m * c, l);
+          *reinterpret_cast<float2*>(pieces.ml + slot * 2) = make_float2(base, l);
         else if (a.lse != nullptr)
           a.lse[static_cast<int64_t>(seg.token0 + tok) * a.heads + head] =
-              (m * c + log2f(l)) * 0.69314718055994531f;
+              (base + log2f(l)) * 0.69314718055994531f;
       }
       __syncwarp();
     }
