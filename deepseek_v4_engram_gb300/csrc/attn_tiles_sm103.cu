@@ -45,7 +45,9 @@
 // A probability of 0 does not undo an infinity or NaN that it multiplies. In the tiles that reach
 // past what the item's first row sees, warps 10-11 clear the value rows that no row sees (another
 // sequence's, or memory that was never written) and replace infinities and NaN in the others by
-// 0; if they replaced any, the rows that do see them get them added at the end.
+// 0; if they replaced any, the rows that do see them get them added at the end, each times the key's
+// probability, formed once more: where that has underflowed, the product is NaN, as in a tile that
+// every row sees.
 #include "attn_device.cuh"
 #include "kernels.h"
 #include "wkv_tiles.cuh"
@@ -247,14 +249,18 @@ __device__ __forceinline__ void exchange4(uint32_t (&w)[4][4], int own) {
     }
 }
 
-// Value row of position `pos` (for the rare rows that see an infinity or NaN).
-__device__ __forceinline__ const uint16_t* value_row(const AttnArgs& a, const AttnSegment& s,
-                                                     int32_t pos) {
-  if (a.table == nullptr) return a.v + (int64_t(s.q0) + pos) * a.v_token + s.h * a.v_head;
+// Key row (`values` false) or value row of position `pos`, for the rare rows that see an infinity or
+// NaN; null: the position's page number is not the cache's, its row reads as zeros.
+__device__ __forceinline__ const uint16_t* kv_row(const AttnArgs& a, const AttnSegment& s,
+                                                  bool values, int32_t pos) {
+  const uint16_t* p = values ? a.v : a.k;
+  const int64_t token = values ? a.v_token : a.k_token, head = values ? a.v_head : a.k_head;
+  if (a.table == nullptr) return p + (int64_t(s.q0) + pos) * token + s.h * head;
   const int32_t col = pos / a.page_size;
   const int32_t page = a.table[int64_t(s.b) * a.table_width + col];
-  if (page < 0 || page >= a.n_pages) return nullptr;   // read as zeros
-  return a.v + page * a.v_page + (pos - int64_t(col) * a.page_size) * a.v_token + s.h * a.v_head;
+  if (page < 0 || page >= a.n_pages) return nullptr;
+  return p + page * (values ? a.v_page : a.k_page) + (pos - int64_t(col) * a.page_size) * token +
+         s.h * head;
 }
 
 template <int DH, bool kBf16>
@@ -455,14 +461,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t k0 = seg.first > seg.tile0 * kTileKeys ? seg.first
                                                                   : seg.tile0 * kTileKeys;
         const int32_t k1 = limit < seg.tile1 * kTileKeys ? limit : seg.tile1 * kTileKeys;
+        const float base = m == -INFINITY ? 0.f : fmaf(-m, c, kLift<kBf16>);
+        const uint16_t* q = a.q + static_cast<int64_t>(seg.token0 + tok) * a.q_token +
+                            static_cast<int64_t>(head) * a.q_head;
 #pragma unroll 1
         for (int col = 0; col < a.head_dim; ++col) {
           uint32_t o = tc_ld_32x32b_x1(tO + col);
 #pragma unroll 1
           for (int32_t k = k0; k < k1; ++k) {
-            const uint16_t* v = value_row(a, seg, k);
+            const uint16_t* v = kv_row(a, seg, true, k);
             const float x = v == nullptr ? 0.f : to_f32<kBf16>(v[col]);
-            if (!(fabsf(x) < INFINITY)) o = __float_as_uint(__uint_as_float(o) + x);
+            if (fabsf(x) < INFINITY) continue;
+            // times the key's probability, which may be 0 for all that
+            const uint16_t* key = kv_row(a, seg, false, k);
+            float s = 0.f;
+#pragma unroll 1
+            for (int d = 0; d < a.head_dim; ++d)
+              s += to_f32<kBf16>(q[d]) * (key == nullptr ? 0.f : to_f32<kBf16>(key[d]));
+            const uint32_t p = pack16x2<kBf16>(exp2_fast(fmaf(s, c, base)), 0.f);
+            o = __float_as_uint(__uint_as_float(o) + to_f32<kBf16>(static_cast<uint16_t>(p)) * x);
           }
           __syncwarp();
           tc_st_32x32b_x1(tO + col, o);

@@ -479,7 +479,8 @@ ENGRAM_API size_t engram_attn_workspace_size(const engram_attn_desc_t* desc);
  *   out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j, h']) v[j, h'],  lse = ln sum_j exp(scale ...).
  * Scores, maxima and sums in f32, probabilities rounded to dtype for the product with the values,
  * one rounding of the result. Keys and values that a token does not see do not reach its row,
- * whatever they hold (infinities and NaN too).
+ * whatever they hold (infinities and NaN too); an infinite value that it sees counts with the
+ * rounded probability, as NaN where that is 0.
  *   q, out [total, n_heads, head_dim]; k, v [total, n_kv_heads, head_dim]; cu_seqlens int32
  *   [n_seqs + 1] (device); lse f32 [total, n_heads] or NULL. Tokens of no sequence are not
  *   written. cu_seqlens is clamped to [0, total]. total < 2^24.
