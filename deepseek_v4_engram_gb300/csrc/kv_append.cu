@@ -35,7 +35,8 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
     }
     const int32_t end = attn_clamp(a.cu[lo + 1], 0, a.total);
     if (t < a.cu[lo] || t >= end) continue;   // a token of no sequence
-    const int32_t p = a.kv_len[lo] - (end - t);
+    const int32_t len = a.kv_len[lo];
+    const int32_t p = (len > 0 ? len : 0) - (end - t);   // a negative length is an empty cache
     if (p < 0) continue;   // before the cache's first position: such a token is not kept
     const int32_t col = p / a.page_size;
     if (col >= a.table_width) {

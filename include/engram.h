@@ -498,9 +498,10 @@ ENGRAM_API int engram_attn_prompt(const engram_attn_desc_t* desc, const engram_a
  * holds kv_len[b] positions, the chunk's own among them (engram_kv_append writes them first), and
  * chunk token t sees the positions 0 .. kv_len[b] - n + t. A row that sees nothing (kv_len[b] < n,
  * an empty cache) is written as zeros, with lse -infinity.
- *   kv_len int32 [n_seqs]: cache_len as engram_forward leaves it after the same tokens. A length
- *   beyond table_width * page_size is cut there and sets ENGRAM_DEVERR_CACHE_FULL; a page number
- *   outside [0, n_pages) reads as zeros and sets ENGRAM_DEVERR_PAGE_RANGE.
+ *   kv_len int32 [n_seqs]: cache_len as engram_forward leaves it after the same tokens. A negative
+ *   length counts as 0; one beyond table_width * page_size is cut there and sets
+ *   ENGRAM_DEVERR_CACHE_FULL; a page number outside [0, n_pages) reads as zeros and sets
+ *   ENGRAM_DEVERR_PAGE_RANGE.
  *   max_q: the longest chunk, which picks the kernel: where max_q * n_heads / n_kv_heads, the rows
  *   that a key-value head serves, is at most 32, the one made for decoding. A longer chunk than it
  *   says is computed all the same, only slower.
@@ -516,7 +517,7 @@ ENGRAM_API int engram_attn_paged(const engram_attn_desc_t* desc, const engram_at
 /*
  * Writes the keys and values [total, n_kv_heads, head_dim] of a chunk per sequence (cu_seqlens as
  * in engram_attn_paged) into a paged cache: token t of n goes to position kv_len[b] - n + t, where
- * kv_len already counts the chunk. A position before 0 is not kept; one beyond the block table is
+ * kv_len already counts the chunk (negative: 0). A position before 0 is not kept; one beyond the block table is
  * not written and sets ENGRAM_DEVERR_CACHE_FULL; nor is one whose page number is outside
  * [0, n_pages), which sets ENGRAM_DEVERR_PAGE_RANGE. Slots of the same page given to two
  * sequences are written by both, in no order.
