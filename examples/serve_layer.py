@@ -49,6 +49,7 @@ class Layer:
         # the block's look-back cache
         self.ids = torch.zeros((batch, capacity), dtype=torch.int32, device="cuda")
         self.length = torch.zeros(batch, dtype=torch.int32, device="cuda")
+        self.started = False    # whether the caches hold anything
         # pages of the attention's cache, dealt to the sequences in turn
         per_seq = -(-capacity // page)
         shape = (batch * per_seq, page, kv_heads, head_dim)
@@ -59,10 +60,11 @@ class Layer:
         self.scratch = torch.empty(eg.engram_attn_workspace_size(self.attn), dtype=torch.uint8, device="cuda")
 
     def step(self, x, tokens):
-        """x bf16 [B, T, hc, dim] and the T new tokens of each sequence: returns the block's streams
-        [B, T, hc, dim] and the queries, keys, values and attention outputs [B * T, heads, head_dim]."""
+        """x bf16 [B, T, hc, dim] and the T new tokens of each sequence (a prompt first, then any number at
+        a time): returns the block's streams [B, T, hc, dim] and the queries, keys, values and attention
+        outputs [B * T, heads, head_dim]."""
         B, T = tokens.shape
-        first = T > 1           # a prompt: its keys are all in hand, the cache is only filled
+        first, self.started = not self.started, True    # a prompt's keys are all in hand: the cache is only filled
         streams = torch.empty_like(x)
         work = torch.empty(max(eg.engram_forward_workspace_size(self.desc, B * T), 256), dtype=torch.uint8,
                            device="cuda")
