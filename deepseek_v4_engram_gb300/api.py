@@ -1,7 +1,8 @@
 """Thin Python binding of libengram.so: the entry points of include/engram.h under the same names.
 
-Argument marshalling only. Tensors must be CUDA tensors, contiguous, of the element size the C
-ABI expects (bf16 may be passed as torch.bfloat16 or as int16/uint16 bits). Every computation
+Argument marshalling only. Tensors must be CUDA tensors on the current device (where the library
+launches), contiguous, of the element size the C ABI expects (bf16 may be passed as torch.bfloat16
+or as int16/uint16 bits). Every computation
 runs in the library's kernels; if the library is missing, the first call raises.
 """
 from __future__ import annotations
@@ -30,6 +31,7 @@ def _check(rc: int) -> None:
         raise EngramError(rc, lib().engram_last_error().decode())
 
 
+_current_device = torch._C._cuda_getDevice
 _ITEMSIZE = {"bf16": 2, "u8": 1, "i32": 4, "u64": 8, "i64": 8, "f32": 4}
 
 
@@ -38,8 +40,12 @@ def _ptr(t: torch.Tensor | None, kind: str, name: str):
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
-    if not t.is_cuda:
+    device = t.get_device()
+    if device < 0:
         raise ValueError(f"{name}: must be a CUDA tensor (the library takes device pointers)")
+    if device != _current_device():
+        raise ValueError(f"{name}: on cuda:{device}, but the current device, where the library "
+                         f"launches, is cuda:{_current_device()}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     if t.element_size() != _ITEMSIZE[kind]:
@@ -50,6 +56,9 @@ def _ptr(t: torch.Tensor | None, kind: str, name: str):
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
         stream = torch.cuda.current_stream()
+    elif stream.device_index != _current_device():
+        raise ValueError(f"stream: on cuda:{stream.device_index}, but the current device, where "
+                         f"the library launches, is cuda:{_current_device()}")
     return ctypes.c_void_p(stream.cuda_stream)
 
 
