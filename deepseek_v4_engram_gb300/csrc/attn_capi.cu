@@ -6,6 +6,7 @@
 #include "attn.h"
 #include "engram.h"
 #include "kernels.h"
+#include "strided.h"
 
 namespace engram {
 
@@ -41,8 +42,11 @@ int check_desc(const engram_attn_desc_t* d) {
   return ENGRAM_OK;
 }
 
+// Tensor maps take strides below 2^40 bytes; a tensor that reaches further than an address does not
+// exist, and would overflow the sums of strided.h.
 bool good_stride(int64_t n, int64_t stride) {
-  return n <= 1 || (stride > 0 && stride % 8 == 0 && stride < (int64_t(1) << 38));
+  return n <= 1 || (stride > 0 && stride % 8 == 0 && stride < (int64_t(1) << 38) &&
+                    stride <= (int64_t(1) << 56) / (n - 1));
 }
 
 int check_view(const engram_attn_view_t* t, const char* name, int32_t tokens, int32_t heads) {
@@ -82,38 +86,51 @@ int check_cache(const engram_attn_desc_t* d, const engram_kv_cache_t* c, const i
   return ENGRAM_OK;
 }
 
-// The bytes from the first to the last element of a [n0, n1, n2, dim] tensor, for overlap checks.
-struct Extent {
-  uintptr_t lo, hi;
-  Extent(const void* p, int32_t dim, int64_t n0, int64_t s0, int64_t n1, int64_t s1,
-         int64_t n2 = 1, int64_t s2 = 0)
-      : lo(reinterpret_cast<uintptr_t>(p)),
-        hi(lo + 2 * ((n0 - 1) * (n0 > 1 ? s0 : 0) + (n1 - 1) * (n1 > 1 ? s1 : 0) +
-                     (n2 - 1) * (n2 > 1 ? s2 : 0) + dim)) {}
+Strided strided(const engram_attn_view_t* t, int32_t tokens, int32_t heads, int32_t dim) {
+  return Strided(t->ptr, int64_t(dim) * 2, tokens, t->token_stride * 2, heads, t->head_stride * 2);
+}
+
+Strided strided_keys(const engram_attn_desc_t* d, const engram_kv_cache_t* c) {
+  return Strided(c->k, int64_t(d->head_dim) * 2, c->n_pages, c->k_page_stride * 2, c->page_size,
+                 c->k_slot_stride * 2, d->n_kv_heads, c->k_head_stride * 2);
+}
+Strided strided_values(const engram_attn_desc_t* d, const engram_kv_cache_t* c) {
+  return Strided(c->v, int64_t(d->head_dim) * 2, c->n_pages, c->v_page_stride * 2, c->page_size,
+                 c->v_slot_stride * 2, d->n_kv_heads, c->v_head_stride * 2);
+}
+
+// What a call reads and writes, by name. Parts of one buffer may interleave (a projection's q, k and v,
+// and an output beside them); what is written may share no byte with anything else, nor two rows of it
+// with each other.
+struct Operand {
+  const char* name;
+  Strided at;
 };
 
-// Views into one buffer interleave (a projection's q, k and v parts), and `out` may be such a part
-// too, so extents that overlap are an error only where both start in the same columns of the same
-// rows; here: where they are the same pointer, or where one of them is dense.
-bool same_rows(const Extent& a, const Extent& b) { return a.lo < b.hi && b.lo < a.hi; }
-
-bool dense(const engram_attn_view_t* t, int32_t tokens, int32_t heads, int32_t dim) {
-  return (heads == 1 || t->head_stride == dim) &&
-         (tokens == 1 || t->token_stride == int64_t(heads) * dim);
-}
-
-Extent extent(const engram_attn_view_t* t, int32_t tokens, int32_t heads, int32_t dim) {
-  return Extent(t->ptr, dim, tokens, t->token_stride, heads, t->head_stride);
-}
-
-int check_out(const engram_attn_desc_t* d, const engram_attn_view_t* out,
-              const engram_attn_view_t* in, const char* name, int32_t total, int32_t heads) {
-  if (out->ptr == in->ptr ||
-      ((dense(out, total, d->n_heads, d->head_dim) || dense(in, total, heads, d->head_dim)) &&
-       same_rows(extent(out, total, d->n_heads, d->head_dim),
-                 extent(in, total, heads, d->head_dim))))
-    return fail(ENGRAM_EINVAL, "out overlaps %s", name);
+int check_overlap(const Operand* written, int n_written, const Operand* read, int n_read) {
+  for (int i = 0; i < n_written; ++i) {
+    const Operand& w = written[i];
+    for (int j = 0; j < n_read; ++j)
+      if (shares_memory(w.at, read[j].at))
+        return fail(ENGRAM_EINVAL, "%s overlaps %s", w.name, read[j].name);
+    for (int j = 0; j < i; ++j)
+      if (shares_memory(w.at, written[j].at))
+        return fail(ENGRAM_EINVAL, "%s overlaps %s", w.name, written[j].name);
+    if (rows_share_memory(w.at))
+      return fail(ENGRAM_EINVAL, "%s: its rows overlap each other", w.name);
+  }
   return ENGRAM_OK;
+}
+
+// out, the workspace and lse (of no width where it is NULL) against `read`.
+template <int N>
+int check_written(const engram_attn_desc_t* d, const engram_attn_view_t* out, int32_t total,
+                  const float* lse, const void* workspace, const Operand (&read)[N]) {
+  const Operand written[] = {
+      {"out", strided(out, total, d->n_heads, d->head_dim)},
+      {"workspace", Strided(workspace, static_cast<int64_t>(engram_attn_workspace_size(d)))},
+      {"lse", Strided(lse, lse ? int64_t(total) * d->n_heads * 4 : 0)}};
+  return check_overlap(written, 3, read, N);
 }
 
 int check_workspace(const engram_attn_desc_t* d, void* ws, size_t bytes, const float* lse) {
@@ -190,11 +207,13 @@ ENGRAM_API int engram_attn_prompt(const engram_attn_desc_t* desc, const engram_a
       (rc = check_view(k, "k", total, desc->n_kv_heads)) != 0 ||
       (rc = check_view(v, "v", total, desc->n_kv_heads)) != 0 ||
       (rc = check_view(out, "out", total, desc->n_heads)) != 0 ||
-      (rc = check_out(desc, out, q, "q", total, desc->n_heads)) != 0 ||
-      (rc = check_out(desc, out, k, "k", total, desc->n_kv_heads)) != 0 ||
-      (rc = check_out(desc, out, v, "v", total, desc->n_kv_heads)) != 0 ||
       (rc = check_workspace(desc, workspace, workspace_bytes, lse)) != 0)
     return rc;
+  const Operand read[] = {{"q", strided(q, total, desc->n_heads, desc->head_dim)},
+                          {"k", strided(k, total, desc->n_kv_heads, desc->head_dim)},
+                          {"v", strided(v, total, desc->n_kv_heads, desc->head_dim)},
+                          {"cu_seqlens", Strided(cu_seqlens, (int64_t(n_seqs) + 1) * 4)}};
+  if ((rc = check_written(desc, out, total, lse, workspace, read)) != 0) return rc;
   cudaError_t e;
   uint32_t* err = device_error_word(&e);
   if (!err) return report(e, "engram_attn_prompt");
@@ -224,17 +243,16 @@ ENGRAM_API int engram_attn_paged(const engram_attn_desc_t* desc, const engram_at
   if ((rc = check_view(q, "q", total, desc->n_heads)) != 0 ||
       (rc = check_view(out, "out", total, desc->n_heads)) != 0 ||
       (rc = check_cache(desc, cache, kv_len)) != 0 ||
-      (rc = check_out(desc, out, q, "q", total, desc->n_heads)) != 0 ||
       (rc = check_workspace(desc, workspace, workspace_bytes, lse)) != 0)
     return rc;
-  const Extent o = extent(out, total, desc->n_heads, desc->head_dim);
-  if (same_rows(o, Extent(cache->k, desc->head_dim, cache->n_pages, cache->k_page_stride,
-                          cache->page_size, cache->k_slot_stride, desc->n_kv_heads,
-                          cache->k_head_stride)) ||
-      same_rows(o, Extent(cache->v, desc->head_dim, cache->n_pages, cache->v_page_stride,
-                          cache->page_size, cache->v_slot_stride, desc->n_kv_heads,
-                          cache->v_head_stride)))
-    return fail(ENGRAM_EINVAL, "out overlaps the cache");
+  const Operand read[] = {
+      {"q", strided(q, total, desc->n_heads, desc->head_dim)},
+      {"the cache", strided_keys(desc, cache)},
+      {"the cache", strided_values(desc, cache)},
+      {"cu_seqlens", Strided(cu_seqlens, (int64_t(n_seqs) + 1) * 4)},
+      {"kv_len", Strided(kv_len, int64_t(n_seqs) * 4)},
+      {"block_table", Strided(cache->block_table, int64_t(n_seqs) * cache->table_width * 4)}};
+  if ((rc = check_written(desc, out, total, lse, workspace, read)) != 0) return rc;
   cudaError_t e;
   uint32_t* err = device_error_word(&e);
   if (!err) return report(e, "engram_attn_paged");

@@ -484,7 +484,9 @@ ENGRAM_API size_t engram_attn_workspace_size(const engram_attn_desc_t* desc);
  *   q, out [total, n_heads, head_dim]; k, v [total, n_kv_heads, head_dim]; cu_seqlens int32
  *   [n_seqs + 1] (device); lse f32 [total, n_heads] or NULL. Tokens of no sequence are not
  *   written. cu_seqlens is clamped to [0, total]. total < 2^24.
- * total = 0 or n_seqs = 0 launches nothing. out must not overlap q, k or v.
+ * total = 0 or n_seqs = 0 launches nothing. out, lse and workspace may not share a byte with any
+ * other argument, nor two rows of out with each other (ENGRAM_EINVAL); parts of one buffer that lie
+ * between each other's rows are fine.
  */
 ENGRAM_API int engram_attn_prompt(const engram_attn_desc_t* desc, const engram_attn_view_t* q,
                                   const engram_attn_view_t* k, const engram_attn_view_t* v,
@@ -505,7 +507,7 @@ ENGRAM_API int engram_attn_prompt(const engram_attn_desc_t* desc, const engram_a
  *   max_q: the longest chunk, which picks the kernel: where max_q * n_heads / n_kv_heads, the rows
  *   that a key-value head serves, is at most 32, the one made for decoding. A longer chunk than it
  *   says is computed all the same, only slower.
- * Everything else as engram_attn_prompt. out must not overlap q or the cache.
+ * Everything else as engram_attn_prompt.
  */
 ENGRAM_API int engram_attn_paged(const engram_attn_desc_t* desc, const engram_attn_view_t* q,
                                  const int32_t* cu_seqlens, int32_t n_seqs, int32_t total,
@@ -517,9 +519,9 @@ ENGRAM_API int engram_attn_paged(const engram_attn_desc_t* desc, const engram_at
 /*
  * Writes the keys and values [total, n_kv_heads, head_dim] of a chunk per sequence (cu_seqlens as
  * in engram_attn_paged) into a paged cache: token t of n goes to position kv_len[b] - n + t, where
- * kv_len already counts the chunk (negative: 0). A position before 0 is not kept; one beyond the block table is
- * not written and sets ENGRAM_DEVERR_CACHE_FULL; nor is one whose page number is outside
- * [0, n_pages), which sets ENGRAM_DEVERR_PAGE_RANGE. Slots of the same page given to two
+ * kv_len already counts the chunk (negative: 0). A position before 0 is not kept; one beyond the
+ * block table is not written and sets ENGRAM_DEVERR_CACHE_FULL; nor is one whose page number is
+ * outside [0, n_pages), which sets ENGRAM_DEVERR_PAGE_RANGE. Slots of the same page given to two
  * sequences are written by both, in no order.
  */
 ENGRAM_API int engram_kv_append(const engram_attn_desc_t* desc, const engram_attn_view_t* k,
