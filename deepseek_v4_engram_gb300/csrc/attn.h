@@ -99,9 +99,6 @@ struct KvAppendArgs {
 };
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t st);
 
-// In the device error word, beside the bits of device.cuh: a page number outside the paged cache.
-constexpr uint32_t kErrPageRange = 16u;
-
 // Device address of the current device's error word (capi.cu), or null with the reason in *e.
 uint32_t* device_error_word(cudaError_t* e);
 

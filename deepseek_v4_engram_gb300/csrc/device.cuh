@@ -15,6 +15,7 @@ enum : uint32_t {
   kErrCacheCapacity = 2u,  // a sequence's cache would grow past its capacity
   kErrIdRange = 4u,        // a hash id outside [0, num_embeddings)
   kErrWaitTimeout = 8u,    // a bounded wait inside a kernel gave up
+  kErrPageRange = 16u,     // a page number outside the paged cache
 };
 
 // A bounded wait gives up after this long (ns, %globaltimer): far beyond any legitimate wait.
