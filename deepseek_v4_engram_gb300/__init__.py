@@ -2,8 +2,8 @@
 
 Importing the package loads nothing; the library is loaded on the first call and must have been
 built (``python -m deepseek_v4_engram_gb300.build``). There is no CPU fallback. Beside the block's
-own stages there is the causal attention of its decoder layer: over packed prompts, over a paged cache,
-and the writing of that cache (``attn.py``).
+own stages there is grouped-head causal attention over packed prompts and over a paged cache, and the
+writing of that cache (``attn.py``).
 """
 from .api import (DeviceLayerHash, DeviceTables, DeviceWeights, EngramError, EngramGraph,  # noqa: F401,E501
                   engram_check_errors, engram_embed_rows, engram_embed_rows_shard,

@@ -72,8 +72,9 @@ constexpr int32_t attn_width(int32_t head_dim) { return head_dim <= 64 ? 64 : 12
 
 // Items of up to kAttnFewRows rows (attn_rows_sm103.cu): decoding and short chunks. `rows`: of the
 // longest chunk, at least the heads that share a key-value head. Over 16 caches of 3000-4665
-// positions, 4 key-value heads of 128: 16 rows 34.1 us, 24 rows 37.6 us (on tcgen05 39.0), 32 rows
-// 37.9 us (38.9); 40 rows take 38 us on tcgen05 and took 49.5 in a form for 64 rows made like these.
+// positions in pages of 48, 4 key-value heads of 128: 8 rows 32.0 us, 24 rows 36.3 us (on tcgen05
+// 39.0), 32 rows 37.2 us (38.9); 40 rows take 38.5 us on tcgen05 and took 49.5 in a form for 64 rows
+// made like these.
 constexpr int32_t kAttnFewRows = 32;
 cudaError_t launch_attn_rows(const AttnArgs& a, int32_t rows, cudaStream_t st);
 

@@ -15,8 +15,8 @@
 // every worker evaluates it for itself from the lengths in device memory. An item that a boundary
 // cuts is computed in pieces, each with its own running maximum and sum, that are joined afterwards
 // (attn_combine.cu), always in the same order. Where an item is small beside a worker's share, the
-// boundary moves to the item's nearer end instead: up to a quarter of a share of imbalance costs
-// less than the pieces' way through memory.
+// boundary moves to the item's nearer end instead: up to a quarter of a share at either end of a
+// worker's range costs less than the pieces' way through memory.
 //
 // A worker holds at most two pieces: one of an item that an earlier worker began (its first
 // segment), and one of an item that it begins and a later worker finishes (its last segment).

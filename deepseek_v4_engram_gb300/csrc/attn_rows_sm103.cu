@@ -18,10 +18,12 @@
 // probabilities), and a tcgen05 tile would be seven eighths padding.
 //
 // Measured (8 key-value heads of 128): one token each over 64 caches of 1584-2048 positions 80-82 us,
-// 5.9 TB/s, and over 4 caches of 70001-131072 positions 255-263 us, 6.7-6.9 TB/s, which is the
-// memory's measured rate; one token over 511 positions 9.3 us. What every call pays, about 9 us, is a
-// worker's look for its range (2.3), the latency of its first page entry, page and tile, the eight
-// warps' results becoming one and the joining kernel (3). The warps put their results down side by
+// 5.9 TB/s (a kernel that only reads as many bytes takes 74.5), and over 4 caches of 70001-131072
+// positions 256-263 us, 6.7-6.9 TB/s (260); one token over 511 positions 8.9-9.9 us. What every call
+// pays, about 9 us, is a worker's look for its range (2.3), the latency of its first page entry, page
+// and tile (3.4), the eight warps' results becoming one (1.1) and the joining kernel (3). A tile takes
+// 1.3 us with 16 rows (memory's rate; 1.56 where pages of 48 slots make copies of 16 keys) and 1.65 with
+// 32, where a warp has twice the keys and its own chain sets the pace. The warps put their results down side by
 // side and each joins a part of the rows; handing them over pairwise, in three steps with less to
 // do in each, took 0.6-1.1 us more.
 #include "attn_device.cuh"
@@ -36,11 +38,12 @@ constexpr int kConsumers = 8;
 constexpr int kExtraUnits = 1;   // an item's fixed time, in key tiles; with 0 to 3 within 2-5%
 constexpr int kThreads = (kConsumers + 1) * 32;
 
-// Probabilities are rounded to the values' type for the product with them, but summed as they are:
-// what rounding takes from a small one is lost. bf16 has the exponents of f32; f16 ends at 2^-24, and
-// a long cache may hold much weight in keys below that. So exponentials are taken against the
-// maximum less this, and f16 reaches from 2^15 for the largest, half its range, to 2^-39 of it. Maxima
-// below are all lower by it; the quotient of outputs and sum is the same.
+// Probabilities are rounded to the values' type for the product with them, since mma.sync takes both
+// operands in one 16-bit type: each by half a unit in its last place, as the result is at the end.
+// They are summed as they are, so what rounding takes from a small one is lost. bf16 has the exponents
+// of f32; f16 ends at 2^-24, and a long cache may hold much weight in keys below that. So exponentials
+// are taken against the maximum less this, and f16 reaches from 2^15 for the largest, half its range,
+// to 2^-39 of it. Maxima below are all lower by it; the quotient of outputs and sum is the same.
 template <bool kBf16>
 constexpr float kLift = kBf16 ? 0.f : 15.f;
 

@@ -13,15 +13,16 @@
 //
 // Measured (bf16, queries, keys and values in one buffer): 16384 tokens with 16 heads of 128 over
 // 4 key-value heads 640-645 us, 1705-1720 TFLOP/s, 89-90% of a large library matrix product's rate;
-// 8192 tokens 186 us (1477), with heads of 64 columns 158-160 us (860-870). What bounds it there, at
-// either width, is the chain from a row tile's scores through its softmax to the product and the
-// next scores, of which two row tiles in turn hide most and for a third TMEM has no columns: at
-// 8192 tokens the tensor cores are busy 67% of the time (39% at 64 columns), the special-function
-// units 34% (39%), and the schedulers issue in 38% (42%) of the cycles. Short prompts wait for
+// 8192 tokens 184-187 us (1470-1490), with heads of 64 columns 157-166 us (830-875). What bounds it
+// there, at either width, is the chain from a row tile's scores through its softmax to the product
+// and the next scores, of which two row tiles in turn hide most. For scores that run ahead TMEM has no
+// columns left at 128; at 64 it has 128, which nothing uses yet. At 8192 tokens the tensor cores are
+// busy 69% of the time (39% at 64 columns), the special-function units 35% (39%), and the schedulers
+// issue in 39% (42%) of the cycles. Short prompts wait for
 // instructions (2.9 stalled warps per issue against 0.3 in a long one): a worker with a handful of
 // items runs through most of the kernel a few times only, out of caches that do not hold all of
 // it. So loops are rolled where they do not carry the inner work, and one warp walks the work for
-// all: with 90 KB of code instead of 137 a batch of 14 prompts of 0-801 tokens took 45 us, not 55.
+// all: with 90 KB of code (93 now) instead of 137 a batch of 14 prompts of 0-801 tokens took 45 us, not 55.
 // It takes 43 now: 5 before the first product, 1.3 per key tile, 2.5 per item (its output 1.2-1.8).
 // Tried and slower: two threads per row (the barrier between their maxima costs what the shorter
 // rows save); scores in blocks of 64 keys, so that a row tile always has the next ones; an MMA warp
@@ -69,10 +70,11 @@ constexpr int kPoisonSlots = 8;
 // Of a tile's probabilities against an older maximum. With 1, where nearly every tile looks for its
 // maximum, the prompt of 16384 tokens took 1093 us instead of 661.
 constexpr float kMostSum = 512.f;
-// Probabilities are rounded to the values' type for the product with them, but summed as they are:
-// what rounding takes from a small one is lost, and a long cache may hold much weight in keys that
-// f16 has no value for beside 1. So they are 2^kLift times larger there, kMostSum of it below f16's
-// largest value. bf16 has the exponents of f32.
+// Probabilities are rounded to the values' type for the product with them, since the MMA takes both
+// operands in one 16-bit type: each by half a unit in its last place, as the result is at the end.
+// They are summed as they are, so what rounding takes from a small one is lost, and a long cache may
+// hold much weight in keys that f16 has no value for beside 1. So they are 2^kLift times larger there,
+// kMostSum of it below f16's largest value. bf16 has the exponents of f32.
 template <bool kBf16>
 constexpr float kLift = kBf16 ? 0.f : 6.f;
 template <bool kBf16>

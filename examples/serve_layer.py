@@ -1,5 +1,5 @@
-"""The Engram block and the attention of its decoder layer, served together: a batch of prompts, then
-one token per sequence and step.
+"""The Engram block and an attention beside it, served together: a batch of prompts, then one or several
+tokens per sequence and step.
 
     python examples/serve_layer.py
 

@@ -416,15 +416,16 @@ ENGRAM_API int engram_probe_stream_read(const void* src, size_t bytes, int32_t m
                                         void* stream);
 
 /*
- * The attention of the decoder layer that holds the block: over packed prompts, and over a paged
- * cache that a prompt's keys and values were written to. The pages have no counterpart; a layer
- * that serves prompts and decodes with engram_forward needs it next to the block.
+ * Grouped-head causal attention next to the block: over packed prompts, and over a paged cache that a
+ * prompt's keys and values were written to, with the lengths that engram_forward advances. The pages
+ * have no counterpart: they do not show the attention of the layer that holds the block.
  *
  *   n_heads query heads share n_kv_heads key-value heads: head h reads key-value head
  *   h / (n_heads / n_kv_heads). dtype is the type of queries, keys, values and outputs. scale
  *   multiplies the products q . k (usually head_dim^-1/2).
- * Requirements: n_heads % n_kv_heads == 0; 1 <= head_dim <= 128, head_dim % 8 == 0; at most 128
- * query heads per key-value head (else ENGRAM_EUNSUPPORTED); scale finite and > 0.
+ * Requirements: n_heads % n_kv_heads == 0; 1 <= head_dim <= 128, head_dim % 8 == 0 (products are
+ * formed at 64 columns up to that width and at 128 above it); at most 128 query heads per key-value
+ * head (else ENGRAM_EUNSUPPORTED); scale finite and > 0.
  */
 #define ENGRAM_BF16 0
 #define ENGRAM_F16 1
