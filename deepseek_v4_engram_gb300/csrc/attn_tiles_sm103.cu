@@ -22,7 +22,7 @@
 // instructions (2.9 stalled warps per issue against 0.3 in a long one): a worker with a handful of
 // items runs through most of the kernel a few times only, out of caches that do not hold all of
 // it. So loops are rolled where they do not carry the inner work, and one warp walks the work for
-// all: with 90 KB of code (93 now) instead of 137 a batch of 14 prompts of 0-801 tokens took 45 us, not 55.
+// all: with 90 KB of code (94 now) instead of 137 a batch of 14 prompts of 0-801 tokens took 45 us, not 55.
 // It takes 43 now: 5 before the first product, 1.3 per key tile, 2.5 per item (its output 1.2-1.8).
 // Tried and slower: two threads per row (the barrier between their maxima costs what the shorter
 // rows save); scores in blocks of 64 keys, so that a row tile always has the next ones; an MMA warp
@@ -463,30 +463,56 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t k0 = seg.first > seg.tile0 * kTileKeys ? seg.first
                                                                   : seg.tile0 * kTileKeys;
         const int32_t k1 = limit < seg.tile1 * kTileKeys ? limit : seg.tile1 * kTileKeys;
+        const int32_t end = seg.keys < seg.tile1 * kTileKeys ? seg.keys : seg.tile1 * kTileKeys;
         const float base = m == -INFINITY ? 0.f : fmaf(-m, c, kLift<kBf16>);
         const uint16_t* q = a.q + static_cast<int64_t>(seg.token0 + tok) * a.q_token +
                             static_cast<int64_t>(head) * a.q_head;
+        // 32 keys at a time, the same for all rows: which of them hold such values, and which of those
+        // have no probability left, are found once, not once per column
 #pragma unroll 1
-        for (int col = 0; col < a.head_dim; ++col) {
-          uint32_t o = tc_ld_32x32b_x1(tO + col);
+        for (int32_t from = k0; from < end; from += 32) {
+          uint32_t found = 0, gone = 0;
 #pragma unroll 1
-          for (int32_t k = k0; k < k1; ++k) {
+          for (int32_t k = from; k < from + 32 && k < k1; ++k) {
             const uint16_t* v = kv_row(a, seg, true, k);
-            const float x = v == nullptr ? 0.f : to_f32<kBf16>(v[col]);
-            if (fabsf(x) < INFINITY) continue;
-            // times the key's probability, which may be 0 for all that
+            uint32_t any = 0;
+#pragma unroll 1
+            for (int d = 0; v != nullptr && d < a.head_dim; d += 8) {
+              const uint4 w = *reinterpret_cast<const uint4*>(v + d);
+              any |= nonfinite_bits<kBf16>(w.x) | nonfinite_bits<kBf16>(w.y) |
+                     nonfinite_bits<kBf16>(w.z) | nonfinite_bits<kBf16>(w.w);
+            }
+            if (any == 0) continue;
             const uint16_t* key = kv_row(a, seg, false, k);
             float s = 0.f;
 #pragma unroll 1
-            for (int d = 0; d < a.head_dim; ++d)
-              s += to_f32<kBf16>(q[d]) * (key == nullptr ? 0.f : to_f32<kBf16>(key[d]));
+            for (int d = 0; d < a.head_dim; d += 2) {
+              const uint32_t x = *reinterpret_cast<const uint32_t*>(q + d);
+              const uint32_t y = *reinterpret_cast<const uint32_t*>(key + d);
+              s += to_f32<kBf16>(static_cast<uint16_t>(x)) * to_f32<kBf16>(static_cast<uint16_t>(y));
+              s += to_f32<kBf16>(static_cast<uint16_t>(x >> 16)) *
+                   to_f32<kBf16>(static_cast<uint16_t>(y >> 16));
+            }
             const uint32_t p = pack16x2<kBf16>(exp2_fast(fmaf(s, c, base)), 0.f);
-            o = __float_as_uint(__uint_as_float(o) + to_f32<kBf16>(static_cast<uint16_t>(p)) * x);
+            found |= 1u << (k - from);
+            if (!(to_f32<kBf16>(static_cast<uint16_t>(p)) > 0.f)) gone |= 1u << (k - from);
           }
-          __syncwarp();
-          tc_st_32x32b_x1(tO + col, o);
+          if (!__any_sync(0xFFFFFFFFu, found != 0)) continue;
+#pragma unroll 1
+          for (int col = 0; col < a.head_dim; ++col) {
+            uint32_t o = tc_ld_32x32b_x1(tO + col);
+#pragma unroll 1
+            for (uint32_t left = found; left != 0; left &= left - 1) {
+              const int k = __ffs(left) - 1;
+              const float x = to_f32<kBf16>(kv_row(a, seg, true, from + k)[col]);
+              if (!(fabsf(x) < INFINITY))
+                o = __float_as_uint(__uint_as_float(o) + (gone >> k & 1u ? x * 0.f : x));
+            }
+            __syncwarp();
+            tc_st_32x32b_x1(tO + col, o);
+          }
+          tc_wait_st();
         }
-        tc_wait_st();
       }
       // 32 columns at a time; 16 bytes of a row are 8 results or 4 sums
 #pragma unroll 1

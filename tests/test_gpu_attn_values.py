@@ -48,3 +48,27 @@ def test_infinite_value_of_small_weight(q_len, dtype, below, want, where):
     assert np.isposinf(x) if want == "inf" else np.isnan(x), x
     if where == N - 1:       # seen by the last row alone
         np.testing.assert_allclose(got[:-1], clean[:-1], rtol=2.0 ** -7, atol=1e-4)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_values_that_are_nowhere_finite(value, dtype):
+    # every value of every tile, in prompts and chunks: the rare path for each of them, in time
+    heads, kv_heads, d, lens = 8, 2, 128, [1000, 3, 260]
+    total = sum(lens)
+    q, k = randn((total, heads, d), 1, dtype), randn((total, kv_heads, d), 2, dtype)
+    v = torch.full((total, kv_heads, d), value, dtype=dtype, device="cuda")
+    desc = eg.make_attn_desc(heads, kv_heads, d, dtype)
+    out = torch.zeros_like(q)
+    eg.engram_attn_prompt(desc, q, k, v, cu_of(lens), out)
+    assert eg.engram_check_errors() == 0
+    o = f64(out)
+    assert (np.isposinf(o) if value == float("inf") else np.isnan(o)).all()
+    cache = Paged(lens, 16, kv_heads, d, dtype, 3)
+    cache.v.fill_(value)
+    for chunk in ([700, 3, 200], [1, 2, 4]):
+        q, out = q[:sum(chunk)], torch.zeros_like(q[:sum(chunk)])
+        eg.engram_attn_paged(desc, q, cu_of(chunk), cache.kv_len, cache.table, cache.k, cache.v, out, max(chunk))
+        assert eg.engram_check_errors() == 0
+        o = f64(out)
+        assert (np.isposinf(o) if value == float("inf") else np.isnan(o)).all()
