@@ -523,7 +523,7 @@ ENGRAM_API int engram_attn_paged(const engram_attn_desc_t* desc, const engram_at
  * kv_len already counts the chunk (negative: 0). A position before 0 is not kept; one beyond the
  * block table is not written and sets ENGRAM_DEVERR_CACHE_FULL; nor is one whose page number is
  * outside [0, n_pages), which sets ENGRAM_DEVERR_PAGE_RANGE. Slots of the same page given to two
- * sequences are written by both, in no order.
+ * sequences are written by both, in no order; k and v may not lie in slots that the call writes.
  */
 ENGRAM_API int engram_kv_append(const engram_attn_desc_t* desc, const engram_attn_view_t* k,
                                 const engram_attn_view_t* v, const int32_t* cu_seqlens,
