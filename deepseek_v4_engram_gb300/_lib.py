@@ -71,6 +71,18 @@ class EngramKvCache(ctypes.Structure):
                 ("block_table", ctypes.c_void_p), ("table_width", ctypes.c_int32)]
 
 
+class EngramKvCacheFp8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("k_page_stride", ctypes.c_int64), ("k_slot_stride", ctypes.c_int64),
+                ("k_head_stride", ctypes.c_int64), ("v_page_stride", ctypes.c_int64),
+                ("v_slot_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("k_scale_page_stride", ctypes.c_int64), ("k_scale_head_stride", ctypes.c_int64),
+                ("v_scale_page_stride", ctypes.c_int64), ("v_scale_head_stride", ctypes.c_int64),
+                ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("block_table", ctypes.c_void_p), ("table_width", ctypes.c_int32)]
+
+
 MAX_HASH_LAYERS = 16
 
 _P = ctypes.c_void_p
@@ -85,6 +97,7 @@ _ADESC = ctypes.POINTER(EngramAttnDesc)
 _VIEW = _CACHE = ctypes.c_void_p
 PACK_VIEW = struct.Struct("Pqq")
 PACK_CACHE = struct.Struct("PP6q2iPi0P")
+PACK_CACHE_FP8 = struct.Struct("PPPP10q2iPi0P")
 
 # name -> (restype, argtypes); the same names as include/engram.h
 SIGNATURES = {
@@ -120,6 +133,10 @@ SIGNATURES = {
     "engram_attn_paged": (ctypes.c_int, [_ADESC, _VIEW, _P, _I32, _I32, _I32, _P, _CACHE, _VIEW,
                                          _P, _P, _SZ, _P]),
     "engram_kv_append": (ctypes.c_int, [_ADESC, _VIEW, _VIEW, _P, _I32, _I32, _P, _CACHE, _P]),
+    "engram_kv_append_fp8": (ctypes.c_int, [_ADESC, _VIEW, _VIEW, _P, _I32, _I32, _P, _CACHE, _P]),
+    "engram_kv_read_fp8": (ctypes.c_int, [_ADESC, _P, _I32, _I32, _P, _CACHE, _VIEW, _VIEW, _P]),
+    "engram_attn_paged_fp8": (ctypes.c_int, [_ADESC, _VIEW, _P, _I32, _I32, _I32, _P, _CACHE,
+                                             _VIEW, _P, _P, _SZ, _P]),
 }
 
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024

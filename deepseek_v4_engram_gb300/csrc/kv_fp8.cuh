@@ -1,0 +1,82 @@
+// The 8-bit cache's format on the device. A row, the head_dim values of one position and key-value
+// head, is e4m3 codes and one e8m0 byte, value = code * 2^(byte - 127). Where the table's rows have a
+// scale for every 32 values, a cache row has one: codes are floating point, so that only rows whose
+// values span more than 2^15 would gain by more, and a scale that belongs to a key or a value as a
+// whole leaves the products to the codes (it is a factor of a score, or of a probability). A power of
+// two makes both ways exact but for the one rounding to a code.
+#pragma once
+
+#include "attn_device.cuh"
+#include "kv_fp8.h"
+
+namespace engram {
+
+// Rows are not scaled up beyond 2^100: sums over a long cache of weights that were divided by a value's
+// scale then stay finite in f32. Bytes below it count as it; a page that is not the cache's reads as 0.
+constexpr uint32_t kMinScale = 27;
+constexpr uint32_t kNanScale = 255;
+
+// The scale of a row whose largest magnitude is `top` (at least 0, infinite or NaN if any value is): the
+// smallest power of two that leaves every value within 448 = 1.75 * 2^8, the largest code; 1 for a row
+// of zeros. From the bits: top = 1.f * 2^(E - 127) fits under 448 * 2^(E - 135) unless 1.f > 1.75.
+__device__ __forceinline__ uint32_t fp8_scale(float top) {
+  const uint32_t b = __float_as_uint(top), E = b >> 23;
+  if (E == 255) return kNanScale;
+  if (b == 0) return 127;
+  const uint32_t s = E + ((b & 0x7FFFFFu) > 0x600000u ? 1u : 0u);
+  return s < kMinScale + 8 ? kMinScale : s - 8;
+}
+
+// 2^(byte - 127), NaN for its byte.
+__device__ __forceinline__ float fp8_scale_value(uint32_t byte) {
+  return byte == kNanScale ? __uint_as_float(0x7FC00000u)
+                           : __uint_as_float((byte < kMinScale ? kMinScale : byte) << 23);
+}
+
+// Two f32 -> two codes (lo in the low byte), round to nearest even.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+
+// Two codes -> f16 pair, exactly; NaN codes give NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(codes));
+  return r;
+}
+
+// Where token t of the packed ones lies in the cache: it is one of the last positions of the sequence
+// that holds it. kNone: a token of no sequence; kOutside: before the first position, or (reported) beyond
+// the table or on a page that the cache does not have.
+struct Fp8Place {
+  enum Kind { kInside, kNone, kOutside } kind;
+  int32_t page, slot;
+};
+__device__ __forceinline__ Fp8Place fp8_place(const KvFp8Args& a, int32_t t) {
+  int32_t lo = 0, hi = a.n_seqs;   // the last b with cu[b] <= t
+  while (hi - lo > 1) {
+    const int32_t mid = lo + (hi - lo) / 2;
+    if (a.cu[mid] <= t) lo = mid;
+    else hi = mid;
+  }
+  const int32_t end = attn_clamp(a.cu[lo + 1], 0, a.total);
+  if (t < a.cu[lo] || t >= end) return {Fp8Place::kNone, 0, 0};
+  const int32_t len = a.kv_len[lo];
+  const int32_t p = (len > 0 ? len : 0) - (end - t);   // a negative length is an empty cache
+  if (p < 0) return {Fp8Place::kOutside, 0, 0};
+  const int32_t col = p / a.page_size;
+  if (col >= a.table_width) {
+    set_error(a.err, kErrCacheCapacity);
+    return {Fp8Place::kOutside, 0, 0};
+  }
+  const int32_t page = a.table[static_cast<int64_t>(lo) * a.table_width + col];
+  if (page < 0 || page >= a.n_pages) {
+    set_error(a.err, kErrPageRange);
+    return {Fp8Place::kOutside, 0, 0};
+  }
+  return {Fp8Place::kInside, page, p - col * a.page_size};
+}
+
+}  // namespace engram

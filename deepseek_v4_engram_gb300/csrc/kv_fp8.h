@@ -1,0 +1,37 @@
+// A paged cache in eight bits: what the C ABI (attn_fp8_capi.cu) hands to the kernels. Host-only
+// launch declarations; pointers are device pointers already validated.
+#pragma once
+
+#include "attn.h"
+
+namespace engram {
+
+// Codes [pages, page_size, heads, D] and scales [pages, heads, page_size] of the keys or the values,
+// with the byte strides of a page, a slot and a head.
+struct KvFp8Part {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t page, slot, head;
+  int64_t scale_page, scale_head;
+};
+
+struct KvFp8Args {
+  const int32_t* cu;
+  const int32_t* kv_len;
+  const int32_t* table;
+  int32_t n_seqs, total, table_width, page_size, n_pages, kv_heads, head_dim;
+  bool bf16;                 // else f16
+  KvFp8Part k, v;
+  uint16_t* k16;             // the 16-bit side: element strides of a token and of a head follow
+  uint16_t* v16;
+  int64_t k_token, k_head, v_token, v_head;
+  uint32_t* err;
+};
+cudaError_t launch_kv_append_fp8(const KvFp8Args& a, cudaStream_t st);   // 16 bits to the pages
+cudaError_t launch_kv_read_fp8(const KvFp8Args& a, cudaStream_t st);     // the pages to 16 bits
+
+// Attention over such a cache: `a` as for a paged cache of 16 bits, but for its keys and values.
+cudaError_t launch_attn_fp8(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows,
+                            cudaStream_t st);
+
+}  // namespace engram

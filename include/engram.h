@@ -530,6 +530,78 @@ ENGRAM_API int engram_kv_append(const engram_attn_desc_t* desc, const engram_att
                                 int32_t n_seqs, int32_t total, const int32_t* kv_len,
                                 const engram_kv_cache_t* cache, void* stream);
 
+/*
+ * A paged cache in eight bits, half the bytes that decoding reads: a row, the head_dim values of one
+ * position and key-value head, is e4m3fn codes and one e8m0 byte, value = code * 2^(byte - 127), or
+ * NaN throughout where the byte is 255. (The table of stage 2 has a byte for every 32 values; in a
+ * cache one for a row is as exact unless its values span more than 2^15, and costs the attention
+ * nothing.) The pages have no counterpart.
+ *   k, v              codes [n_pages, page_size, n_kv_heads, head_dim], strides in bytes;
+ *   k_scale, v_scale  bytes [n_pages, n_kv_heads, page_size], dense in the slots, strides in bytes;
+ *   block_table, n_pages, page_size and table_width as in engram_kv_cache.
+ * Requirements: head_dim % 16 == 0 and page_size % 16 == 0 (else ENGRAM_EUNSUPPORTED); strides
+ * multiples of 16, > 0 (one of a dimension of a single element is not read); arrays 16-byte aligned.
+ */
+typedef struct engram_kv_cache_fp8 {
+  const void* k;
+  const void* v;
+  const void* k_scale;
+  const void* v_scale;
+  int64_t k_page_stride, k_slot_stride, k_head_stride;
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+  int64_t k_scale_page_stride, k_scale_head_stride;
+  int64_t v_scale_page_stride, v_scale_head_stride;
+  int32_t n_pages;
+  int32_t page_size;
+  const int32_t* block_table;
+  int32_t table_width;
+} engram_kv_cache_fp8_t;
+
+/*
+ * engram_kv_append into an 8-bit cache: each row is quantised as it is written, its scale the
+ * smallest power of two, from 2^-100 on, for which no value exceeds 448 times it (1 for a row of
+ * zeros), its codes the values over the scale rounded to nearest, ties to even. A row that holds an
+ * infinity or NaN gets the byte 255 and codes of 0. Tokens, positions, lengths and errors as in
+ * engram_kv_append. The cache's four arrays may share no byte with each other or any other argument
+ * (ENGRAM_EINVAL).
+ */
+ENGRAM_API int engram_kv_append_fp8(const engram_attn_desc_t* desc, const engram_attn_view_t* k,
+                                    const engram_attn_view_t* v, const int32_t* cu_seqlens,
+                                    int32_t n_seqs, int32_t total, const int32_t* kv_len,
+                                    const engram_kv_cache_fp8_t* cache, void* stream);
+
+/*
+ * Reads back what engram_kv_append_fp8 with the same cu_seqlens and kv_len wrote: the last n of each
+ * sequence's kv_len positions, n = cu_seqlens[b + 1] - cu_seqlens[b] (the whole cache where that is
+ * kv_len), to rows of dtype, rounded to nearest (exact but for values below the type's normal range;
+ * the type's largest value where a code's rounding went past it). Bytes below 27 (2^-100, the smallest that
+ * an append writes) count as 27. A position before 0 reads as zeros; so does one beyond the block
+ * table, which sets ENGRAM_DEVERR_CACHE_FULL, and one on a page outside [0, n_pages), which sets
+ * ENGRAM_DEVERR_PAGE_RANGE. Tokens of no sequence are not written. k_out and v_out
+ * [total, n_kv_heads, head_dim] may share no byte with each other or any other argument, nor two of
+ * their rows with each other (ENGRAM_EINVAL).
+ */
+ENGRAM_API int engram_kv_read_fp8(const engram_attn_desc_t* desc, const int32_t* cu_seqlens,
+                                  int32_t n_seqs, int32_t total, const int32_t* kv_len,
+                                  const engram_kv_cache_fp8_t* cache,
+                                  const engram_attn_view_t* k_out, const engram_attn_view_t* v_out,
+                                  void* stream);
+
+/*
+ * engram_attn_paged over an 8-bit cache: the same chunks, masks, lengths, workspace and errors, and
+ * the value of a cached row as above. Scores, maxima and sums in f32; products take codes and queries
+ * in f16, which holds both exactly (a bf16 query row is first scaled by a power of two; what lies
+ * 2^-39 below its largest element or further is rounded away); probabilities are rounded to f16 times
+ * their value's scale, and what one value contributes below 2^-30 of the largest contribution to its
+ * row may be lost. A NaN in a row that a token does not see does not reach it.
+ */
+ENGRAM_API int engram_attn_paged_fp8(const engram_attn_desc_t* desc, const engram_attn_view_t* q,
+                                     const int32_t* cu_seqlens, int32_t n_seqs, int32_t total,
+                                     int32_t max_q, const int32_t* kv_len,
+                                     const engram_kv_cache_fp8_t* cache,
+                                     const engram_attn_view_t* out, float* lse, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
