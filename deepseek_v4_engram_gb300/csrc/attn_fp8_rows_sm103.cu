@@ -1,0 +1,586 @@
+// Attention over an 8-bit paged cache for items of at most 8, 16 or 32 query rows: decoding, a few
+// drafted tokens, any chunk of a sequence whose rows (tokens x heads that share a key-value head) are few.
+//
+//   x_rj = scale log2(e) 2^k_j q_r . K_j,   y_rj = x_rj + v_j        K_j, V_j: codes; k_j, v_j: scales
+//   o_r  = sum_j 2^(y_rj - B_r) V_j / sum_j 2^(y_rj - B_r) 2^-v_j
+//
+// in one pass over the keys. What bounds it is the cache's bytes, half of a 16-bit cache's, so there is
+// half the time for a key: a code must cost little on its way into a product. A scale belongs to a key
+// or a value as a whole, so it is a factor of a score and of a probability, and codes become f16 with one
+// conversion for two and nothing else, exactly; queries are f16 too (a bf16 row scaled by a power of two).
+//
+// The products run on mma.sync m16n8k16 turned over: S^T = K Q^T and O^T = V^T P^T, with the codes as the
+// 16-row operand and 8 query rows as the narrow one, so that a decoding item of up to 8 rows fills it.
+// Which of a lane's elements stand for which index of a contraction is free as long as both operands
+// agree, and so codes are read 16 bytes at a time, straight from where TMA puts them: a lane's 16 bytes
+// of a key row are the columns of four steps, and 16 bytes of four value rows, their bytes interleaved in
+// pairs, are eight tiles of V^T. S^T becomes P^T's operand by two 8 x 8 transposes in registers.
+//
+// Roles (384 threads): warp 8 requests the tiles by TMA, a page granule's keys, values or scales per
+// lane; warps 0-7 each take 16 of a tile's 128 keys, so every warp has its own base, sum and output and
+// no step of the loop waits for another warp. Work is shared out by key tiles (attn_plan.cuh).
+//
+// The base B_r lags behind the maximum: it is found anew only when some y exceeds it by 2^kSlack or more,
+// which a warp finds out with one vote instead of the shuffles of a maximum.
+#include "kernels.h"
+#include "kv_fp8.cuh"
+#include "wkv_tiles.cuh"
+
+namespace engram {
+
+namespace {
+
+constexpr int kConsumers = 8;
+constexpr int kExtraUnits = 1;   // an item's fixed time, in key tiles
+constexpr int kThreads = (kConsumers + 4) * 32;
+// 256 * 232 + 128 * 40 = 384 * 168: warps 9-11 are there for their registers
+constexpr int kConsumerRegs = 232, kProducerRegs = 40;
+constexpr int kMaxGranules = 8;  // of a tile: pages are multiples of 16 slots
+
+// Probabilities times their values' scales are rounded to f16 for the product with the codes, by half a
+// unit in the last place (2^-11); f16 ends at 2^-24. They are taken kLift above the largest one, and up
+// to kSlack more until the base is raised: 2^15 at most, and what lies 2^-35 below the largest is lost.
+constexpr float kLift = 11.f, kSlack = 4.f;
+// Scores beyond 2^24 or so leave no room for kLift between them: a difference may be a whole step of theirs.
+constexpr float kMostExponent = 15.5f;
+// The sum goes without the values' scales: from a probability times its value's scale, 2^-v of it. With
+// scales from 2^-100 on that may be large, so it is taken this much lower and the sum stays finite. (Terms
+// whose probability has underflowed in f32 are missing: values 2^100 below the ones that count.)
+constexpr int kSumDrop = 6;
+
+template <int DH, int NT>
+struct Geo {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kTensorBytes = kTileKeys * DH;                  // codes of K or V of a stage
+  static constexpr int kScaleBytes = kMaxGranules * 128;               // a copy starts on 128 bytes
+  static constexpr int kJoinRow = DH + 4;
+  static constexpr int kJoinRows = NT == 1 ? 8 : 16;                   // joined at a time
+  static constexpr int kJoinBytes = kConsumers * kJoinRows * kJoinRow * 4;
+  static constexpr bool kQueriesShared = NT == 4;                      // else in registers
+  static constexpr int kQueryBytes = kQueriesShared ? DH / 16 * NT * 32 * 8 : 0;
+  static constexpr int kStages = DH == 128 ? (NT == 1 ? 5 : 4) : 8;
+};
+
+template <int DH, int NT>
+struct Shared {
+  uint64_t full[Geo<DH, NT>::kStages];
+  uint64_t empty[Geo<DH, NT>::kStages];
+  AttnStart start;
+  float2 ml[kConsumers][Geo<DH, NT>::kRows];   // bases and sums
+  float row_scale[Geo<DH, NT>::kRows];
+  uint32_t poison[Geo<DH, NT>::kRows][DH / 32];   // columns of a row that are NaN by a value's code
+  int poisoned;
+  int abort;
+};
+
+template <int DH, int NT>
+constexpr size_t smem_bytes() {
+  using G = Geo<DH, NT>;
+  return 1024 + size_t(G::kStages) * 2 * (G::kTensorBytes + G::kScaleBytes) + G::kJoinBytes +
+         G::kQueryBytes + sizeof(Shared<DH, NT>);
+}
+static_assert(smem_bytes<128, 1>() <= 232448 && smem_bytes<128, 2>() <= 232448 &&
+              smem_bytes<128, 4>() <= 232448 && smem_bytes<64, 4>() <= 232448, "shared memory");
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+
+template <int N>
+__device__ __forceinline__ void set_max_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
+  return e4m3x2_to_f16x2(static_cast<uint16_t>(w));
+}
+__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
+  return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
+}
+
+// The bytes of `w` that are NaN codes, by their top bits.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// Which key of 16 (of each half) a lane's row `i` of S^T stands for. 128 columns: row i of the 128-byte
+// swizzle meets every bank once when lanes g and g + 1 read rows that differ in bit 2. 64 columns: rows of
+// 64 bytes meet them when the two differ in bit 0, and the value rows of lanes t when those differ in
+// bits 0 and 2.
+template <int DH>
+__device__ __forceinline__ int key_of(int i) {
+  if constexpr (DH == 128) return ((i & 1) << 2) | (i >> 1);
+  const int t = i >> 1;
+  return ((t & 1) | ((t & 2) << 1)) ^ ((i & 1) * 3);
+}
+
+template <int DH, int NT, bool kBf16>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                         const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ CUtensorMap tmVs,
+                         const __grid_constant__ AttnArgs a, const AttnPieces pieces) {
+  using G = Geo<DH, NT>;
+  constexpr int kSteps = DH / 16;   // of a score's contraction; and tiles of V^T
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_1024(smem_raw);
+  uint8_t* scales = smem + G::kStages * 2 * G::kTensorBytes;
+  uint2* queries = reinterpret_cast<uint2*>(scales + G::kStages * 2 * G::kScaleBytes);
+  float* join = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(queries) + G::kQueryBytes);
+  Shared<DH, NT>* sh = reinterpret_cast<Shared<DH, NT>*>(reinterpret_cast<uint8_t*>(join) + G::kJoinBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < G::kStages; ++s) {
+      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->empty[s], kConsumers);
+    }
+    sh->abort = 0;
+    sh->poisoned = 0;
+    for (int i = 0; i < G::kRows * (DH / 32); ++i) (&sh->poison[0][0])[i] = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmK);
+    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmKs);
+    tma_prefetch_desc(&tmVs);
+  }
+  pdl_wait();   // queries, lengths and the cache may come from the previous kernel
+  pdl_launch_dependents();
+  attn_find_start<kThreads>(a.plan, blockIdx.x, &sh->start, a.err);
+  volatile int* abort = &sh->abort;
+
+  if (warp >= kConsumers) {
+    // ------------------------------------------------------------- TMA producer
+    set_max_regs_down<kProducerRegs>();
+    AttnCursor cur = sh->start.cursor;
+    AttnSegment seg;
+    TmaRingT<G::kStages> ring;
+    const int gran = lane & 7, part = lane >> 3;   // part: keys, values, keys' scales, values' scales
+    const CUtensorMap* map = part == 0 ? &tmK : part == 1 ? &tmV : part == 2 ? &tmKs : &tmVs;
+    bool stop = warp > kConsumers;
+    while (!stop && cur.next(a.plan, seg)) {
+      for (int32_t t = seg.tile0; t < seg.tile1 && t * kTileKeys < seg.keys; ++t) {
+        const int32_t k0 = t * kTileKeys;
+        const int32_t n = seg.keys - k0 < kTileKeys ? seg.keys - k0 : kTileKeys;
+        const int32_t grans = (n + a.granule - 1) / a.granule;
+        KvPlace at{0, 0};
+        if (gran < grans) at = kv_place(a, seg, k0 + gran * a.granule);
+        stop = __any_sync(0xFFFFFFFFu, !attn_wait(&sh->empty[ring.stage], ring.phase ^ 1u, abort));
+        if (stop) break;
+        if (lane == 0)
+          mbar_arrive_expect_tx(&sh->full[ring.stage], static_cast<uint32_t>(grans * a.granule) * 2 * (DH + 1));
+        __syncwarp();
+        if (gran < grans) {
+          if (part < 2)
+            tma_load_4d(smem + (ring.stage * 2 + part) * G::kTensorBytes + gran * a.granule * DH, map,
+                        &sh->full[ring.stage], 0, seg.h, at.z, at.w);
+          else
+            tma_load_3d(scales + (ring.stage * 2 + part - 2) * G::kScaleBytes + gran * 128, map,
+                        &sh->full[ring.stage], at.z, seg.h, at.w);
+        }
+        ring.issued();
+      }
+    }
+    __syncwarp();
+    ring.drain(sh->full);
+  } else {
+    // ------------------------------------------------------------- consumers
+    set_max_regs_up<kConsumerRegs>();
+    AttnCursor cur = sh->start.cursor;
+    AttnSegment seg;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int keys_at = warp * 16;
+    const int kg = key_of<DH>(g);              // rows g and g + 8 of S^T: keys kg and kg + 8
+    const int granule_log = 31 - __clz(a.granule);
+    auto scale_at = [&](int key) { return ((key >> granule_log) << 7) | (key & (a.granule - 1)); };
+    const int scale0 = scale_at(keys_at + kg), scale1 = scale_at(keys_at + kg + 8);
+    // a lane's place in a tile: 16 bytes of columns of two key rows, and of four value rows
+    const uint32_t k_off = DH == 128 ? keys_at * 128 + kg * 128 + ((t4 ^ kg) << 4)
+                                     : keys_at * 64 + kg * 64 + ((t4 ^ (kg >> 1 & 3)) << 4);
+    const int va = DH == 128 ? t4 + 4 * (g & 1) : key_of<DH>(2 * t4);        // the first of a pair of rows
+    const int vb = DH == 128 ? va ^ 4 : key_of<DH>(2 * t4 + 1);
+    auto v_at = [&](int row) {
+      return DH == 128 ? (keys_at + row) * 128 + ((g ^ row) << 4)
+                       : (keys_at + row) * 64 + (((g >> 1) ^ (row >> 1 & 3)) << 4) + (g & 1) * 8;
+    };
+    const uint32_t va_off = v_at(va), vb_off = v_at(vb);
+    const bool swapped = DH == 128 && (g & 1);   // the first one read is the second of the pair
+    const uint32_t sel_lo = swapped ? 0x1504 : 0x5140, sel_hi = swapped ? 0x3726 : 0x7362;
+    uint32_t stage = 0, phase = 0;
+    if (threadIdx.x == 0) attn_no_pieces(pieces);
+    while (cur.next(a.plan, seg)) {
+      // ---- queries: row n of a tile of 8 is token n / G of the item, head h * G + n % G
+      uint2 qf[G::kQueriesShared ? 1 : NT][kSteps];
+      float rc[NT][2];       // of rows 2 t4 and + 1: what turns a product into a score, but for the key's scale
+      int32_t limit[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if (!G::kQueriesShared || warp == nt) {
+          const int32_t r = nt * 8 + g, tok = r / a.group;
+          const bool valid = tok < seg.ntok;
+          const uint16_t* qp = a.q + static_cast<int64_t>(seg.token0 + tok) * a.q_token +
+                               static_cast<int64_t>(seg.h * a.group + (r - tok * a.group)) * a.q_head;
+          uint32_t w[kSteps][2];
+#pragma unroll
+          for (int half = 0; half < DH / 64; ++half) {   // columns 16 (t4 + 4 half) + 0 .. 15
+            const int col = 16 * (t4 + 4 * half);
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            if (valid && col < a.head_dim) {
+              x = *reinterpret_cast<const uint4*>(qp + col);
+              y = *reinterpret_cast<const uint4*>(qp + col + 8);
+            }
+            w[half * 4][0] = x.x;
+            w[half * 4][1] = x.y;
+            w[half * 4 + 1][0] = x.z;
+            w[half * 4 + 1][1] = x.w;
+            w[half * 4 + 2][0] = y.x;
+            w[half * 4 + 2][1] = y.y;
+            w[half * 4 + 3][0] = y.z;
+            w[half * 4 + 3][1] = y.w;
+          }
+          float back = a.scale_log2;
+          if constexpr (kBf16) {
+            // the largest element goes to 2^14 .. 2^15
+            uint32_t top = 0;
+#pragma unroll
+            for (int kk = 0; kk < kSteps; ++kk)
+              top = __vmaxu2(top, __vmaxu2(w[kk][0] & 0x7FFF7FFFu, w[kk][1] & 0x7FFF7FFFu));
+            top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            top = max(top >> 16, top & 0xFFFFu) >> 7;          // its exponent
+            top = top < 15 ? 15 : top;
+            const float f = __uint_as_float((268u - top) << 23);
+            back *= __uint_as_float((top - 14) << 23);
+#pragma unroll
+            for (int kk = 0; kk < kSteps; ++kk)
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                w[kk][e] = pack16x2<false>(__uint_as_float(w[kk][e] << 16) * f,
+                                           __uint_as_float(w[kk][e] & 0xFFFF0000u) * f);
+          }
+          if constexpr (G::kQueriesShared) {
+#pragma unroll
+            for (int kk = 0; kk < kSteps; ++kk) queries[(kk * NT + nt) * 32 + lane] = make_uint2(w[kk][0], w[kk][1]);
+            if (t4 == 0) sh->row_scale[nt * 8 + g] = back;
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < kSteps; ++kk) qf[nt][kk] = make_uint2(w[kk][0], w[kk][1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) rc[nt][j] = __shfl_sync(0xFFFFFFFFu, back, (2 * t4 + j) * 4);
+          }
+        }
+      }
+      if constexpr (G::kQueriesShared) named_bar_sync(1, kConsumers * 32);
+      float base[NT][2], sum[NT][2];
+      float o[NT][kSteps][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int32_t r = nt * 8 + 2 * t4 + j, tok = r / a.group;
+          const bool valid = tok < seg.ntok;
+          const int32_t lim = seg.first + tok;
+          limit[nt][j] = valid && lim > 0 ? lim : 0;
+          base[nt][j] = valid ? -INFINITY : 1e30f;   // rows that are not there never ask for a new one
+          sum[nt][j] = 0.f;
+          if constexpr (G::kQueriesShared) rc[nt][j] = sh->row_scale[r];
+        }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      }
+
+      for (int32_t tile = seg.tile0; tile < seg.tile1 && tile * kTileKeys < seg.keys; ++tile) {
+        const bool here = !__any_sync(0xFFFFFFFFu, !attn_wait(&sh->full[stage], phase, abort));
+        const int32_t key0 = tile * kTileKeys + keys_at;
+        if (here && key0 < seg.keys) {
+          const uint8_t* sk = smem + stage * 2 * G::kTensorBytes;
+          const uint8_t* sv = sk + G::kTensorBytes;
+          const uint8_t* ss = scales + stage * 2 * G::kScaleBytes;
+          // ---- scores of 16 keys by the rows
+          float s[NT][4] = {};
+#pragma unroll
+          for (int half = 0; half < DH / 64; ++half) {
+            const uint4 lo = *reinterpret_cast<const uint4*>(sk + (k_off ^ (half * 64)));
+            const uint4 hi = *reinterpret_cast<const uint4*>(sk + (k_off ^ (half * 64)) + 8 * DH);
+            const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t f[4] = {codes_lo(wl[i]), codes_lo(wh[i]), codes_hi(wl[i]), codes_hi(wh[i])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                uint2 q;
+                if constexpr (G::kQueriesShared) q = queries[((half * 4 + i) * NT + nt) * 32 + lane];
+                else q = qf[nt][half * 4 + i];
+                mma_f16(s[nt], f, q.x, q.y);
+              }
+            }
+          }
+          // ---- values: four rows of 16 (8) columns, pairs of rows to be interleaved
+          constexpr int kWords = DH / 32;
+          uint32_t v[4][kWords];
+          {
+            const uint32_t at[4] = {va_off, vb_off, va_off + 8 * DH, vb_off + 8 * DH};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (DH == 128) {
+                const uint4 w = *reinterpret_cast<const uint4*>(sv + at[i]);
+                v[i][0] = w.x;
+                v[i][1] = w.y;
+                v[i][2] = w.z;
+                v[i][3] = w.w;
+              } else {
+                const uint2 w = *reinterpret_cast<const uint2*>(sv + at[i]);
+                v[i][0] = w.x;
+                v[i][1] = w.y;
+              }
+            }
+          }
+          const float kf[2] = {fp8_scale_value(ss[scale0]), fp8_scale_value(ss[scale1])};
+          uint32_t vs[2] = {ss[G::kScaleBytes + scale0], ss[G::kScaleBytes + scale1]};
+          if (__any_sync(0xFFFFFFFFu, vs[0] == kNanScale || vs[1] == kNanScale)) {   // rare: NaN codes instead
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = keys_at + (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
+              if (ss[G::kScaleBytes + scale_at(key)] == kNanScale)
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) v[i][w] = 0x7F7F7F7Fu;
+            }
+            vs[0] = vs[0] == kNanScale ? 127u : vs[0];
+            vs[1] = vs[1] == kNanScale ? 127u : vs[1];
+          }
+          float ve[2], unscale[2];   // exponents, and 2^-(v + kSumDrop)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            ve[i] = static_cast<float>(static_cast<int>(max(vs[i], kMinScale)) - 127);
+            unscale[i] = __uint_as_float((254u - kSumDrop - min(max(vs[i], kMinScale), 247u)) << 23);
+          }
+          const bool edge = key0 + 16 > seg.first;   // some row does not see all of them
+          float y[NT][4];
+          bool over = false;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = e & 1, k = e >> 1;
+              const bool hidden = edge && key0 + kg + 8 * k >= limit[nt][j];
+              y[nt][e] = hidden ? -INFINITY : fmaf(s[nt][e], rc[nt][j] * kf[k], ve[k]);
+              over |= y[nt][e] > base[nt][j] + (kLift + kSlack);
+            }
+          if (__any_sync(0xFFFFFFFFu, over)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float m = fmaxf(y[nt][j], y[nt][2 + j]);
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+                m = fmaxf(m - kLift, base[nt][j]);
+                const float f = m == -INFINITY ? 1.f : exp2_fast(base[nt][j] - m);
+                base[nt][j] = m;
+                sum[nt][j] *= f;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                  o[nt][i][j] *= f;
+                  o[nt][i][2 + j] *= f;
+                }
+              }
+          }
+          uint32_t p[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float b = base[nt][i & 1] == -INFINITY ? 0.f : base[nt][i & 1];
+              e[i] = exp2_fast(min_nan(y[nt][i] - b, kMostExponent));
+              sum[nt][i & 1] = fmaf(e[i], unscale[i >> 1], sum[nt][i & 1]);
+            }
+            p[nt][0] = transpose8x8(pack16x2<false>(e[0], e[1]));
+            p[nt][1] = transpose8x8(pack16x2<false>(e[2], e[3]));
+          }
+          // ---- a probability of 0 does not undo a NaN that it multiplies: the codes of values past the
+          // last key are cleared; NaN codes of values that only some rows see are taken out, and noted for
+          // the rows that do see them
+          uint32_t poison = 0;
+          if (edge) {
+            const int32_t pair_key[4] = {va, vb, va + 8, vb + 8};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int w = 0; w < kWords; ++w) {
+                if (key0 + pair_key[i] >= seg.keys) v[i][w] = 0;
+                poison |= nan_codes(v[i][w]);
+              }
+          }
+          if (__any_sync(0xFFFFFFFFu, poison != 0)) {   // rare
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int32_t key = key0 + (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
+              uint32_t columns = 0;   // of the lane's 4 kWords
+#pragma unroll
+              for (int w = 0; w < kWords; ++w) {
+                const uint32_t n = nan_codes(v[i][w]) >> 7;   // 1 in such a byte
+                v[i][w] &= ~(n * 0xFFu);
+                columns |= ((n | n >> 7 | n >> 14 | n >> 21) & 15u) << (4 * w);
+              }
+              if (columns == 0) continue;
+              sh->poisoned = 1;
+              const int bit = g * (DH / 8);
+#pragma unroll 1
+              for (int r = 0; r < seg.ntok * a.group; ++r)
+                if (key < seg.first + r / a.group) atomicOr(&sh->poison[r][bit / 32], columns << (bit % 32));
+            }
+          }
+          // ---- products with the values
+#pragma unroll
+          for (int w = 0; w < kWords; ++w) {
+            const uint32_t l0 = __byte_perm(v[0][w], v[1][w], sel_lo), h0 = __byte_perm(v[0][w], v[1][w], sel_hi);
+            const uint32_t l1 = __byte_perm(v[2][w], v[3][w], sel_lo), h1 = __byte_perm(v[2][w], v[3][w], sel_hi);
+            const uint32_t fl[4] = {codes_lo(l0), codes_hi(l0), codes_lo(l1), codes_hi(l1)};
+            const uint32_t fh[4] = {codes_lo(h0), codes_hi(h0), codes_lo(h1), codes_hi(h1)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_f16(o[nt][2 * w], fl, p[nt][0], p[nt][1]);
+              mma_f16(o[nt][2 * w + 1], fh, p[nt][0], p[nt][1]);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->empty[stage]);
+        if (++stage == G::kStages) { stage = 0; phase ^= 1u; }
+      }
+
+      // ---- the warps' bases, sums and outputs become one: each puts its own down and then takes a part of
+      // the rows. From here on both are relative to base + kSumDrop.
+      const bool whole = seg.begins() && seg.ends();
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg.begins() ? 1 : 0);
+      constexpr float drop = 1.f / (1 << kSumDrop);
+#pragma unroll
+      for (int r0 = 0; r0 < G::kRows; r0 += G::kJoinRows) {
+        if (r0 >= seg.ntok * a.group) break;
+        named_bar_sync(1, kConsumers * 32);   // what was there has been read
+#pragma unroll
+        for (int n = 0; n < G::kJoinRows / 8; ++n) {
+          const int nt = r0 / 8 + n;
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float l = sum[nt][j];
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+            if (g == 0) sh->ml[warp][nt * 8 + 2 * t4 + j] = make_float2(base[nt][j] + kSumDrop, l);
+            float* to = join + (warp * G::kJoinRows + n * 8 + 2 * t4 + j) * G::kJoinRow + g * (DH / 8);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+              *reinterpret_cast<float2*>(to + 2 * i) = make_float2(o[nt][i][j] * drop, o[nt][i][2 + j] * drop);
+          }
+        }
+        named_bar_sync(1, kConsumers * 32);
+        constexpr int kLanes = DH / 4;   // of a row
+        const int col = lane % kLanes * 4;
+#pragma unroll 1
+        for (int n = warp * (32 / kLanes) + lane / kLanes; n < G::kJoinRows; n += kConsumers * (32 / kLanes)) {
+          const int r = r0 + n, tok = r / a.group;
+          if (tok >= seg.ntok) continue;
+          float m = -INFINITY, l = 0.f, acc[4] = {};
+#pragma unroll
+          for (int w = 0; w < kConsumers; ++w) m = fmaxf(m, sh->ml[w][r].x);
+          const float b = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int w = 0; w < kConsumers; ++w) {
+            const float2 ml = sh->ml[w][r];
+            const float4 v = *reinterpret_cast<const float4*>(join + (w * G::kJoinRows + n) * G::kJoinRow + col);
+            const float f = exp2_fast(ml.x - b);
+            l += f * ml.y;
+            acc[0] += f * v.x;
+            acc[1] += f * v.y;
+            acc[2] += f * v.z;
+            acc[3] += f * v.w;
+          }
+          if (sh->poisoned) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (sh->poison[r][col / 32] >> (col % 32 + e) & 1) acc[e] = __uint_as_float(0x7FC00000u);
+          }
+          if (whole) {
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int32_t head = seg.h * a.group + (r - tok * a.group);
+            const int64_t token = static_cast<int64_t>(seg.token0) + tok;
+            if (col < a.head_dim)
+              *reinterpret_cast<uint2*>(a.out + token * a.o_token + static_cast<int64_t>(head) * a.o_head + col) =
+                  make_uint2(pack16x2<kBf16>(acc[0] * inv, acc[1] * inv), pack16x2<kBf16>(acc[2] * inv, acc[3] * inv));
+            if (a.lse != nullptr && col == 0)
+              a.lse[token * a.heads + head] = (m + log2f(l)) * 0.69314718055994531f;
+          } else {
+            *reinterpret_cast<float4*>(pieces.o + (slot * G::kRows + r) * DH + col) =
+                make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (col == 0)
+              *reinterpret_cast<float2*>(pieces.ml + (slot * G::kRows + r) * 2) = make_float2(m, l);
+          }
+        }
+      }
+      if (*static_cast<volatile int*>(&sh->poisoned)) {   // the same for every warp: read before it is cleared
+        named_bar_sync(1, kConsumers * 32);
+        for (int i = threadIdx.x; i < G::kRows * (DH / 32); i += kConsumers * 32) (&sh->poison[0][0])[i] = 0;
+        sh->poisoned = 0;
+        named_bar_sync(1, kConsumers * 32);
+      }
+      if (threadIdx.x == 0) attn_piece(pieces, seg);
+    }
+  }
+  __syncwarp();
+  cta_sync_all();
+  if (threadIdx.x == 0) attn_report(abort, a.err);
+}
+
+template <int DH, int NT, bool kBf16>
+cudaError_t launch(const AttnArgs& a, const CUtensorMap (&tm)[4], cudaStream_t st) {
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(attn_fp8_rows_kernel<DH, NT, kBf16>),
+                                            smem_bytes<DH, NT>());
+  if (e != cudaSuccess) return e;
+  return launch_ex(attn_fp8_rows_kernel<DH, NT, kBf16>, dim3(a.plan.workers), dim3(kThreads), smem_bytes<DH, NT>(),
+                   st, true, tm[0], tm[1], tm[2], tm[3], a, attn_pieces_at(a.workspace, a.plan.workers, 8 * NT));
+}
+
+template <int NT>
+cudaError_t launch_any(AttnArgs a, const CUtensorMap (&tm)[4], cudaStream_t st) {
+  a.plan.tokens = 8 * NT / a.group;
+  a.plan.workers = device_sm_count();
+  a.plan.extra = kExtraUnits;
+  cudaError_t e;
+  if (attn_width(a.head_dim) == 64)
+    e = a.bf16 ? launch<64, NT, true>(a, tm, st) : launch<64, NT, false>(a, tm, st);
+  else
+    e = a.bf16 ? launch<128, NT, true>(a, tm, st) : launch<128, NT, false>(a, tm, st);
+  return e != cudaSuccess ? e : launch_attn_combine(a, 8 * NT, st);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows,
+                                 cudaStream_t st) {
+  alignas(64) CUtensorMap tm[4];
+  if (!attn_fp8_tensor_maps(a, k, v, tm)) return cudaErrorInvalidValue;
+  return rows <= 8 ? launch_any<1>(a, tm, st) : rows <= 16 ? launch_any<2>(a, tm, st) : launch_any<4>(a, tm, st);
+}
+
+}  // namespace engram

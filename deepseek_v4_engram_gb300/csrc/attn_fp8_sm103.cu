@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kThreads) attn_fp8_kernel(const AttnArgs a, co
 
 }  // namespace
 
-cudaError_t launch_attn_fp8(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t, cudaStream_t st) {
+cudaError_t launch_attn_fp8(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows, cudaStream_t st) {
+  if (rows <= kAttnFp8FewRows) return launch_attn_fp8_rows(a, k, v, rows, st);
   return launch_ex(a.bf16 ? attn_fp8_kernel<true> : attn_fp8_kernel<false>, dim3(a.plan.total, a.heads), dim3(kThreads),
                    0, st, true, a, Parts{k, v});
 }

@@ -11,6 +11,7 @@
 #include "attn.h"
 #include "engram.h"
 #include "kernels.h"
+#include "kv_fp8.h"
 #include "shard.h"
 #include "stream_probe.h"
 
@@ -324,6 +325,34 @@ bool tensor_map_attn(void* map_out, const void* base, bool bf16, uint64_t dim, u
                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool tensor_map_fp8_codes(void* map_out, const KvFp8Part& p, int32_t head_dim, int32_t heads, int32_t page_size,
+                          int32_t n_pages, int32_t width, int32_t granule) {
+  if (!have_encoder()) return false;
+  // a dimension of one element has no step: any stride that the encoder accepts will do
+  auto step = [&](int32_t n, int64_t stride) { return static_cast<cuuint64_t>(n > 1 ? stride : head_dim); };
+  const cuuint64_t dims[4] = {cuuint64_t(head_dim), cuuint64_t(heads), cuuint64_t(page_size), cuuint64_t(n_pages)};
+  const cuuint64_t strides[3] = {step(heads, p.head), step(page_size, p.slot), step(n_pages, p.page)};
+  const cuuint32_t box[4] = {cuuint32_t(width), 1, cuuint32_t(granule), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return g_encode(static_cast<CUtensorMap*>(map_out), CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.codes, dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool tensor_map_fp8_scales(void* map_out, const KvFp8Part& p, int32_t heads, int32_t page_size, int32_t n_pages,
+                           int32_t granule) {
+  if (!have_encoder()) return false;
+  auto step = [&](int32_t n, int64_t stride) { return static_cast<cuuint64_t>(n > 1 ? stride : page_size); };
+  const cuuint64_t dims[3] = {cuuint64_t(page_size), cuuint64_t(heads), cuuint64_t(n_pages)};
+  const cuuint64_t strides[2] = {step(heads, p.scale_head), step(n_pages, p.scale_page)};
+  const cuuint32_t box[3] = {cuuint32_t(granule), 1, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return g_encode(static_cast<CUtensorMap*>(map_out), CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.scales, dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 uint32_t* device_error_word(cudaError_t* e) { return error_word(e); }
