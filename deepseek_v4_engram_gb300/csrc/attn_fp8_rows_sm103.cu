@@ -16,8 +16,7 @@
 // of a key row are the columns of four steps, and 16 bytes of four value rows, their bytes interleaved in
 // pairs, are eight tiles of V^T. S^T becomes P^T's operand by two 8 x 8 transposes in registers.
 //
-// Roles (384 threads): warp 8 requests the tiles by TMA, a page granule's keys, values or scales per
-// lane; warps 0-7 each take 16 of a tile's 128 keys, so every warp has its own base, sum and output and
+// Roles (384 threads): warps 8-10 request the tiles; warps 0-7 each take 16 of a tile's 128 keys, so every warp has its own base, sum and output and
 // no step of the loop waits for another warp. Work is shared out by key tiles (attn_plan.cuh).
 //
 // The base B_r lags behind the maximum: it is found anew only when some y exceeds it by 2^kSlack or more,
@@ -33,9 +32,8 @@ namespace {
 constexpr int kConsumers = 8;
 constexpr int kExtraUnits = 1;   // an item's fixed time, in key tiles
 constexpr int kThreads = (kConsumers + 4) * 32;
-// 256 * 232 + 128 * 40 = 384 * 168: warps 9-11 are there for their registers
+// 256 * 232 + 128 * 40 = 384 * 168
 constexpr int kConsumerRegs = 232, kProducerRegs = 40;
-constexpr int kMaxGranules = 8;  // of a tile: pages are multiples of 16 slots
 
 // Probabilities times their values' scales are rounded to f16 for the product with the codes, by half a
 // unit in the last place (2^-11); f16 ends at 2^-24. They are taken kLift above the largest one, and up
@@ -52,7 +50,7 @@ template <int DH, int NT>
 struct Geo {
   static constexpr int kRows = 8 * NT;
   static constexpr int kTensorBytes = kTileKeys * DH;                  // codes of K or V of a stage
-  static constexpr int kScaleBytes = kMaxGranules * 128;               // a copy starts on 128 bytes
+  static constexpr int kScaleBytes = kTileKeys;
   static constexpr int kJoinRow = DH + 4;
   static constexpr int kJoinRows = NT == 1 ? 8 : 16;                   // joined at a time
   static constexpr int kJoinBytes = kConsumers * kJoinRows * kJoinRow * 4;
@@ -87,6 +85,15 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Asynchronous copy of 4 bytes to shared memory, zeros where there is nothing to read; and this thread's
+// arrival on `bar` once its copies so far are there.
+__device__ __forceinline__ void copy4(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 __device__ __forceinline__ float min_nan(float a, float b) {
@@ -136,8 +143,8 @@ __device__ __forceinline__ int key_of(int i) {
 template <int DH, int NT, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                         const __grid_constant__ CUtensorMap tmKs, const __grid_constant__ CUtensorMap tmVs,
-                         const __grid_constant__ AttnArgs a, const AttnPieces pieces) {
+                         const __grid_constant__ AttnArgs a, const KvFp8Part ks, const KvFp8Part vs,
+                         const AttnPieces pieces) {
   using G = Geo<DH, NT>;
   constexpr int kSteps = DH / 16;   // of a score's contraction; and tiles of V^T
   extern __shared__ uint8_t smem_raw[];
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < G::kStages; ++s) {
-      mbar_init(&sh->full[s], 1);
+      mbar_init(&sh->full[s], 2 + 32);   // keys, values, and each lane's scales
       mbar_init(&sh->empty[s], kConsumers);
     }
     sh->abort = 0;
@@ -159,8 +166,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
-    tma_prefetch_desc(&tmKs);
-    tma_prefetch_desc(&tmVs);
   }
   pdl_wait();   // queries, lengths and the cache may come from the previous kernel
   pdl_launch_dependents();
@@ -168,33 +173,42 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort = &sh->abort;
 
   if (warp >= kConsumers) {
-    // ------------------------------------------------------------- TMA producer
+    // ------------------------------------------------------------- producers
+    // Warp 8 requests the keys, warp 9 the values, a page granule per lane (a warp issues its lanes' copies
+    // one after the other: with both in one warp that, not memory, set the pace); warp 10 the scales of both,
+    // four slots per lane, with copies of 4 bytes: TMA takes as long for a granule's as for its codes.
     set_max_regs_down<kProducerRegs>();
+    const int part = warp - kConsumers;
     AttnCursor cur = sh->start.cursor;
     AttnSegment seg;
     TmaRingT<G::kStages> ring;
-    const int gran = lane & 7, part = lane >> 3;   // part: keys, values, keys' scales, values' scales
-    const CUtensorMap* map = part == 0 ? &tmK : part == 1 ? &tmV : part == 2 ? &tmKs : &tmVs;
-    bool stop = warp > kConsumers;
+    bool stop = part > 2;
     while (!stop && cur.next(a.plan, seg)) {
       for (int32_t t = seg.tile0; t < seg.tile1 && t * kTileKeys < seg.keys; ++t) {
         const int32_t k0 = t * kTileKeys;
         const int32_t n = seg.keys - k0 < kTileKeys ? seg.keys - k0 : kTileKeys;
         const int32_t grans = (n + a.granule - 1) / a.granule;
+        const int32_t mine = part < 2 ? lane * a.granule : lane * 4;   // first slot of the lane's copy
+        const bool live = mine < grans * a.granule;
         KvPlace at{0, 0};
-        if (gran < grans) at = kv_place(a, seg, k0 + gran * a.granule);
+        if (live) at = kv_place(a, seg, k0 + mine);
         stop = __any_sync(0xFFFFFFFFu, !attn_wait(&sh->empty[ring.stage], ring.phase ^ 1u, abort));
         if (stop) break;
-        if (lane == 0)
-          mbar_arrive_expect_tx(&sh->full[ring.stage], static_cast<uint32_t>(grans * a.granule) * 2 * (DH + 1));
-        __syncwarp();
-        if (gran < grans) {
-          if (part < 2)
-            tma_load_4d(smem + (ring.stage * 2 + part) * G::kTensorBytes + gran * a.granule * DH, map,
-                        &sh->full[ring.stage], 0, seg.h, at.z, at.w);
-          else
-            tma_load_3d(scales + (ring.stage * 2 + part - 2) * G::kScaleBytes + gran * 128, map,
-                        &sh->full[ring.stage], at.z, seg.h, at.w);
+        uint64_t* full = &sh->full[ring.stage];
+        if (part < 2) {
+          if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(grans * a.granule) * DH);
+          __syncwarp();
+          if (live)
+            tma_load_4d(smem + (ring.stage * 2 + part) * G::kTensorBytes + lane * a.granule * DH,
+                        part == 0 ? &tmK : &tmV, full, 0, seg.h, at.z, at.w);
+        } else {
+          if (live) {
+            const uint32_t to = smem_u32(scales + ring.stage * 2 * kTileKeys + mine);
+            const bool there = at.w < a.n_pages;
+            copy4(to, ks.scales + (there ? at.w * ks.scale_page + seg.h * ks.scale_head + at.z : 0), there);
+            copy4(to + kTileKeys, vs.scales + (there ? at.w * vs.scale_page + seg.h * vs.scale_head + at.z : 0), there);
+          }
+          arrive_after_copies(full);
         }
         ring.issued();
       }
@@ -209,9 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = lane >> 2, t4 = lane & 3;
     const int keys_at = warp * 16;
     const int kg = key_of<DH>(g);              // rows g and g + 8 of S^T: keys kg and kg + 8
-    const int granule_log = 31 - __clz(a.granule);
-    auto scale_at = [&](int key) { return ((key >> granule_log) << 7) | (key & (a.granule - 1)); };
-    const int scale0 = scale_at(keys_at + kg), scale1 = scale_at(keys_at + kg + 8);
+    const int scale0 = keys_at + kg, scale1 = scale0 + 8;
     // a lane's place in a tile: 16 bytes of columns of two key rows, and of four value rows
     const uint32_t k_off = DH == 128 ? keys_at * 128 + kg * 128 + ((t4 ^ kg) << 4)
                                      : keys_at * 64 + kg * 64 + ((t4 ^ (kg >> 1 & 3)) << 4);
@@ -354,23 +366,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           const float kf[2] = {fp8_scale_value(ss[scale0]), fp8_scale_value(ss[scale1])};
-          uint32_t vs[2] = {ss[G::kScaleBytes + scale0], ss[G::kScaleBytes + scale1]};
-          if (__any_sync(0xFFFFFFFFu, vs[0] == kNanScale || vs[1] == kNanScale)) {   // rare: NaN codes instead
+          uint32_t vb8[2] = {ss[G::kScaleBytes + scale0], ss[G::kScaleBytes + scale1]};   // the values' bytes
+          if (__any_sync(0xFFFFFFFFu, vb8[0] == kNanScale || vb8[1] == kNanScale)) {   // rare: NaN codes instead
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int key = keys_at + (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
-              if (ss[G::kScaleBytes + scale_at(key)] == kNanScale)
+              if (ss[G::kScaleBytes + key] == kNanScale)
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) v[i][w] = 0x7F7F7F7Fu;
             }
-            vs[0] = vs[0] == kNanScale ? 127u : vs[0];
-            vs[1] = vs[1] == kNanScale ? 127u : vs[1];
+            vb8[0] = vb8[0] == kNanScale ? 127u : vb8[0];
+            vb8[1] = vb8[1] == kNanScale ? 127u : vb8[1];
           }
           float ve[2], unscale[2];   // exponents, and 2^-(v + kSumDrop)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            ve[i] = static_cast<float>(static_cast<int>(max(vs[i], kMinScale)) - 127);
-            unscale[i] = __uint_as_float((254u - kSumDrop - min(max(vs[i], kMinScale), 247u)) << 23);
+            ve[i] = static_cast<float>(static_cast<int>(max(vb8[i], kMinScale)) - 127);
+            unscale[i] = __uint_as_float((254u - kSumDrop - min(max(vb8[i], kMinScale), 247u)) << 23);
           }
           const bool edge = key0 + 16 > seg.first;   // some row does not see all of them
           float y[NT][4];
@@ -553,24 +565,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <int DH, int NT, bool kBf16>
-cudaError_t launch(const AttnArgs& a, const CUtensorMap (&tm)[4], cudaStream_t st) {
+cudaError_t launch(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, const CUtensorMap (&tm)[2],
+                   cudaStream_t st) {
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(attn_fp8_rows_kernel<DH, NT, kBf16>),
                                             smem_bytes<DH, NT>());
   if (e != cudaSuccess) return e;
   return launch_ex(attn_fp8_rows_kernel<DH, NT, kBf16>, dim3(a.plan.workers), dim3(kThreads), smem_bytes<DH, NT>(),
-                   st, true, tm[0], tm[1], tm[2], tm[3], a, attn_pieces_at(a.workspace, a.plan.workers, 8 * NT));
+                   st, true, tm[0], tm[1], a, k, v, attn_pieces_at(a.workspace, a.plan.workers, 8 * NT));
 }
 
 template <int NT>
-cudaError_t launch_any(AttnArgs a, const CUtensorMap (&tm)[4], cudaStream_t st) {
+cudaError_t launch_any(AttnArgs a, const KvFp8Part& k, const KvFp8Part& v, const CUtensorMap (&tm)[2],
+                       cudaStream_t st) {
   a.plan.tokens = 8 * NT / a.group;
   a.plan.workers = device_sm_count();
   a.plan.extra = kExtraUnits;
   cudaError_t e;
   if (attn_width(a.head_dim) == 64)
-    e = a.bf16 ? launch<64, NT, true>(a, tm, st) : launch<64, NT, false>(a, tm, st);
+    e = a.bf16 ? launch<64, NT, true>(a, k, v, tm, st) : launch<64, NT, false>(a, k, v, tm, st);
   else
-    e = a.bf16 ? launch<128, NT, true>(a, tm, st) : launch<128, NT, false>(a, tm, st);
+    e = a.bf16 ? launch<128, NT, true>(a, k, v, tm, st) : launch<128, NT, false>(a, k, v, tm, st);
   return e != cudaSuccess ? e : launch_attn_combine(a, 8 * NT, st);
 }
 
@@ -578,9 +592,9 @@ cudaError_t launch_any(AttnArgs a, const CUtensorMap (&tm)[4], cudaStream_t st) 
 
 cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows,
                                  cudaStream_t st) {
-  alignas(64) CUtensorMap tm[4];
+  alignas(64) CUtensorMap tm[2];
   if (!attn_fp8_tensor_maps(a, k, v, tm)) return cudaErrorInvalidValue;
-  return rows <= 8 ? launch_any<1>(a, tm, st) : rows <= 16 ? launch_any<2>(a, tm, st) : launch_any<4>(a, tm, st);
+  return rows <= 8 ? launch_any<1>(a, k, v, tm, st) : rows <= 16 ? launch_any<2>(a, k, v, tm, st) : launch_any<4>(a, k, v, tm, st);
 }
 
 }  // namespace engram

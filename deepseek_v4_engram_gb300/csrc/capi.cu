@@ -339,19 +339,8 @@ bool tensor_map_fp8_codes(void* map_out, const KvFp8Part& p, int32_t head_dim, i
   return g_encode(static_cast<CUtensorMap*>(map_out), CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.codes, dims, strides, box,
                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool tensor_map_fp8_scales(void* map_out, const KvFp8Part& p, int32_t heads, int32_t page_size, int32_t n_pages,
-                           int32_t granule) {
-  if (!have_encoder()) return false;
-  auto step = [&](int32_t n, int64_t stride) { return static_cast<cuuint64_t>(n > 1 ? stride : page_size); };
-  const cuuint64_t dims[3] = {cuuint64_t(page_size), cuuint64_t(heads), cuuint64_t(n_pages)};
-  const cuuint64_t strides[2] = {step(heads, p.scale_head), step(n_pages, p.scale_page)};
-  const cuuint32_t box[3] = {cuuint32_t(granule), 1, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  return g_encode(static_cast<CUtensorMap*>(map_out), CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, p.scales, dims, strides, box,
-                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  // a row is no longer: with 256 its neighbour's, another head's, came along unread
+                  width == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -41,21 +41,16 @@ constexpr int32_t kAttnFp8FewRows = 32;
 cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows,
                                  cudaStream_t st);
 
-// Tensor maps (capi.cu) of an 8-bit cache's codes, element (d, head, slot, page) in boxes of 64 or 128
-// columns by `granule` slots with the swizzle of that width, columns past head_dim reading as zero; and
-// of its scales, element (slot, head, page) in boxes of `granule` slots.
+// Tensor map (capi.cu) of an 8-bit cache's codes, element (d, head, slot, page) in boxes of 64 or 128
+// columns by `granule` slots with the swizzle of that width; columns past head_dim read as zero.
 bool tensor_map_fp8_codes(void* map_out, const KvFp8Part& p, int32_t head_dim, int32_t heads, int32_t page_size,
                           int32_t n_pages, int32_t width, int32_t granule);
-bool tensor_map_fp8_scales(void* map_out, const KvFp8Part& p, int32_t heads, int32_t page_size, int32_t n_pages,
-                           int32_t granule);
 
-// Those of keys, values, keys' scales and values' scales.
-inline bool attn_fp8_tensor_maps(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, CUtensorMap (&tm)[4]) {
+// Those of the keys and the values.
+inline bool attn_fp8_tensor_maps(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, CUtensorMap (&tm)[2]) {
   const int32_t heads = a.plan.kv_heads, width = attn_width(a.head_dim);
   return tensor_map_fp8_codes(&tm[0], k, a.head_dim, heads, a.page_size, a.n_pages, width, a.granule) &&
-         tensor_map_fp8_codes(&tm[1], v, a.head_dim, heads, a.page_size, a.n_pages, width, a.granule) &&
-         tensor_map_fp8_scales(&tm[2], k, heads, a.page_size, a.n_pages, a.granule) &&
-         tensor_map_fp8_scales(&tm[3], v, heads, a.page_size, a.n_pages, a.granule);
+         tensor_map_fp8_codes(&tm[1], v, a.head_dim, heads, a.page_size, a.n_pages, width, a.granule);
 }
 
 }  // namespace engram
