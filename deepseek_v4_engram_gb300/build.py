@@ -20,7 +20,7 @@ SOURCES = ["capi.cu", "stages.cu", "wkv_sm103.cu", "small_m_sm103.cu", "forward_
            "decode_sm103.cu", "noalloc.cu", "shard_rows.cu",
            "stream_probe.cu", "graph.cu", "attn_capi.cu", "attn_rows_sm103.cu",
            "attn_tiles_sm103.cu", "attn_combine.cu", "kv_append.cu", "attn_fp8_capi.cu",
-           "attn_fp8_sm103.cu", "attn_fp8_rows_sm103.cu", "kv_fp8.cu"]
+           "attn_fp8_rows_sm103.cu", "attn_fp8_tiles_sm103.cu", "kv_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden",
          "--expt-relaxed-constexpr", f"-I{INCLUDE}"]

@@ -180,9 +180,10 @@ ENGRAM_API int engram_attn_paged_fp8(const engram_attn_desc_t* desc, const engra
   a.n_pages = cache->n_pages;
   a.granule = granule_of(cache->page_size);
   const int64_t rows = int64_t(max_q > 1 ? max_q : 1) * a.group;
-  return report(launch_attn_fp8(a, part(cache, false), part(cache, true),
-                                static_cast<int32_t>(rows < (1 << 30) ? rows : 1 << 30),
-                                static_cast<cudaStream_t>(stream)),
+  const KvFp8Part k = part(cache, false), v = part(cache, true);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return report(rows <= kAttnFp8FewRows ? launch_attn_fp8_rows(a, k, v, static_cast<int32_t>(rows), st)
+                                        : launch_attn_fp8_tiles(a, k, v, st),
                 "engram_attn_paged_fp8");
 }
 

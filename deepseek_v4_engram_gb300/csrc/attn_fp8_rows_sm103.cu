@@ -87,15 +87,6 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Asynchronous copy of 4 bytes to shared memory, zeros where there is nothing to read; and this thread's
-// arrival on `bar` once its copies so far are there.
-__device__ __forceinline__ void copy4(uint32_t to, const void* from, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
 __device__ __forceinline__ float min_nan(float a, float b) {
   float d;
   asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
@@ -122,11 +113,6 @@ __device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
 }
 __device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
   return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
-}
-
-// The bytes of `w` that are NaN codes, by their top bits.
-__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
-  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
 // Which key of 16 (of each half) a lane's row `i` of S^T stands for. 128 columns: row i of the 128-byte

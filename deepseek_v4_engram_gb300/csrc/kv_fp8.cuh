@@ -47,6 +47,20 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
   return r;
 }
 
+// The bytes of `w` that are NaN codes, by their top bits.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// Asynchronous copy of 4 bytes to shared memory, zeros where there is nothing to read; and this thread's
+// arrival on `bar` once its copies so far are there.
+__device__ __forceinline__ void copy4(uint32_t to, const void* from, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(there ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void arrive_after_copies(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // Where token t of the packed ones lies in the cache: it is one of the last positions of the sequence
 // that holds it. kNone: a token of no sequence; kOutside: before the first position, or (reported) beyond
 // the table or on a page that the cache does not have.

@@ -30,16 +30,15 @@ struct KvFp8Args {
 cudaError_t launch_kv_append_fp8(const KvFp8Args& a, cudaStream_t st);   // 16 bits to the pages
 cudaError_t launch_kv_read_fp8(const KvFp8Args& a, cudaStream_t st);     // the pages to 16 bits
 
-// Attention over such a cache: `a` as for a paged cache of 16 bits, but for its keys and values.
-cudaError_t launch_attn_fp8(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows,
-                            cudaStream_t st);
-
-
+// Attention over such a cache, `a` as for a paged cache of 16 bits, but for its keys and values.
 // Items of up to kAttnFp8FewRows rows (attn_fp8_rows_sm103.cu); `rows`: of the longest chunk, at least
 // the heads that share a key-value head.
 constexpr int32_t kAttnFp8FewRows = 32;
 cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows,
                                  cudaStream_t st);
+
+// Items of up to 256 rows (attn_fp8_tiles_sm103.cu).
+cudaError_t launch_attn_fp8_tiles(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, cudaStream_t st);
 
 // Tensor map (capi.cu) of an 8-bit cache's codes, element (d, head, slot, page) in boxes of 64 or 128
 // columns by `granule` slots with the swizzle of that width; columns past head_dim read as zero.

@@ -588,12 +588,15 @@ ENGRAM_API int engram_kv_read_fp8(const engram_attn_desc_t* desc, const int32_t*
                                   void* stream);
 
 /*
- * engram_attn_paged over an 8-bit cache: the same chunks, masks, lengths, workspace and errors, and
- * the value of a cached row as above. Scores, maxima and sums in f32; products take codes and queries
- * in f16, which holds both exactly (a bf16 query row is first scaled by a power of two; what lies
- * 2^-39 below its largest element or further is rounded away); probabilities are rounded to f16 times
- * their value's scale, and what one value contributes below 2^-30 of the largest contribution to its
- * row may be lost. A NaN in a row that a token does not see does not reach it.
+ * engram_attn_paged over an 8-bit cache: the same chunks, masks, lengths, workspace and errors; keys
+ * and values are the cache's, as above. Scores, maxima and sums in f32. Where max_q * n_heads /
+ * n_kv_heads is at most 32, products take codes and queries in f16, which holds both exactly (a bf16 query
+ * row is first scaled by a power of two; what lies 2^-39 below its largest element is rounded away), and
+ * probabilities are rounded to f16 times their value's scale; what a value contributes to a row 2^-35
+ * below the largest contribution, or what lies 2^100 below the largest value of the head, may be lost.
+ * Above, keys and values are rounded to dtype as engram_kv_read_fp8 gives them (exact where they were
+ * appended in dtype) and probabilities to dtype. A NaN in a row that a token does not see does not reach
+ * it.
  */
 ENGRAM_API int engram_attn_paged_fp8(const engram_attn_desc_t* desc, const engram_attn_view_t* q,
                                      const int32_t* cu_seqlens, int32_t n_seqs, int32_t total,

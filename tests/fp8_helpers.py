@@ -80,23 +80,35 @@ class PagedFp8:
         return self.k, self.v, self.k_scale, self.v_scale
 
 
-def tolerance(ref, extra, dtype, head_dim, scale):
-    """How far out and lse may be from the exact ones (ref = attend(...) over the cache's values).
+#: A call whose longest chunk has more rows (tokens x heads that share a key-value head) goes to the kernel
+#: that computes on 16-bit tiles.
+FEW_ROWS = 32
 
-    Codes and queries enter the products exactly, but for what of a query row lies 2^-39 below its largest
-    element (`small`: what it adds to a score). The scores are f32 sums of head_dim products: off by at most
+
+def tolerance(ref, extra, dtype, head_dim, scale, rows):
+    """How far out and lse may be from the exact ones (ref = attend(...) over the cache's values), for a call of
+    `rows` rows.
+
+    Few rows: codes and queries enter the products exactly, but for what of a query row lies 2^-39 below its
+    largest element (`small`: what it adds to a score). The scores are f32 sums of head_dim products: off by at most
     e = (head_dim + 6) 2^-24 * scale sum_d |q_d k_d| + small, the products with the scales and the base of the
     logarithm included, so each probability is off by a factor of 1 +- (e + 2^-21). It is rounded to f16 times its
     value's scale: by 2^-11 relative, or by half of f16's smallest step, which is at most 2^-31 of the largest
     such product of the row (`steps`: summed over the keys with their codes). The sum of the probabilities brings
     e + 2^-21 once more, its own additions and the output's accumulation less than 2^-16 for the lengths
     here. The result is rounded once.
+
+    More rows: keys and values are 16-bit tiles of exactly the cache's values (those of these tests have one in
+    dtype), and a probability is rounded to dtype by itself, as over a 16-bit cache: by half a unit in its last
+    place, 2^-8 in bf16 and 2^-11 in f16, or by half the type's smallest step against a sum that is at least 1.
+    All else as above.
     """
     out, lse, mass, dot, vsum = ref
     small, steps = extra
     u = UNIT[dtype]
+    few = rows <= FEW_ROWS
     e = (head_dim + 6) * 2.0 ** -24 * dot + small + 2.0 ** -21 * (1 + dot / 16)
-    t = (2.0 ** -11 + 2 * e + 2.0 ** -16)[..., None] * mass + steps
+    t = ((2.0 ** -11 if few else u) + 2 * e + 2.0 ** -16)[..., None] * mass + (steps if few else STEP[dtype] * vsum)
     return t + u * (np.abs(out) + t) + STEP[dtype], e + 2.0 ** -16 + 2.0 ** -22 * np.abs(dot)
 
 
@@ -122,8 +134,8 @@ def reference(cache, i, q, scale):
     return ref, (small, steps)
 
 
-def assert_close(got, lse, ref, extra, dtype, head_dim, scale):
-    t_out, t_lse = tolerance(ref, extra, dtype, head_dim, scale)
+def assert_close(got, lse, ref, extra, dtype, head_dim, scale, rows):
+    t_out, t_lse = tolerance(ref, extra, dtype, head_dim, scale, rows)
     g = f64(got)
     assert np.isfinite(g).all(), f"{(~np.isfinite(g)).sum()} outputs are not finite"
     bad = np.abs(g - ref[0]) > t_out
@@ -155,7 +167,9 @@ def check(q_lens, kv_lens, page, heads, kv_heads, head_dim, dtype, seed=2, layou
     q, out, lse = run(cache, q_lens, heads, head_dim, dtype, seed, **kw)
     assert eg.engram_check_errors() == 0
     scale, at = kw.get("scale") or 1 / math.sqrt(head_dim), 0
+    max_q = kw.get("max_q")
+    n_rows = max(max(q_lens) if max_q is None else max_q, 1) * (heads // kv_heads)
     for i, n in enumerate(q_lens):
         s = slice(at, at + n)
-        assert_close(out[s], lse[s], *reference(cache, i, q[s], scale), dtype, head_dim, scale)
+        assert_close(out[s], lse[s], *reference(cache, i, q[s], scale), dtype, head_dim, scale, n_rows)
         at += n
