@@ -115,7 +115,7 @@ struct Geo {
                                           : (DH == 128 ? 5 : 10);   // of one K or V tile each: as many
                                                              // as fit (3 / 6 are as fast)
   static constexpr int kCodeBytes = 128 * DH;                // a tile of K or V in eight bits
-  static constexpr int kCodeStages = Kv::kFp8 ? (DH == 128 ? 3 : 6) : 0;
+  static constexpr int kCodeStages = Kv::kFp8 ? (DH == 128 ? 4 : 8) : 0;
   static constexpr uint32_t kO = 256;                        // TMEM columns: S0 S1 O0 O1
 };
 
@@ -297,26 +297,50 @@ __device__ __forceinline__ const uint16_t* kv_row(const AttnArgs& a, const AttnS
          s.h * head;
 }
 
-// Two codes times a scale in the 16-bit type, rounded once, as engram_kv_read_fp8 gives them. `plain`: none
-// goes beyond its range, and f16 has the scale.
+// Two codes times a scale in the 16-bit type, rounded once, as engram_kv_read_fp8 gives them.
 template <bool kBf16>
-__device__ __forceinline__ uint32_t scaled16x2(uint16_t codes, float scale, uint32_t scale16, bool plain) {
-  const uint32_t h = e4m3x2_to_f16x2(codes);
-  if constexpr (!kBf16) {
-    if (plain) {
-      const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&scale16));
-      return *reinterpret_cast<const uint32_t*>(&r);
-    }
-  }
+__device__ __forceinline__ uint32_t scaled16x2(uint32_t codes, float scale) {
+  const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(codes));
   float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  const float most = kBf16 ? __uint_as_float(0x7F7F0000u) : 65504.f;
   x.x *= scale;
   x.y *= scale;
-  if (!plain) {
-    const float most = kBf16 ? __uint_as_float(0x7F7F0000u) : 65504.f;
-    x.x = fabsf(x.x) > most ? copysignf(most, x.x) : x.x;   // NaN stays
-    x.y = fabsf(x.y) > most ? copysignf(most, x.y) : x.y;
-  }
+  x.x = fabsf(x.x) > most ? copysignf(most, x.x) : x.x;   // NaN stays
+  x.y = fabsf(x.y) > most ? copysignf(most, x.y) : x.y;
   return pack16x2<kBf16>(x.x, x.y);
+}
+
+// The same for four codes whose scale is from 2^-14 to 2^7 (f16, with one product for two) or from 2^-100 to
+// 2^118 (bf16, through f32): nothing goes beyond the type's range. `scale`: what fast_scale gives.
+template <bool kBf16>
+__device__ __forceinline__ bool is_fast(uint32_t byte) {
+  return kBf16 ? byte >= kMinScale && byte <= 245 : byte >= 113 && byte <= 134;
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t fast_scale(uint32_t byte) {
+  const uint32_t half = (byte - 112) << 10;
+  return kBf16 ? byte << 23 : half | half << 16;
+}
+template <bool kBf16>
+__device__ __forceinline__ void scaled16x4(uint32_t codes, uint32_t scale, uint32_t& lo, uint32_t& hi) {
+  lo = e4m3x2_to_f16x2(static_cast<uint16_t>(codes));
+  hi = e4m3x2_to_f16x2(static_cast<uint16_t>(codes >> 16));
+  if constexpr (kBf16) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    const float f = __uint_as_float(scale);
+    lo = pack16x2<true>(x.x * f, x.y * f);
+    hi = pack16x2<true>(y.x * f, y.y * f);
+  } else {
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(scale));
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(scale));
+  }
+}
+
+__device__ __forceinline__ uint2 lds64(uint32_t saddr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(saddr) : "memory");
+  return v;
 }
 
 // Warp-wide: rows [first, first + 32) of a tile of codes (rows of DH bytes with the swizzle of that width) to a
@@ -326,54 +350,84 @@ template <int DH, bool kBf16>
 __device__ __forceinline__ bool convert_tile(uint32_t codes, const uint8_t* scales, uint32_t tile, int first,
                                              int32_t end, int32_t guard, bool values) {
   constexpr int kChunks = DH / 16, kAtOnce = 32 / kChunks;   // 16-byte chunks of a row, rows at a time
-  const int c = (threadIdx.x & 31) % kChunks, in = (threadIdx.x & 31) / kChunks;
-  bool taken = false;
-#pragma unroll 2
-  for (int i = 0; i < 32; i += kAtOnce) {
-    const int r = first + i + in;
-    const uint32_t swizzle = DH == 128 ? (c ^ (r & 7)) : (c ^ (r >> 1 & 3));
-    uint4 w = lds128(codes + r * DH + (swizzle << 4));
-    uint32_t byte = scales[r];
-    if (r >= end) {
-      byte = 127;
-      if (values) w = make_uint4(0, 0, 0, 0);
-    } else if (r >= guard) {   // some rows must not see it
-      const uint32_t bad = nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w);
-      if (bad != 0 || byte == kNanScale) {
-        taken = true;
-        if (byte == kNanScale) {
-          w = make_uint4(0, 0, 0, 0);
-          byte = 127;
+  const int lane = threadIdx.x & 31, c = lane % kChunks, in = lane / kChunks;
+  // A lane takes chunk c of a row as two halves, each 8 codes in and 16 bytes out. Of 128 columns the
+  // lanes of the second box begin with the second half, so that eight lanes meet every bank once.
+  const int flip = DH == 128 && c >= 4;
+  auto from = [&](int r, int half) {
+    return codes + r * DH + ((DH == 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3)) << 4) + (half ^ flip) * 8;
+  };
+  auto to = [&](int r, int half) {
+    return tile + (c >> 2) * (kTileKeys * 128) + r * 128 + ((((2 * c & 7) + (half ^ flip)) ^ (r & 7)) << 4);
+  };
+  const uint32_t own = first + lane < end ? scales[first + lane] : 127u;   // of row `lane`
+  if (__all_sync(0xFFFFFFFFu, is_fast<kBf16>(own))) {
+    // the swizzle repeats every 8 rows: with two sets of addresses (one, for 64 columns) the rest is offsets
+    constexpr int kSets = 8 / kAtOnce, kBatch = 16 / kAtOnce;
+    uint32_t at[kSets][2], put[kSets][2];
+#pragma unroll
+    for (int e = 0; e < kSets; ++e)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        at[e][h] = from(first + in + e * kAtOnce, h);
+        put[e][h] = to(first + in + e * kAtOnce, h);
+      }
+    const uint32_t scale = fast_scale<kBf16>(own);
+    const bool edge = values && (first + 32 > end || first + 32 > guard);   // the same for all lanes
+    uint32_t bad = 0;
+#pragma unroll 1
+    for (int i = 0; i < 32; i += 16) {
+      uint2 w[kBatch][2];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) w[b][h] = lds64(at[b % kSets][h] + (i + b / kSets * 8) * DH);
+      if (edge) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (first + in + i + b * kAtOnce >= end) w[b][h] = make_uint2(0, 0);
+            bad |= nan_codes(w[b][h].x) | nan_codes(w[b][h].y);
+          }
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const uint32_t s = __shfl_sync(0xFFFFFFFFu, scale, in + i + b * kAtOnce);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint4 x;
+          scaled16x4<kBf16>(w[b][h].x, s, x.x, x.y);
+          scaled16x4<kBf16>(w[b][h].y, s, x.z, x.w);
+          sts128(put[b % kSets][h] + (i + b / kSets * 8) * 128, x);
         }
-        w = make_uint4(w.x & ~((nan_codes(w.x) >> 7) * 0xFFu), w.y & ~((nan_codes(w.y) >> 7) * 0xFFu),
-                       w.z & ~((nan_codes(w.z) >> 7) * 0xFFu), w.w & ~((nan_codes(w.w) >> 7) * 0xFFu));
       }
     }
-    const float scale = fp8_scale_value(byte);
-    // 448 times the scale is in the type's range, and the scale itself in its normal range
-    const bool mine = kBf16 ? byte >= kMinScale && byte <= 245 : byte >= 113 && byte <= 134;
-    const bool plain = __all_sync(0xFFFFFFFFu, mine);
-    const uint32_t half = (byte - 112) << 10, scale16 = half | half << 16;   // where it is plain
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    uint32_t x[8];
-    if (plain) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = scaled16x2<kBf16>(static_cast<uint16_t>(u[e / 2] >> (16 * (e & 1))), scale, scale16, true);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = scaled16x2<kBf16>(static_cast<uint16_t>(u[e / 2] >> (16 * (e & 1))), scale, scale16, false);
-    }
-    // chunks 2 c and 2 c + 1 of the row; of 128 columns the second half's lanes begin with the odd one, so
-    // that eight lanes meet every bank once
-    const bool odd = DH == 128 && c >= 4;
-    const uint32_t row = tile + (c >> 2) * (kTileKeys * 128) + r * 128;
-    const int ch = (2 * c) & 7;
-    const uint4 lo = make_uint4(x[0], x[1], x[2], x[3]), hi = make_uint4(x[4], x[5], x[6], x[7]);
-    sts128(row + (((ch + odd) ^ (r & 7)) << 4), odd ? hi : lo);
-    sts128(row + (((ch + !odd) ^ (r & 7)) << 4), odd ? lo : hi);
+    if (!__any_sync(0xFFFFFFFFu, bad != 0)) return false;
   }
+  bool taken = false;
+#pragma unroll 1
+  for (int r = first + in; r < first + 32; r += kAtOnce)
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      const uint2 q = lds64(from(r, h));
+      uint32_t w[2] = {q.x, q.y}, byte = scales[r];
+      if (r >= end) {
+        byte = 127;
+        if (values) w[0] = w[1] = 0;
+      } else if (r >= guard) {   // some rows must not see it
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t bad = byte == kNanScale ? 0x80808080u : nan_codes(w[e]);
+          taken |= bad != 0;
+          w[e] &= ~((bad >> 7) * 0xFFu);
+        }
+        if (byte == kNanScale) byte = 127;
+      }
+      const float scale = fp8_scale_value(byte);
+      sts128(to(r, h), make_uint4(scaled16x2<kBf16>(w[0], scale), scaled16x2<kBf16>(w[0] >> 16, scale),
+                                  scaled16x2<kBf16>(w[1], scale), scaled16x2<kBf16>(w[1] >> 16, scale)));
+    }
   return taken;
 }
 
