@@ -46,39 +46,40 @@ constexpr float kMostExponent = 15.5f;
 // whose probability has underflowed in f32 are missing: values 2^100 below the ones that count.)
 constexpr int kSumDrop = 6;
 
-template <int DH, int NT>
+// kHeads: key-value heads of an item, 1 or 2. NT: tiles of 8 rows of each.
+template <int DH, int NT, int kHeads>
 struct Geo {
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kTensorBytes = kTileKeys * DH;                  // codes of K or V of a stage
-  static constexpr int kScaleBytes = kTileKeys;
+  static constexpr int kHeadRows = 8 * NT, kRows = kHeads * kHeadRows;
+  static constexpr int kKeys = DH == 128 && kHeads == 2 ? 64 : kTileKeys;   // of a stage
+  static constexpr int kTensorBytes = kKeys * kHeads * DH;                  // codes of K or V of a stage
+  static constexpr int kScaleBytes = kKeys * kHeads;
   static constexpr int kJoinRow = DH + 4;
-  static constexpr int kJoinRows = NT == 1 ? 8 : 16;                   // joined at a time
+  static constexpr int kJoinRows = NT == 1 ? 8 : 16;                   // of a head, joined at a time
   static constexpr int kJoinBytes = kConsumers * kJoinRows * kJoinRow * 4;
   static constexpr bool kQueriesShared = NT == 4;                      // else in registers
-  static constexpr int kQueryBytes = kQueriesShared ? DH / 16 * NT * 32 * 8 : 0;
-  static constexpr int kStages = DH == 128 ? (NT == 1 ? 5 : 4) : 8;
+  static constexpr int kQueryBytes = kQueriesShared ? DH / 16 * NT * kHeads * 32 * 8 : 0;
+  static constexpr int kStages = kTensorBytes == 16384 ? (NT == 1 ? 5 : 4) : 8;
 };
 
-template <int DH, int NT>
+template <int DH, int NT, int kHeads>
 struct Shared {
-  uint64_t full[Geo<DH, NT>::kStages];
-  uint64_t empty[Geo<DH, NT>::kStages];
+  using G = Geo<DH, NT, kHeads>;
+  uint64_t full[G::kStages];
+  uint64_t empty[G::kStages];
   AttnStart start;
-  float2 ml[kConsumers][Geo<DH, NT>::kRows];   // bases and sums
-  float row_scale[Geo<DH, NT>::kRows];
-  uint32_t poison[Geo<DH, NT>::kRows][DH / 32];   // columns of a row that are NaN by a value's code
+  float2 ml[kConsumers][G::kHeadRows];   // bases and sums
+  float row_scale[G::kRows];
+  uint32_t poison[G::kRows][DH / 32];   // columns of a row that are NaN by a value's code
   int poisoned;
   int abort;
 };
 
-template <int DH, int NT>
+template <int DH, int NT, int kHeads>
 constexpr size_t smem_bytes() {
-  using G = Geo<DH, NT>;
+  using G = Geo<DH, NT, kHeads>;
   return 1024 + size_t(G::kStages) * 2 * (G::kTensorBytes + G::kScaleBytes) + G::kJoinBytes +
-         G::kQueryBytes + sizeof(Shared<DH, NT>);
+         G::kQueryBytes + sizeof(Shared<DH, NT, kHeads>);
 }
-static_assert(smem_bytes<128, 1>() <= 232448 && smem_bytes<128, 2>() <= 232448 &&
-              smem_bytes<128, 4>() <= 232448 && smem_bytes<64, 4>() <= 232448, "shared memory");
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
@@ -115,30 +116,37 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
   return e4m3x2_to_f16x2(static_cast<uint16_t>(w >> 16));
 }
 
-// Which key of 16 (of each half) a lane's row `i` of S^T stands for. 128 columns: row i of the 128-byte
-// swizzle meets every bank once when lanes g and g + 1 read rows that differ in bit 2. 64 columns: rows of
-// 64 bytes meet them when the two differ in bit 0, and the value rows of lanes t when those differ in
-// bits 0 and 2.
-template <int DH>
+// Which key of 16 (of each half) a lane's row `i` of S^T stands for: chosen so that eight lanes' 16-byte
+// reads of a key row (lanes g and g + 1, four chunks each), and of a value row (lanes t, and two or four
+// chunks), meet every bank of the swizzle once.
+//   128 columns, one head:   keys of g and g + 1 differ in bit 2 (values: see `swapped`)
+//   128 columns, two heads:  a key is two rows, so in bit 1; values of lanes t in their low two bits
+//   64 columns, one head:    rows of 64 bytes, keys differ in bit 0, values in bits 0 and 2
+//   64 columns, two heads:   in bit 2, values in bits 1 and 2
+template <int DH, int kHeads>
 __device__ __forceinline__ int key_of(int i) {
-  if constexpr (DH == 128) return ((i & 1) << 2) | (i >> 1);
-  const int t = i >> 1;
-  return ((t & 1) | ((t & 2) << 1)) ^ ((i & 1) * 3);
+  const int t = i >> 1, up = i & 1;
+  if constexpr (DH == 128) return kHeads == 1 ? (up << 2) | t : (up ? (t ^ 2) + 4 : t);
+  if constexpr (kHeads == 2) return up ? (2 * t ^ 4) + 1 : 2 * t;
+  return ((t & 1) | ((t & 2) << 1)) ^ (up * 3);
 }
 
-template <int DH, int NT, bool kBf16>
+template <int DH, int NT, int kHeads, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ AttnArgs a, const KvFp8Part ks, const KvFp8Part vs,
                          const AttnPieces pieces) {
-  using G = Geo<DH, NT>;
+  using G = Geo<DH, NT, kHeads>;
+  constexpr int kStagesPerTile = kTileKeys / G::kKeys;
+  constexpr int kWarpKeys = G::kKeys * kHeads / kConsumers;   // of a stage: 16 or 32
   constexpr int kSteps = DH / 16;   // of a score's contraction; and tiles of V^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
   uint8_t* scales = smem + G::kStages * 2 * G::kTensorBytes;
   uint2* queries = reinterpret_cast<uint2*>(scales + G::kStages * 2 * G::kScaleBytes);
   float* join = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(queries) + G::kQueryBytes);
-  Shared<DH, NT>* sh = reinterpret_cast<Shared<DH, NT>*>(reinterpret_cast<uint8_t*>(join) + G::kJoinBytes);
+  using S = Shared<DH, NT, kHeads>;
+  S* sh = reinterpret_cast<S*>(reinterpret_cast<uint8_t*>(join) + G::kJoinBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -170,11 +178,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     TmaRingT<G::kStages> ring;
     bool stop = part > 2;
     while (!stop && cur.next(a.plan, seg)) {
-      for (int32_t t = seg.tile0; t < seg.tile1 && t * kTileKeys < seg.keys; ++t) {
-        const int32_t k0 = t * kTileKeys;
-        const int32_t n = seg.keys - k0 < kTileKeys ? seg.keys - k0 : kTileKeys;
+      const int32_t h0 = seg.h * kHeads;
+      for (int32_t k0 = seg.tile0 * kTileKeys; k0 < seg.tile1 * kTileKeys && k0 < seg.keys; k0 += G::kKeys) {
+        const int32_t n = seg.keys - k0 < G::kKeys ? seg.keys - k0 : G::kKeys;
         const int32_t grans = (n + a.granule - 1) / a.granule;
-        const int32_t mine = part < 2 ? lane * a.granule : lane * 4;   // first slot of the lane's copy
+        const int32_t mine = part < 2 ? lane * a.granule : lane * 4 % G::kKeys;   // first slot of the lane's copy
         const bool live = mine < grans * a.granule;
         KvPlace at{0, 0};
         if (live) at = kv_place(a, seg, k0 + mine);
@@ -182,17 +190,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (stop) break;
         uint64_t* full = &sh->full[ring.stage];
         if (part < 2) {
-          if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(grans * a.granule) * DH);
+          if (lane == 0) mbar_arrive_expect_tx(full, static_cast<uint32_t>(grans * a.granule) * kHeads * DH);
           __syncwarp();
           if (live)
-            tma_load_4d(smem + (ring.stage * 2 + part) * G::kTensorBytes + lane * a.granule * DH,
-                        part == 0 ? &tmK : &tmV, full, 0, seg.h, at.z, at.w);
+            tma_load_4d(smem + (ring.stage * 2 + part) * G::kTensorBytes + lane * a.granule * kHeads * DH,
+                        part == 0 ? &tmK : &tmV, full, 0, DH == 64 ? seg.h : h0, at.z, at.w);
         } else {
-          if (live) {
-            const uint32_t to = smem_u32(scales + ring.stage * 2 * kTileKeys + mine);
-            const bool there = at.w < a.n_pages;
-            copy4(to, ks.scales + (there ? at.w * ks.scale_page + seg.h * ks.scale_head + at.z : 0), there);
-            copy4(to + kTileKeys, vs.scales + (there ? at.w * vs.scale_page + seg.h * vs.scale_head + at.z : 0), there);
+          // lanes 0 .. kKeys / 4 - 1 the first head's, and so on
+          const bool there = at.w < a.n_pages;
+#pragma unroll
+          for (int r = 0; r < kHeads; r += 128 / G::kKeys) {
+            const int32_t sub = r + lane * 4 / G::kKeys;
+            if (live) {
+              const uint32_t to = smem_u32(scales + ring.stage * 2 * G::kScaleBytes + sub * G::kKeys + mine);
+              copy4(to, ks.scales + (there ? at.w * ks.scale_page + (h0 + sub) * ks.scale_head + at.z : 0), there);
+              copy4(to + G::kScaleBytes,
+                    vs.scales + (there ? at.w * vs.scale_page + (h0 + sub) * vs.scale_head + at.z : 0), there);
+            }
           }
           arrive_after_copies(full);
         }
@@ -207,35 +221,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     AttnCursor cur = sh->start.cursor;
     AttnSegment seg;
     const int g = lane >> 2, t4 = lane & 3;
-    const int keys_at = warp * 16;
-    const int kg = key_of<DH>(g);              // rows g and g + 8 of S^T: keys kg and kg + 8
-    const int scale0 = keys_at + kg, scale1 = scale0 + 8;
-    // a lane's place in a tile: 16 bytes of columns of two key rows, and of four value rows
-    const uint32_t k_off = DH == 128 ? keys_at * 128 + kg * 128 + ((t4 ^ kg) << 4)
-                                     : keys_at * 64 + kg * 64 + ((t4 ^ (kg >> 1 & 3)) << 4);
-    const int va = DH == 128 ? t4 + 4 * (g & 1) : key_of<DH>(2 * t4);        // the first of a pair of rows
-    const int vb = DH == 128 ? va ^ 4 : key_of<DH>(2 * t4 + 1);
-    auto v_at = [&](int row) {
-      return DH == 128 ? (keys_at + row) * 128 + ((g ^ row) << 4)
-                       : (keys_at + row) * 64 + (((g >> 1) ^ (row >> 1 & 3)) << 4) + (g & 1) * 8;
+    const int sub = kHeads == 2 ? warp & 1 : 0;                 // the warp's key-value head
+    const int keys_at = warp / kHeads * kWarpKeys;              // its first key of a stage
+    const int group = a.group / kHeads;                         // query heads of a key-value head
+    const int kg = key_of<DH, kHeads>(g);                       // rows g and g + 8 of S^T: keys kg and kg + 8
+    const int scale0 = sub * G::kKeys + keys_at + kg;
+    // Where chunk `c` of 16 bytes of the warp's head in key `key` of a stage lies. Two heads: 128-byte rows of
+    // one key and head each, in this order, or of both heads of a key.
+    auto row_at = [&](int key, int c) -> uint32_t {
+      if constexpr (DH == 128) {
+        const int row = key * kHeads + sub;
+        return row * 128 + ((c ^ (row & 7)) << 4);
+      } else if constexpr (kHeads == 2) {
+        return key * 128 + (((c + 4 * sub) ^ (key & 7)) << 4);
+      } else {
+        return key * 64 + ((c ^ (key >> 1 & 3)) << 4);
+      }
+    };
+    constexpr int kKeyBytes = kHeads * DH;
+    // a lane's place in a stage: 16 bytes of columns of two key rows, and of four value rows
+    const uint32_t k_off = row_at(keys_at + kg, t4);
+    const bool swapped = DH == 128 && kHeads == 1 && (g & 1);   // the first one read is the second of the pair
+    const int va = key_of<DH, kHeads>(2 * t4 + swapped), vb = key_of<DH, kHeads>(2 * t4 + !swapped);
+    auto v_at = [&](int key) {
+      return DH == 128 ? row_at(keys_at + key, g) : row_at(keys_at + key, g >> 1) + (g & 1) * 8;
     };
     const uint32_t va_off = v_at(va), vb_off = v_at(vb);
-    const bool swapped = DH == 128 && (g & 1);   // the first one read is the second of the pair
     const uint32_t sel_lo = swapped ? 0x1504 : 0x5140, sel_hi = swapped ? 0x3726 : 0x7362;
     uint32_t stage = 0, phase = 0;
     if (threadIdx.x == 0) attn_no_pieces(pieces);
     while (cur.next(a.plan, seg)) {
-      // ---- queries: row n of a tile of 8 is token n / G of the item, head h * G + n % G
+      // ---- queries: row n of a head's is token n / group of the item, its query head n % group
       uint2 qf[G::kQueriesShared ? 1 : NT][kSteps];
       float rc[NT][2];       // of rows 2 t4 and + 1: what turns a product into a score, but for the key's scale
       int32_t limit[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (!G::kQueriesShared || warp == nt) {
-          const int32_t r = nt * 8 + g, tok = r / a.group;
+        if (!G::kQueriesShared || warp / kHeads == nt) {
+          const int32_t r = nt * 8 + g, tok = r / group;
           const bool valid = tok < seg.ntok;
           const uint16_t* qp = a.q + static_cast<int64_t>(seg.token0 + tok) * a.q_token +
-                               static_cast<int64_t>(seg.h * a.group + (r - tok * a.group)) * a.q_head;
+                               static_cast<int64_t>(seg.h * a.group + sub * group + (r - tok * group)) * a.q_head;
           uint32_t w[kSteps][2];
 #pragma unroll
           for (int half = 0; half < DH / 64; ++half) {   // columns 16 (t4 + 4 half) + 0 .. 15
@@ -276,8 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if constexpr (G::kQueriesShared) {
 #pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk) queries[(kk * NT + nt) * 32 + lane] = make_uint2(w[kk][0], w[kk][1]);
-            if (t4 == 0) sh->row_scale[nt * 8 + g] = back;
+            for (int kk = 0; kk < kSteps; ++kk)
+              queries[((kk * kHeads + sub) * NT + nt) * 32 + lane] = make_uint2(w[kk][0], w[kk][1]);
+            if (t4 == 0) sh->row_scale[sub * G::kHeadRows + nt * 8 + g] = back;
           } else {
 #pragma unroll
             for (int kk = 0; kk < kSteps; ++kk) qf[nt][kk] = make_uint2(w[kk][0], w[kk][1]);
@@ -293,31 +320,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int32_t r = nt * 8 + 2 * t4 + j, tok = r / a.group;
+          const int32_t r = nt * 8 + 2 * t4 + j, tok = r / group;
           const bool valid = tok < seg.ntok;
           const int32_t lim = seg.first + tok;
           limit[nt][j] = valid && lim > 0 ? lim : 0;
           base[nt][j] = valid ? -INFINITY : 1e30f;   // rows that are not there never ask for a new one
           sum[nt][j] = 0.f;
-          if constexpr (G::kQueriesShared) rc[nt][j] = sh->row_scale[r];
+          if constexpr (G::kQueriesShared) rc[nt][j] = sh->row_scale[sub * G::kHeadRows + r];
         }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
       }
 
-      for (int32_t tile = seg.tile0; tile < seg.tile1 && tile * kTileKeys < seg.keys; ++tile) {
+      for (int32_t first = seg.tile0 * kTileKeys; first < seg.tile1 * kTileKeys && first < seg.keys;
+           first += G::kKeys) {
         const bool here = !__any_sync(0xFFFFFFFFu, !attn_wait(&sh->full[stage], phase, abort));
-        const int32_t key0 = tile * kTileKeys + keys_at;
-        if (here && key0 < seg.keys) {
-          const uint8_t* sk = smem + stage * 2 * G::kTensorBytes;
+#pragma unroll 1
+        for (int step = 0; step < kWarpKeys; step += 16) {
+          const int32_t key0 = first + keys_at + step;
+          if (!here || key0 >= seg.keys) break;
+          const uint8_t* sk = smem + stage * 2 * G::kTensorBytes + step * kKeyBytes;
           const uint8_t* sv = sk + G::kTensorBytes;
-          const uint8_t* ss = scales + stage * 2 * G::kScaleBytes;
+          const uint8_t* ss = scales + stage * 2 * G::kScaleBytes + step;
           // ---- scores of 16 keys by the rows
           float s[NT][4] = {};
 #pragma unroll
           for (int half = 0; half < DH / 64; ++half) {
             const uint4 lo = *reinterpret_cast<const uint4*>(sk + (k_off ^ (half * 64)));
-            const uint4 hi = *reinterpret_cast<const uint4*>(sk + (k_off ^ (half * 64)) + 8 * DH);
+            const uint4 hi = *reinterpret_cast<const uint4*>(sk + (k_off ^ (half * 64)) + 8 * kKeyBytes);
             const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -325,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 uint2 q;
-                if constexpr (G::kQueriesShared) q = queries[((half * 4 + i) * NT + nt) * 32 + lane];
+                if constexpr (G::kQueriesShared) q = queries[(((half * 4 + i) * kHeads + sub) * NT + nt) * 32 + lane];
                 else q = qf[nt][half * 4 + i];
                 mma_f16(s[nt], f, q.x, q.y);
               }
@@ -335,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int kWords = DH / 32;
           uint32_t v[4][kWords];
           {
-            const uint32_t at[4] = {va_off, vb_off, va_off + 8 * DH, vb_off + 8 * DH};
+            const uint32_t at[4] = {va_off, vb_off, va_off + 8 * kKeyBytes, vb_off + 8 * kKeyBytes};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               if constexpr (DH == 128) {
@@ -351,13 +381,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          const float kf[2] = {fp8_scale_value(ss[scale0]), fp8_scale_value(ss[scale1])};
-          uint32_t vb8[2] = {ss[G::kScaleBytes + scale0], ss[G::kScaleBytes + scale1]};   // the values' bytes
+          const float kf[2] = {fp8_scale_value(ss[scale0]), fp8_scale_value(ss[scale0 + 8])};
+          uint32_t vb8[2] = {ss[G::kScaleBytes + scale0], ss[G::kScaleBytes + scale0 + 8]};   // the values' bytes
           if (__any_sync(0xFFFFFFFFu, vb8[0] == kNanScale || vb8[1] == kNanScale)) {   // rare: NaN codes instead
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int key = keys_at + (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
-              if (ss[G::kScaleBytes + key] == kNanScale)
+              if (ss[G::kScaleBytes + sub * G::kKeys + key] == kNanScale)
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) v[i][w] = 0x7F7F7F7Fu;
             }
@@ -444,8 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               sh->poisoned = 1;
               const int bit = g * (DH / 8);
 #pragma unroll 1
-              for (int r = 0; r < seg.ntok * a.group; ++r)
-                if (key < seg.first + r / a.group) atomicOr(&sh->poison[r][bit / 32], columns << (bit % 32));
+              for (int r = 0; r < seg.ntok * group; ++r)
+                if (key < seg.first + r / group)
+                  atomicOr(&sh->poison[sub * G::kHeadRows + r][bit / 32], columns << (bit % 32));
             }
           }
           // ---- products with the values
@@ -473,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg.begins() ? 1 : 0);
       constexpr float drop = 1.f / (1 << kSumDrop);
 #pragma unroll
-      for (int r0 = 0; r0 < G::kRows; r0 += G::kJoinRows) {
-        if (r0 >= seg.ntok * a.group) break;
+      for (int r0 = 0; r0 < G::kHeadRows; r0 += G::kJoinRows) {
+        if (r0 >= seg.ntok * group) break;
         named_bar_sync(1, kConsumers * 32);   // what was there has been read
 #pragma unroll
         for (int n = 0; n < G::kJoinRows / 8; ++n) {
@@ -496,17 +527,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kLanes = DH / 4;   // of a row
         const int col = lane % kLanes * 4;
 #pragma unroll 1
-        for (int n = warp * (32 / kLanes) + lane / kLanes; n < G::kJoinRows; n += kConsumers * (32 / kLanes)) {
-          const int r = r0 + n, tok = r / a.group;
+        for (int at = warp * (32 / kLanes) + lane / kLanes; at < kHeads * G::kJoinRows;
+             at += kConsumers * (32 / kLanes)) {
+          const int n = at / kHeads, head = at % kHeads;   // a row of one of the heads
+          const int r = r0 + n, tok = r / group;
           if (tok >= seg.ntok) continue;
           float m = -INFINITY, l = 0.f, acc[4] = {};
 #pragma unroll
-          for (int w = 0; w < kConsumers; ++w) m = fmaxf(m, sh->ml[w][r].x);
+          for (int w = 0; w < kConsumers; w += kHeads) m = fmaxf(m, sh->ml[w + head][r].x);
           const float b = m == -INFINITY ? 0.f : m;
 #pragma unroll
-          for (int w = 0; w < kConsumers; ++w) {
-            const float2 ml = sh->ml[w][r];
-            const float4 v = *reinterpret_cast<const float4*>(join + (w * G::kJoinRows + n) * G::kJoinRow + col);
+          for (int w = 0; w < kConsumers; w += kHeads) {
+            const float2 ml = sh->ml[w + head][r];
+            const float4 v = *reinterpret_cast<const float4*>(
+                join + ((w + head) * G::kJoinRows + n) * G::kJoinRow + col);
             const float f = exp2_fast(ml.x - b);
             l += f * ml.y;
             acc[0] += f * v.x;
@@ -517,22 +551,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (sh->poisoned) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (sh->poison[r][col / 32] >> (col % 32 + e) & 1) acc[e] = __uint_as_float(0x7FC00000u);
+              if (sh->poison[head * G::kHeadRows + r][col / 32] >> (col % 32 + e) & 1)
+                acc[e] = __uint_as_float(0x7FC00000u);
           }
+          const int32_t of_token = head * group + (r - tok * group);   // which of a token's rows
           if (whole) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int32_t head = seg.h * a.group + (r - tok * a.group);
+            const int32_t query = seg.h * a.group + of_token;
             const int64_t token = static_cast<int64_t>(seg.token0) + tok;
             if (col < a.head_dim)
-              *reinterpret_cast<uint2*>(a.out + token * a.o_token + static_cast<int64_t>(head) * a.o_head + col) =
+              *reinterpret_cast<uint2*>(a.out + token * a.o_token + static_cast<int64_t>(query) * a.o_head + col) =
                   make_uint2(pack16x2<kBf16>(acc[0] * inv, acc[1] * inv), pack16x2<kBf16>(acc[2] * inv, acc[3] * inv));
             if (a.lse != nullptr && col == 0)
-              a.lse[token * a.heads + head] = (m + log2f(l)) * 0.69314718055994531f;
+              a.lse[token * a.heads + query] = (m + log2f(l)) * 0.69314718055994531f;
           } else {
-            *reinterpret_cast<float4*>(pieces.o + (slot * G::kRows + r) * DH + col) =
-                make_float4(acc[0], acc[1], acc[2], acc[3]);
-            if (col == 0)
-              *reinterpret_cast<float2*>(pieces.ml + (slot * G::kRows + r) * 2) = make_float2(m, l);
+            const int64_t to = slot * G::kRows + tok * a.group + of_token;
+            *reinterpret_cast<float4*>(pieces.o + to * DH + col) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            if (col == 0) *reinterpret_cast<float2*>(pieces.ml + to * 2) = make_float2(m, l);
           }
         }
       }
@@ -550,37 +585,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) attn_report(abort, a.err);
 }
 
-template <int DH, int NT, bool kBf16>
+template <int DH, int NT, int kHeads, bool kBf16>
 cudaError_t launch(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, const CUtensorMap (&tm)[2],
                    cudaStream_t st) {
-  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(attn_fp8_rows_kernel<DH, NT, kBf16>),
-                                            smem_bytes<DH, NT>());
+  constexpr size_t smem = smem_bytes<DH, NT, kHeads>();
+  static_assert(smem <= 232448, "shared memory");
+  const auto kernel = attn_fp8_rows_kernel<DH, NT, kHeads, kBf16>;
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
-  return launch_ex(attn_fp8_rows_kernel<DH, NT, kBf16>, dim3(a.plan.workers), dim3(kThreads), smem_bytes<DH, NT>(),
-                   st, true, tm[0], tm[1], a, k, v, attn_pieces_at(a.workspace, a.plan.workers, 8 * NT));
+  return launch_ex(kernel, dim3(a.plan.workers), dim3(kThreads), smem, st, true, tm[0], tm[1], a, k, v,
+                   attn_pieces_at(a.workspace, a.plan.workers, Geo<DH, NT, kHeads>::kRows));
+}
+
+template <int NT, int kHeads>
+cudaError_t launch_any(AttnArgs a, const KvFp8Part& k, const KvFp8Part& v, cudaStream_t st) {
+  const int width = attn_width(a.head_dim);
+  // An item's heads are one key-value head to the plan and to the joining kernel.
+  a.plan.kv_heads /= kHeads;
+  a.group *= kHeads;
+  a.plan.tokens = 8 * NT * kHeads / a.group;
+  a.plan.workers = device_sm_count();
+  a.plan.extra = kExtraUnits;
+  if (kHeads == 2 && width == 128 && a.granule > 64) a.granule = 64;
+  alignas(64) CUtensorMap tm[2];
+  if (!attn_fp8_tensor_maps(a, k, v, kHeads, tm)) return cudaErrorInvalidValue;
+  cudaError_t e;
+  if (width == 64)
+    e = a.bf16 ? launch<64, NT, kHeads, true>(a, k, v, tm, st) : launch<64, NT, kHeads, false>(a, k, v, tm, st);
+  else
+    e = a.bf16 ? launch<128, NT, kHeads, true>(a, k, v, tm, st) : launch<128, NT, kHeads, false>(a, k, v, tm, st);
+  return e != cudaSuccess ? e : launch_attn_combine(a, 8 * NT * kHeads, st);
 }
 
 template <int NT>
-cudaError_t launch_any(AttnArgs a, const KvFp8Part& k, const KvFp8Part& v, const CUtensorMap (&tm)[2],
-                       cudaStream_t st) {
-  a.plan.tokens = 8 * NT / a.group;
-  a.plan.workers = device_sm_count();
-  a.plan.extra = kExtraUnits;
-  cudaError_t e;
-  if (attn_width(a.head_dim) == 64)
-    e = a.bf16 ? launch<64, NT, true>(a, k, v, tm, st) : launch<64, NT, false>(a, k, v, tm, st);
-  else
-    e = a.bf16 ? launch<128, NT, true>(a, k, v, tm, st) : launch<128, NT, false>(a, k, v, tm, st);
-  return e != cudaSuccess ? e : launch_attn_combine(a, 8 * NT, st);
+cudaError_t launch_heads(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, bool two, cudaStream_t st) {
+  return two ? launch_any<NT, 2>(a, k, v, st) : launch_any<NT, 1>(a, k, v, st);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows,
                                  cudaStream_t st) {
-  alignas(64) CUtensorMap tm[2];
-  if (!attn_fp8_tensor_maps(a, k, v, tm)) return cudaErrorInvalidValue;
-  return rows <= 8 ? launch_any<1>(a, k, v, tm, st) : rows <= 16 ? launch_any<2>(a, k, v, tm, st) : launch_any<4>(a, k, v, tm, st);
+  // Two key-value heads an item where they lie beside each other in memory.
+  const int64_t width = attn_width(a.head_dim);
+  const bool two = a.plan.kv_heads % 2 == 0 && a.head_dim == width && k.head == width && v.head == width;
+  return rows <= 8    ? launch_heads<1>(a, k, v, two, st)
+         : rows <= 16 ? launch_heads<2>(a, k, v, two, st)
+                      : launch_heads<4>(a, k, v, two, st);
 }
 
 }  // namespace engram

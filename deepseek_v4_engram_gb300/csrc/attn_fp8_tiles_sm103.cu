@@ -8,7 +8,7 @@ namespace engram {
 cudaError_t launch_attn_fp8_tiles(const AttnArgs& in, const KvFp8Part& k, const KvFp8Part& v, cudaStream_t st) {
   AttnArgs a = in;
   alignas(64) CUtensorMap tmQ, tm[2];
-  if (!attn_fp8_tensor_maps(a, k, v, tm) || !plan_tiles(a, tmQ)) return cudaErrorInvalidValue;
+  if (!attn_fp8_tensor_maps(a, k, v, 1, tm) || !plan_tiles(a, tmQ)) return cudaErrorInvalidValue;
   const cudaError_t e = launch_tiles_any(a, tmQ, tm[0], tm[1], KvFp8{k, v}, st);
   return e != cudaSuccess ? e : launch_attn_combine(a, kItemRows, st);
 }

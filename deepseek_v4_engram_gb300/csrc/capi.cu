@@ -327,20 +327,22 @@ bool tensor_map_attn(void* map_out, const void* base, bool bf16, uint64_t dim, u
   return r == CUDA_SUCCESS;
 }
 
-bool tensor_map_fp8_codes(void* map_out, const KvFp8Part& p, int32_t head_dim, int32_t heads, int32_t page_size,
-                          int32_t n_pages, int32_t width, int32_t granule) {
+bool tensor_map_fp8_codes(void* map_out, const KvFp8Part& p, int32_t dim, int32_t heads, int32_t page_size,
+                          int32_t n_pages, int32_t width, int32_t box_heads, int32_t granule) {
   if (!have_encoder()) return false;
   // a dimension of one element has no step: any stride that the encoder accepts will do
-  auto step = [&](int32_t n, int64_t stride) { return static_cast<cuuint64_t>(n > 1 ? stride : head_dim); };
-  const cuuint64_t dims[4] = {cuuint64_t(head_dim), cuuint64_t(heads), cuuint64_t(page_size), cuuint64_t(n_pages)};
+  auto step = [&](int32_t n, int64_t stride) { return static_cast<cuuint64_t>(n > 1 ? stride : dim); };
+  const cuuint64_t dims[4] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(page_size), cuuint64_t(n_pages)};
   const cuuint64_t strides[3] = {step(heads, p.head), step(page_size, p.slot), step(n_pages, p.page)};
-  const cuuint32_t box[4] = {cuuint32_t(width), 1, cuuint32_t(granule), 1};
+  const cuuint32_t box[4] = {cuuint32_t(width), cuuint32_t(box_heads), cuuint32_t(granule), 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   return g_encode(static_cast<CUtensorMap*>(map_out), CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, p.codes, dims, strides, box,
                   estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   width == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                  // a row is no longer: with 256 its neighbour's, another head's, came along unread
-                  width == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+                  // no longer than a box's row or rows: with 256 another head's came along unread
+                  width * box_heads == 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                  : width * box_heads == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                             : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

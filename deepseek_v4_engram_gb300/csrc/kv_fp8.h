@@ -40,16 +40,27 @@ cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const Kv
 // Items of up to 256 rows (attn_fp8_tiles_sm103.cu).
 cudaError_t launch_attn_fp8_tiles(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, cudaStream_t st);
 
-// Tensor map (capi.cu) of an 8-bit cache's codes, element (d, head, slot, page) in boxes of 64 or 128
-// columns by `granule` slots with the swizzle of that width; columns past head_dim read as zero.
-bool tensor_map_fp8_codes(void* map_out, const KvFp8Part& p, int32_t head_dim, int32_t heads, int32_t page_size,
-                          int32_t n_pages, int32_t width, int32_t granule);
+// Tensor map (capi.cu) of an 8-bit cache's codes, element (d, head, slot, page) in boxes of `width` (64 or 128)
+// columns by `box_heads` heads by `granule` slots with the swizzle of that width; columns past `dim` read as
+// zero.
+bool tensor_map_fp8_codes(void* map_out, const KvFp8Part& p, int32_t dim, int32_t heads, int32_t page_size,
+                          int32_t n_pages, int32_t width, int32_t box_heads, int32_t granule);
 
-// Those of the keys and the values.
-inline bool attn_fp8_tensor_maps(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, CUtensorMap (&tm)[2]) {
-  const int32_t heads = a.plan.kv_heads, width = attn_width(a.head_dim);
-  return tensor_map_fp8_codes(&tm[0], k, a.head_dim, heads, a.page_size, a.n_pages, width, a.granule) &&
-         tensor_map_fp8_codes(&tm[1], v, a.head_dim, heads, a.page_size, a.n_pages, width, a.granule);
+// Those of the keys and the values, for items of `item_heads` heads (1 or 2), of which the call has
+// a.plan.kv_heads. Two heads of 64 columns are one of 128: they have to lie beside each other.
+inline bool attn_fp8_tensor_maps(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t item_heads,
+                                 CUtensorMap (&tm)[2]) {
+  const int32_t width = attn_width(a.head_dim);
+  const bool merged = item_heads == 2 && width == 64;
+  for (int i = 0; i < 2; ++i) {
+    KvFp8Part p = i == 0 ? k : v;
+    if (merged) p.head *= 2;
+    if (!tensor_map_fp8_codes(&tm[i], p, merged ? 128 : a.head_dim,
+                              merged ? a.plan.kv_heads : a.plan.kv_heads * item_heads, a.page_size, a.n_pages,
+                              merged ? 128 : width, merged ? 1 : item_heads, a.granule))
+      return false;
+  }
+  return true;
 }
 
 }  // namespace engram
