@@ -17,37 +17,42 @@ from ._lib import EngramAttnDesc
 from .api import _check, lib
 from .attn import _TORCH, _device, _ints, _lse, _refuse, _scratch, _sequences, _stream, _view
 
-_CODES = (torch.uint8, torch.float8_e4m3fn)
-_SCALES = (torch.uint8, torch.float8_e8m0fnu)
+_U8, _CODES, _SCALES, _INT = torch.uint8, torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.int32
 _pack_cache = _lib.PACK_CACHE_FP8.pack
 
 
 def _cache(desc: EngramAttnDesc, k_cache, v_cache, k_scale, v_scale, block_table, device: int, n_seqs: int):
-    tensors = (k_cache, v_cache, k_scale, v_scale, block_table)
+    if (isinstance(k_cache, torch.Tensor) and isinstance(v_cache, torch.Tensor) and isinstance(k_scale, torch.Tensor)
+            and isinstance(v_scale, torch.Tensor) and isinstance(block_table, torch.Tensor)
+            and k_cache.get_device() == device and v_cache.get_device() == device and k_scale.get_device() == device
+            and v_scale.get_device() == device and block_table.get_device() == device):
+        codes, scales, shape, table = k_cache.dtype, k_scale.dtype, k_cache.shape, block_table.shape
+        if ((codes is _U8 or codes is _CODES) and v_cache.dtype is codes and (scales is _U8 or scales is _SCALES)
+                and v_scale.dtype is scales and block_table.dtype is _INT and len(shape) == 4 and len(table) == 2):
+            pages, page_size, heads, dim = shape
+            n, width = table
+            if (heads == desc.n_kv_heads and dim == desc.head_dim and n == n_seqs and v_cache.shape == shape
+                    and k_scale.shape == (pages, heads, page_size) and v_scale.shape == k_scale.shape
+                    and block_table.is_contiguous()):
+                k0, k1, k2, k3 = k_cache.stride()
+                v0, v1, v2, v3 = v_cache.stride()
+                a0, a1, a2 = k_scale.stride()
+                b0, b1, b2 = v_scale.stride()
+                if k3 == 1 and v3 == 1 and a2 == 1 and b2 == 1:
+                    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                       k0, k1, k2, v0, v1, v2, a0, a1, b0, b1, pages, page_size,
+                                       block_table.data_ptr(), width)
+    name = "k_cache, v_cache, k_scale, v_scale and block_table"
     want = (f"[pages, page_size, {desc.n_kv_heads}, {desc.head_dim}] whose last dimension is dense, keys and values "
             f"alike, with scales [pages, {desc.n_kv_heads}, page_size] whose last dimension is dense and a contiguous "
             f"int32 block_table [{n_seqs}, width]")
-    name = "k_cache, v_cache, k_scale, v_scale and block_table"
-    for t in tensors:
+    for t in (k_cache, v_cache, k_scale, v_scale, block_table):
         if not isinstance(t, torch.Tensor) or t.get_device() != device:
-            _refuse(t, name, want, "float8_e4m3fn", device)
-    shape, table = k_cache.shape, block_table.shape
-    if (k_cache.dtype in _CODES and v_cache.dtype is k_cache.dtype and k_scale.dtype in _SCALES
-            and v_scale.dtype is k_scale.dtype and block_table.dtype is torch.int32 and len(shape) == 4
-            and shape[2] == desc.n_kv_heads and shape[3] == desc.head_dim and v_cache.shape == shape
-            and k_scale.shape == (shape[0], shape[2], shape[1]) and v_scale.shape == k_scale.shape
-            and len(table) == 2 and table[0] == n_seqs and block_table.is_contiguous()):
-        k0, k1, k2, k3 = k_cache.stride()
-        v0, v1, v2, v3 = v_cache.stride()
-        a0, a1, a2 = k_scale.stride()
-        b0, b1, b2 = v_scale.stride()
-        if k3 == 1 and v3 == 1 and a2 == 1 and b2 == 1:
-            return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), k0, k1,
-                               k2, v0, v1, v2, a0, a1, b0, b1, shape[0], shape[1], block_table.data_ptr(), table[1])
-    for t in tensors:   # the one to name: whose type is wrong, else the keys
-        if t.dtype not in (*_CODES, *_SCALES, torch.int32):
-            _refuse(t, name, want, "float8_e4m3fn", device)
-    _refuse(k_cache, name, want, "float8_e4m3fn", device)
+            _refuse(t, name, want, "float8_e4m3fn or uint8", device)
+    for t, of in ((v_cache, k_cache), (v_scale, k_scale)):   # the one to name: keys, unless the values differ
+        if t.dtype is not of.dtype or t.shape != of.shape:
+            _refuse(t, name, want, "float8_e4m3fn or uint8", device)
+    _refuse(k_cache, name, want, "float8_e4m3fn or uint8", device)
 
 
 def engram_kv_append_fp8(desc: EngramAttnDesc, k, v, cu_seqlens, kv_len, block_table, k_cache, v_cache, k_scale,

@@ -30,7 +30,7 @@ namespace engram {
 namespace {
 
 constexpr int kConsumers = 8;
-constexpr int kExtraUnits = 1;   // an item's fixed time, in key tiles
+constexpr int kExtraUnits = 2;   // an item's fixed time, in key tiles
 constexpr int kThreads = (kConsumers + 4) * 32;
 // 256 * 232 + 128 * 40 = 384 * 168
 constexpr int kConsumerRegs = 232, kProducerRegs = 40;
@@ -50,7 +50,7 @@ constexpr int kSumDrop = 6;
 template <int DH, int NT, int kHeads>
 struct Geo {
   static constexpr int kHeadRows = 8 * NT, kRows = kHeads * kHeadRows;
-  static constexpr int kKeys = DH == 128 && kHeads == 2 ? 64 : kTileKeys;   // of a stage
+  static constexpr int kKeys = DH == 128 && kHeads == 2 && NT > 2 ? 64 : kTileKeys;   // of a stage
   static constexpr int kTensorBytes = kKeys * kHeads * DH;                  // codes of K or V of a stage
   static constexpr int kScaleBytes = kKeys * kHeads;
   static constexpr int kJoinRow = DH + 4;
@@ -58,7 +58,7 @@ struct Geo {
   static constexpr int kJoinBytes = kConsumers * kJoinRows * kJoinRow * 4;
   static constexpr bool kQueriesShared = NT == 4;                      // else in registers
   static constexpr int kQueryBytes = kQueriesShared ? DH / 16 * NT * kHeads * 32 * 8 : 0;
-  static constexpr int kStages = kTensorBytes == 16384 ? (NT == 1 ? 5 : 4) : 8;
+  static constexpr int kStages = kTensorBytes == 32768 ? 2 : kTensorBytes == 16384 ? (NT == 1 ? 5 : 4) : 8;
 };
 
 template <int DH, int NT, int kHeads>
@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using G = Geo<DH, NT, kHeads>;
   constexpr int kStagesPerTile = kTileKeys / G::kKeys;
   constexpr int kWarpKeys = G::kKeys * kHeads / kConsumers;   // of a stage: 16 or 32
+  constexpr int U = NT == 4 ? 1 : kWarpKeys / 16;   // times 16 keys at once, whose chains of steps overlap
   constexpr int kSteps = DH / 16;   // of a score's contraction; and tiles of V^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
@@ -336,88 +337,110 @@ __global__ void __launch_bounds__(kThreads, 1)
            first += G::kKeys) {
         const bool here = !__any_sync(0xFFFFFFFFu, !attn_wait(&sh->full[stage], phase, abort));
 #pragma unroll 1
-        for (int step = 0; step < kWarpKeys; step += 16) {
-          const int32_t key0 = first + keys_at + step;
+        for (int step = 0; step < kWarpKeys; step += 16 * U) {
+          const int32_t key0 = first + keys_at + step;   // of U times 16
           if (!here || key0 >= seg.keys) break;
           const uint8_t* sk = smem + stage * 2 * G::kTensorBytes + step * kKeyBytes;
           const uint8_t* sv = sk + G::kTensorBytes;
           const uint8_t* ss = scales + stage * 2 * G::kScaleBytes + step;
-          // ---- scores of 16 keys by the rows
-          float s[NT][4] = {};
+          // ---- scores of 16 U keys by the rows
+          float s[U][NT][4] = {};
 #pragma unroll
           for (int half = 0; half < DH / 64; ++half) {
-            const uint4 lo = *reinterpret_cast<const uint4*>(sk + (k_off ^ (half * 64)));
-            const uint4 hi = *reinterpret_cast<const uint4*>(sk + (k_off ^ (half * 64)) + 8 * kKeyBytes);
-            const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+            uint32_t wl[U][4], wh[U][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t f[4] = {codes_lo(wl[i]), codes_lo(wh[i]), codes_hi(wl[i]), codes_hi(wh[i])};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                uint2 q;
-                if constexpr (G::kQueriesShared) q = queries[(((half * 4 + i) * kHeads + sub) * NT + nt) * 32 + lane];
-                else q = qf[nt][half * 4 + i];
-                mma_f16(s[nt], f, q.x, q.y);
-              }
+            for (int u = 0; u < U; ++u) {
+              const uint8_t* at = sk + u * 16 * kKeyBytes + (k_off ^ (half * 64));
+              const uint4 lo = *reinterpret_cast<const uint4*>(at);
+              const uint4 hi = *reinterpret_cast<const uint4*>(at + 8 * kKeyBytes);
+              wl[u][0] = lo.x, wl[u][1] = lo.y, wl[u][2] = lo.z, wl[u][3] = lo.w;
+              wh[u][0] = hi.x, wh[u][1] = hi.y, wh[u][2] = hi.z, wh[u][3] = hi.w;
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int u = 0; u < U; ++u) {
+                const uint32_t f[4] = {codes_lo(wl[u][i]), codes_lo(wh[u][i]), codes_hi(wl[u][i]), codes_hi(wh[u][i])};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  uint2 q;
+                  if constexpr (G::kQueriesShared)
+                    q = queries[(((half * 4 + i) * kHeads + sub) * NT + nt) * 32 + lane];
+                  else
+                    q = qf[nt][half * 4 + i];
+                  mma_f16(s[u][nt], f, q.x, q.y);
+                }
+              }
           }
           // ---- values: four rows of 16 (8) columns, pairs of rows to be interleaved
           constexpr int kWords = DH / 32;
-          uint32_t v[4][kWords];
-          {
+          uint32_t v[U][4][kWords];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
             const uint32_t at[4] = {va_off, vb_off, va_off + 8 * kKeyBytes, vb_off + 8 * kKeyBytes};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
+              const uint8_t* from = sv + u * 16 * kKeyBytes + at[i];
               if constexpr (DH == 128) {
-                const uint4 w = *reinterpret_cast<const uint4*>(sv + at[i]);
-                v[i][0] = w.x;
-                v[i][1] = w.y;
-                v[i][2] = w.z;
-                v[i][3] = w.w;
+                const uint4 w = *reinterpret_cast<const uint4*>(from);
+                v[u][i][0] = w.x, v[u][i][1] = w.y, v[u][i][2] = w.z, v[u][i][3] = w.w;
               } else {
-                const uint2 w = *reinterpret_cast<const uint2*>(sv + at[i]);
-                v[i][0] = w.x;
-                v[i][1] = w.y;
+                const uint2 w = *reinterpret_cast<const uint2*>(from);
+                v[u][i][0] = w.x, v[u][i][1] = w.y;
               }
             }
           }
-          const float kf[2] = {fp8_scale_value(ss[scale0]), fp8_scale_value(ss[scale0 + 8])};
-          uint32_t vb8[2] = {ss[G::kScaleBytes + scale0], ss[G::kScaleBytes + scale0 + 8]};   // the values' bytes
-          if (__any_sync(0xFFFFFFFFu, vb8[0] == kNanScale || vb8[1] == kNanScale)) {   // rare: NaN codes instead
+          // ---- scales: a lane's keys are kg and kg + 8 of each 16
+          float kf[2 * U];
+          uint32_t vb8[2 * U];   // the values' bytes
+          bool not_numbers = false;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int key = keys_at + (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
-              if (ss[G::kScaleBytes + sub * G::kKeys + key] == kNanScale)
-#pragma unroll
-                for (int w = 0; w < kWords; ++w) v[i][w] = 0x7F7F7F7Fu;
-            }
-            vb8[0] = vb8[0] == kNanScale ? 127u : vb8[0];
-            vb8[1] = vb8[1] == kNanScale ? 127u : vb8[1];
+          for (int i = 0; i < 2 * U; ++i) {
+            kf[i] = fp8_scale_value(ss[scale0 + 8 * i]);
+            vb8[i] = ss[G::kScaleBytes + scale0 + 8 * i];
+            not_numbers |= vb8[i] == kNanScale;
           }
-          float ve[2], unscale[2];   // exponents, and 2^-(v + kSumDrop)
+          if (__any_sync(0xFFFFFFFFu, not_numbers)) {   // rare: NaN codes instead
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int key = keys_at + u * 16 + (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
+                if (ss[G::kScaleBytes + sub * G::kKeys + key] == kNanScale)
+#pragma unroll
+                  for (int w = 0; w < kWords; ++w) v[u][i][w] = 0x7F7F7F7Fu;
+              }
+#pragma unroll
+            for (int i = 0; i < 2 * U; ++i) vb8[i] = vb8[i] == kNanScale ? 127u : vb8[i];
+          }
+          float ve[2 * U], unscale[2 * U];   // exponents, and 2^-(v + kSumDrop)
+#pragma unroll
+          for (int i = 0; i < 2 * U; ++i) {
             ve[i] = static_cast<float>(static_cast<int>(max(vb8[i], kMinScale)) - 127);
             unscale[i] = __uint_as_float((254u - kSumDrop - min(max(vb8[i], kMinScale), 247u)) << 23);
           }
-          const bool edge = key0 + 16 > seg.first;   // some row does not see all of them
-          float y[NT][4];
+          const bool edge = key0 + 16 * U > seg.first;   // some row does not see all of them
           bool over = false;
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int j = e & 1, k = e >> 1;
-              const bool hidden = edge && key0 + kg + 8 * k >= limit[nt][j];
-              y[nt][e] = hidden ? -INFINITY : fmaf(s[nt][e], rc[nt][j] * kf[k], ve[k]);
-              over |= y[nt][e] > base[nt][j] + (kLift + kSlack);
-            }
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int j = e & 1, k = 2 * u + (e >> 1);
+                const bool hidden = edge && key0 + kg + 8 * k >= limit[nt][j];
+                float& y = s[u][nt][e];
+                y = hidden ? -INFINITY : fmaf(y, rc[nt][j] * kf[k], ve[k]);
+                over |= y > base[nt][j] + (kLift + kSlack);
+              }
           if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                float m = fmaxf(y[nt][j], y[nt][2 + j]);
+                float m = -INFINITY;
+#pragma unroll
+                for (int u = 0; u < U; ++u) m = fmaxf(m, fmaxf(s[u][nt][j], s[u][nt][2 + j]));
                 m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
                 m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
                 m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
@@ -432,19 +455,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
               }
           }
-          uint32_t p[NT][2];
+          uint32_t p[U][NT][2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float e[4];
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float b = base[nt][i & 1] == -INFINITY ? 0.f : base[nt][i & 1];
-              e[i] = exp2_fast(min_nan(y[nt][i] - b, kMostExponent));
-              sum[nt][i & 1] = fmaf(e[i], unscale[i >> 1], sum[nt][i & 1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              float e[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float b = base[nt][i & 1] == -INFINITY ? 0.f : base[nt][i & 1];
+                e[i] = exp2_fast(min_nan(s[u][nt][i] - b, kMostExponent));
+                sum[nt][i & 1] = fmaf(e[i], unscale[2 * u + (i >> 1)], sum[nt][i & 1]);
+              }
+              p[u][nt][0] = transpose8x8(pack16x2<false>(e[0], e[1]));
+              p[u][nt][1] = transpose8x8(pack16x2<false>(e[2], e[3]));
             }
-            p[nt][0] = transpose8x8(pack16x2<false>(e[0], e[1]));
-            p[nt][1] = transpose8x8(pack16x2<false>(e[2], e[3]));
-          }
           // ---- a probability of 0 does not undo a NaN that it multiplies: the codes of values past the
           // last key are cleared; NaN codes of values that only some rows see are taken out, and noted for
           // the rows that do see them
@@ -452,46 +477,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (edge) {
             const int32_t pair_key[4] = {va, vb, va + 8, vb + 8};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-              for (int w = 0; w < kWords; ++w) {
-                if (key0 + pair_key[i] >= seg.keys) v[i][w] = 0;
-                poison |= nan_codes(v[i][w]);
-              }
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                  if (key0 + u * 16 + pair_key[i] >= seg.keys) v[u][i][w] = 0;
+                  poison |= nan_codes(v[u][i][w]);
+                }
           }
           if (__any_sync(0xFFFFFFFFu, poison != 0)) {   // rare
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int32_t key = key0 + (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
-              uint32_t columns = 0;   // of the lane's 4 kWords
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-              for (int w = 0; w < kWords; ++w) {
-                const uint32_t n = nan_codes(v[i][w]) >> 7;   // 1 in such a byte
-                v[i][w] &= ~(n * 0xFFu);
-                columns |= ((n | n >> 7 | n >> 14 | n >> 21) & 15u) << (4 * w);
-              }
-              if (columns == 0) continue;
-              sh->poisoned = 1;
-              const int bit = g * (DH / 8);
+              for (int i = 0; i < 4; ++i) {
+                const int32_t key = key0 + u * 16 + (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
+                uint32_t columns = 0;   // of the lane's 4 kWords
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                  const uint32_t n = nan_codes(v[u][i][w]) >> 7;   // 1 in such a byte
+                  v[u][i][w] &= ~(n * 0xFFu);
+                  columns |= ((n | n >> 7 | n >> 14 | n >> 21) & 15u) << (4 * w);
+                }
+                if (columns == 0) continue;
+                sh->poisoned = 1;
+                const int bit = g * (DH / 8);
 #pragma unroll 1
-              for (int r = 0; r < seg.ntok * group; ++r)
-                if (key < seg.first + r / group)
-                  atomicOr(&sh->poison[sub * G::kHeadRows + r][bit / 32], columns << (bit % 32));
-            }
+                for (int r = 0; r < seg.ntok * group; ++r)
+                  if (key < seg.first + r / group)
+                    atomicOr(&sh->poison[sub * G::kHeadRows + r][bit / 32], columns << (bit % 32));
+              }
           }
           // ---- products with the values
 #pragma unroll
-          for (int w = 0; w < kWords; ++w) {
-            const uint32_t l0 = __byte_perm(v[0][w], v[1][w], sel_lo), h0 = __byte_perm(v[0][w], v[1][w], sel_hi);
-            const uint32_t l1 = __byte_perm(v[2][w], v[3][w], sel_lo), h1 = __byte_perm(v[2][w], v[3][w], sel_hi);
-            const uint32_t fl[4] = {codes_lo(l0), codes_hi(l0), codes_lo(l1), codes_hi(l1)};
-            const uint32_t fh[4] = {codes_lo(h0), codes_hi(h0), codes_lo(h1), codes_hi(h1)};
+          for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_f16(o[nt][2 * w], fl, p[nt][0], p[nt][1]);
-              mma_f16(o[nt][2 * w + 1], fh, p[nt][0], p[nt][1]);
+            for (int w = 0; w < kWords; ++w) {
+              const uint32_t l0 = __byte_perm(v[u][0][w], v[u][1][w], sel_lo);
+              const uint32_t h0 = __byte_perm(v[u][0][w], v[u][1][w], sel_hi);
+              const uint32_t l1 = __byte_perm(v[u][2][w], v[u][3][w], sel_lo);
+              const uint32_t h1 = __byte_perm(v[u][2][w], v[u][3][w], sel_hi);
+              const uint32_t fl[4] = {codes_lo(l0), codes_hi(l0), codes_lo(l1), codes_hi(l1)};
+              const uint32_t fh[4] = {codes_lo(h0), codes_hi(h0), codes_lo(h1), codes_hi(h1)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                mma_f16(o[nt][2 * w], fl, p[u][nt][0], p[u][nt][1]);
+                mma_f16(o[nt][2 * w + 1], fh, p[u][nt][0], p[u][nt][1]);
+              }
             }
-          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh->empty[stage]);
@@ -606,7 +639,7 @@ cudaError_t launch_any(AttnArgs a, const KvFp8Part& k, const KvFp8Part& v, cudaS
   a.plan.tokens = 8 * NT * kHeads / a.group;
   a.plan.workers = device_sm_count();
   a.plan.extra = kExtraUnits;
-  if (kHeads == 2 && width == 128 && a.granule > 64) a.granule = 64;
+  if (kHeads == 2 && width == 128 && NT > 2 && a.granule > 64) a.granule = 64;   // a stage's keys
   alignas(64) CUtensorMap tm[2];
   if (!attn_fp8_tensor_maps(a, k, v, kHeads, tm)) return cudaErrorInvalidValue;
   cudaError_t e;
@@ -626,9 +659,14 @@ cudaError_t launch_heads(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part&
 
 cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows,
                                  cudaStream_t st) {
-  // Two key-value heads an item where they lie beside each other in memory.
+  // Two key-value heads an item where they lie beside each other in memory: TMA then takes rows twice as long,
+  // and memory pieces of 256 bytes. (24 caches of 100-7061 positions with 16 heads of 64: 63 us with one, 45
+  // with two; 4 of 70001-131072 with 8 heads of 128: 146 and 144.) But not where even tables that are full leave
+  // SMs without a tile of one head: one token over 511 positions 8.0 us with one, 8.7 with two.
   const int64_t width = attn_width(a.head_dim);
-  const bool two = a.plan.kv_heads % 2 == 0 && a.head_dim == width && k.head == width && v.head == width;
+  const int64_t most = int64_t(a.plan.n_seqs) * a.plan.kv_heads * ((a.plan.kv_cap + kTileKeys - 1) / kTileKeys);
+  const bool two = a.plan.kv_heads % 2 == 0 && a.head_dim == width && k.head == width && v.head == width &&
+                   most > device_sm_count();
   return rows <= 8    ? launch_heads<1>(a, k, v, two, st)
          : rows <= 16 ? launch_heads<2>(a, k, v, two, st)
                       : launch_heads<4>(a, k, v, two, st);
