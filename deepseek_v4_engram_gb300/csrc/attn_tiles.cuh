@@ -90,6 +90,10 @@ constexpr int kPoisonSlots = 8;
 // Of a tile's probabilities against an older maximum. With 1, where nearly every tile looks for its
 // maximum, the prompt of 16384 tokens took 1093 us instead of 661.
 constexpr float kMostSum = 512.f;
+// Over an 8-bit cache in bf16, whose keys' sizes differ more from row to row in the cases measured: 512 has a
+// quarter of the tiles find their maximum (chunks of 1024 and 300 tokens beside six single ones 215 us), this
+// hardly any (205). Sums stay finite for values up to 2^100.
+constexpr float kMostSumFp8 = 65536.f;
 // Probabilities are rounded to the values' type for the product with them, since the MMA takes both
 // operands in one 16-bit type: each by half a unit in its last place, as the result is at the end.
 // They are summed as they are, so what rounding takes from a small one is lost, and a long cache may
@@ -97,8 +101,8 @@ constexpr float kMostSum = 512.f;
 // kMostSum of it below f16's largest value. bf16 has the exponents of f32.
 template <bool kBf16>
 constexpr float kLift = kBf16 ? 0.f : 6.f;
-template <bool kBf16>
-constexpr float kMostLifted = kBf16 ? kMostSum : kMostSum * 64.f;
+template <bool kBf16, class Kv>
+constexpr float kMostLifted = !kBf16 ? kMostSum * 64.f : Kv::kFp8 ? kMostSumFp8 : kMostSum;
 // The maximum is subtracted in the multiply-add that scales a score, so the rounding of its product stays in
 // the difference: from here on (2^24 in units of log2) it is subtracted first.
 constexpr float kFarScore = 16777216.f;
@@ -259,6 +263,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
@@ -328,9 +337,12 @@ __device__ __forceinline__ void scaled16x4(uint32_t codes, uint32_t scale, uint3
   if constexpr (kBf16) {
     const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
     const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    const float f = __uint_as_float(scale);
-    lo = pack16x2<true>(x.x * f, x.y * f);
-    hi = pack16x2<true>(y.x * f, y.y * f);
+    const uint64_t f = pair(__uint_as_float(scale), __uint_as_float(scale));
+    float p, q;
+    unpair(mul2(pair(x.x, x.y), f), p, q);
+    lo = pack16x2<true>(p, q);
+    unpair(mul2(pair(y.x, y.y), f), p, q);
+    hi = pack16x2<true>(p, q);
   } else {
     asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(scale));
     asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(scale));
@@ -638,7 +650,7 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
             float x, y;
             unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
             sums = x + y;
-            if (fresh || !__any_sync(0xFFFFFFFFu, sums > kMostLifted<kBf16> || (m == -INFINITY && left > 0)))
+            if (fresh || !__any_sync(0xFFFFFFFFu, sums > kMostLifted<kBf16, Kv> || (m == -INFINITY && left > 0)))
               break;
             fresh = true;
           }
