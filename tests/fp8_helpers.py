@@ -22,12 +22,13 @@ def rows(shape, seed, dtype=torch.bfloat16, spread=1.0):
 
 class PagedFp8:
     """A paged 8-bit cache whose pages are shuffled. Slots that no position owns hold NaN codes and NaN
-    scales, page table entries past a sequence's end pages that do not exist."""
+    scales, page table entries past a sequence's end (`columns` more than the longest has) pages that do
+    not exist."""
 
     def __init__(self, kv_lens, page, kv_heads, head_dim, seed, layout="nhd", spare=3, spread=1.0,
-                 dtype=torch.bfloat16, device="cuda"):
+                 dtype=torch.bfloat16, device="cuda", columns=2):
         need = [-(-max(n, 0) // page) for n in kv_lens]
-        pages, width = sum(need) + spare, max(need + [1]) + 2
+        pages, width = sum(need) + spare, max(need + [1]) + columns
         kw = dict(dtype=torch.uint8, device=device)
         if layout == "pool":        # a page's codes and scales one after the other, in one buffer
             part = page * kv_heads * head_dim
@@ -162,8 +163,8 @@ def run(cache, q_lens, heads, head_dim, dtype, seed=2, max_q=None, stream=None, 
     return q, out, lse
 
 
-def check(q_lens, kv_lens, page, heads, kv_heads, head_dim, dtype, seed=2, layout="nhd", spread=1.0, **kw):
-    cache = PagedFp8(kv_lens, page, kv_heads, head_dim, seed, layout, spread=spread)
+def check(q_lens, kv_lens, page, heads, kv_heads, head_dim, dtype, seed=2, layout="nhd", spread=1.0, columns=2, **kw):
+    cache = PagedFp8(kv_lens, page, kv_heads, head_dim, seed, layout, spread=spread, columns=columns)
     q, out, lse = run(cache, q_lens, heads, head_dim, dtype, seed, **kw)
     assert eg.engram_check_errors() == 0
     scale, at = kw.get("scale") or 1 / math.sqrt(head_dim), 0

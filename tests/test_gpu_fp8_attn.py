@@ -56,6 +56,27 @@ def test_chunks(q_lens, kv_lens, heads, kv_heads, dtype):
     check(q_lens, kv_lens, 32, heads, kv_heads, 128, dtype, seed=5)
 
 
+@pytest.mark.parametrize("head_dim,dtype", [(64, BF16), (128, BF16), (128, F16), (64, F16)])
+@pytest.mark.parametrize("q_lens,heads,kv_heads", [
+    ([1, 1, 1], 4, 4), ([1, 1, 1], 20, 4), ([1, 1, 1], 2, 2), ([4, 1, 2], 8, 4), ([3, 0, 5], 6, 2), ([2, 2, 2], 32, 2),
+    ([8, 3, 1], 8, 2), ([1, 1, 1], 64, 2)])
+@pytest.mark.parametrize("page", [16, 48, 128])
+def test_items_of_one_and_of_two_heads(q_lens, heads, kv_heads, head_dim, dtype, page):
+    # an even number of heads that lie beside each other, few and many positions that the table could hold
+    for columns in (2, 4000):
+        check(q_lens, [517, 3, 1030], page, heads, kv_heads, head_dim, dtype, seed=6, columns=columns)
+    # a cache that many items share, and one that ends in the middle of every part of a tile
+    check(q_lens[:1], [9000 + 17 * kv_heads], page, heads, kv_heads, head_dim, dtype, seed=7, columns=4000)
+
+
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("m", [1, 15, 16, 17, 31, 33, 63, 64, 65, 95, 97, 111, 127, 128, 129, 161, 191, 193, 255, 257])
+def test_ends_inside_a_tile(m, head_dim):
+    for q_len in (1, 3):
+        check([q_len, 1], [m, 2], 16, 4, 2, head_dim, BF16, seed=9, columns=4000)
+        check([q_len, 1], [m, 2], 16, 3, 1, head_dim, BF16, seed=9)
+
+
 def test_long_cache_is_shared_between_sms():
     check([1, 1], [40000, 3], 64, 4, 2, 64, BF16, seed=6)
     check([6], [30001], 48, 8, 1, 128, F16, seed=6)
@@ -122,8 +143,9 @@ def test_much_weight_in_small_probabilities(q_len, dtype):
 @pytest.mark.parametrize("where", ["scale", "code"])
 @pytest.mark.parametrize("which", ["k", "v"])
 @pytest.mark.parametrize("q_len,at", [(1, 399), (4, 399), (4, 397), (100, 399), (100, 340), (100, 5)])
-def test_nan_reaches_only_the_rows_that_see_it(q_len, at, which, where):
-    cache = PagedFp8([400], 16, 2, 64, 8)
+@pytest.mark.parametrize("columns", [2, 4000])
+def test_nan_reaches_only_the_rows_that_see_it(q_len, at, which, where, columns):
+    cache = PagedFp8([400], 16, 2, 64, 8, columns=columns)
     clean = run(cache, [q_len], 4, 64, BF16, 9)
     page, slot = cache.place(0, at, 1)
     if where == "scale":
