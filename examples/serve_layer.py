@@ -1,10 +1,11 @@
 """The Engram block and an attention beside it, served together: a batch of prompts, then one or several
 tokens per sequence and step.
 
-    python examples/serve_layer.py
+    python examples/serve_layer.py [--eight-bits]
 
 One length array serves both caches: engram_forward appends the tokens to its look-back cache and
-advances cache_len, and that same array is the kv_len of engram_kv_append and engram_attn_paged. Random
+advances cache_len, and that same array is the kv_len of engram_kv_append and engram_attn_paged, or of
+engram_kv_append_fp8 and engram_attn_paged_fp8 where the attention's cache is kept in eight bits. Random
 weights; the projections around the attention are plain matrix products.
 """
 from __future__ import annotations
@@ -32,7 +33,7 @@ class Layer:
     """The block's tables and weights, the attention's projection, and both caches of a batch."""
 
     def __init__(self, geom: synth.Geometry, heads: int, kv_heads: int, head_dim: int, batch: int,
-                 capacity: int, page: int, seed: int = 1):
+                 capacity: int, page: int, seed: int = 1, eight_bits: bool = False):
         m = synth.make_model(geom, seed)
         t = m.tables
         self.geom, self.heads, self.kv_heads, self.head_dim = geom, heads, kv_heads, head_dim
@@ -52,9 +53,13 @@ class Layer:
         self.started = False    # whether the caches hold anything
         # pages of the attention's cache, dealt to the sequences in turn
         per_seq = -(-capacity // page)
-        shape = (batch * per_seq, page, kv_heads, head_dim)
-        self.k_cache = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
-        self.v_cache = torch.empty(shape, dtype=torch.bfloat16, device="cuda")
+        pages = batch * per_seq
+        shape, kind = (pages, page, kv_heads, head_dim), torch.float8_e4m3fn if eight_bits else torch.bfloat16
+        self.eight_bits = eight_bits
+        self.cache = tuple(torch.empty(shape, dtype=kind, device="cuda") for _ in range(2))   # keys, values
+        if eight_bits:      # and a scale for each of their rows, in the order in which heads read them
+            self.cache += tuple(torch.empty((pages, kv_heads, page), dtype=torch.float8_e8m0fnu, device="cuda")
+                                for _ in range(2))
         self.table = torch.arange(batch * per_seq, dtype=torch.int32, device="cuda").view(per_seq, batch)
         self.table = self.table.t().contiguous()
         self.scratch = torch.empty(eg.engram_attn_workspace_size(self.attn), dtype=torch.uint8, device="cuda")
@@ -75,20 +80,31 @@ class Layer:
         q, k, v = qkv.split([self.heads, self.kv_heads, self.kv_heads], 1)
         out = torch.empty((B * T, self.heads, self.head_dim), dtype=torch.bfloat16, device="cuda")
         cu = torch.arange(0, B * T + 1, T, dtype=torch.int32, device="cuda")
-        paged = (cu, self.length, self.table, self.k_cache, self.v_cache)
-        eg.engram_kv_append(self.attn, k, v, *paged)
+        paged = (cu, self.length, self.table, *self.cache)
+        (eg.engram_kv_append_fp8 if self.eight_bits else eg.engram_kv_append)(self.attn, k, v, *paged)
         if first:
             eg.engram_attn_prompt(self.attn, q, k, v, cu, out, workspace=self.scratch)
         else:
-            eg.engram_attn_paged(self.attn, q, *paged, out, T, workspace=self.scratch)
+            attend = eg.engram_attn_paged_fp8 if self.eight_bits else eg.engram_attn_paged
+            attend(self.attn, q, *paged, out, T, workspace=self.scratch)
         return streams, q, k, v, out
+
+    def cached(self, n: int):
+        """The keys and values [B * n, kv_heads, head_dim] of each sequence's last n positions, as the 8-bit cache
+        holds them."""
+        B = self.length.numel()
+        k, v = (torch.empty((B * n, self.kv_heads, self.head_dim), dtype=torch.bfloat16, device="cuda")
+                for _ in range(2))
+        cu = torch.arange(0, B * n + 1, n, dtype=torch.int32, device="cuda")
+        eg.engram_kv_read_fp8(self.attn, cu, self.length, self.table, *self.cache, k, v)
+        return k, v
 
 
 def serve(batch: int = 3, prompt: int = 40, steps: int = 4, heads: int = 8, kv_heads: int = 2,
-          head_dim: int = 64, page: int = 16, seed: int = 1):
+          head_dim: int = 64, page: int = 16, seed: int = 1, eight_bits: bool = False):
     """A prompt and `steps` decoding steps; returns the layer and what each call of step() returned."""
     geom = synth.TINY
-    layer = Layer(geom, heads, kv_heads, head_dim, batch, prompt + steps, page, seed)
+    layer = Layer(geom, heads, kv_heads, head_dim, batch, prompt + steps, page, seed, eight_bits)
     got = []
     for i, n in enumerate([prompt] + [1] * steps):
         b = synth.make_batch(geom, batch, n, seed + 10 + i)
@@ -100,7 +116,7 @@ def serve(batch: int = 3, prompt: int = 40, steps: int = 4, heads: int = 8, kv_h
 
 
 if __name__ == "__main__":
-    layer, got = serve()
+    layer, got = serve(eight_bits="--eight-bits" in sys.argv[1:])
     print("lengths", layer.length.tolist())
     for i, (streams, q, k, v, out) in enumerate(got):
         print("prompt" if i == 0 else f"step {i}", "out", list(out.shape), "rms %.4f" % out.float().pow(2).mean().sqrt())

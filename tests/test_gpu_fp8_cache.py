@@ -8,7 +8,7 @@ import deepseek_v4_engram_gb300 as eg
 from deepseek_v4_engram_gb300 import _lib
 from oracle import kv_fp8
 from tests.attn_helpers import cu_of, f64
-from tests.fp8_helpers import PagedFp8, rows
+from tests.fp8_helpers import PagedFp8, assert_close, reference, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -209,7 +209,14 @@ def test_offsets_past_32_bits():
             assert torch.equal(codes[p, :m].cpu(), torch.from_numpy(c[64 * j:64 * j + m]))
             assert torch.equal(scales[p, :, :m].cpu(), torch.from_numpy(s[64 * j:64 * j + m].T.copy()))
         np.testing.assert_array_equal(f64(got), kv_fp8.values(c, s))
-    q = torch.randn((1, 16, d), device="cuda").to(BF16)
-    out = torch.empty_like(q)
-    eg.engram_attn_paged_fp8(desc, q, cu_of([1]), kv_len, table, k, v, ks, vs, out, 1)
-    assert torch.isfinite(out).all() and eg.engram_check_errors() == 0
+    scale = d ** -0.5
+    for q_len in (1, 40):       # the few-row kernel and the tiled one
+        q = torch.randn((q_len, 16, d), device="cuda").to(BF16)
+        out = torch.empty_like(q)
+        eg.engram_attn_paged_fp8(desc, q, cu_of([q_len]), kv_len, table, k, v, ks, vs, out, q_len)
+        vc, ve = kv_fp8.quantise(f64(vv))
+        held = PagedFp8.__new__(PagedFp8)
+        held.keys, held.values = [kv_fp8.values(*kv_fp8.quantise(f64(kk)))], [kv_fp8.values(vc, ve)]
+        held.codes, held.exponents = [kv_fp8.e4m3_to_f64(vc)], [ve.astype(np.int64) - 127]
+        assert_close(out, None, *reference(held, 0, q, scale), BF16, d, scale, q_len * 2)
+    assert eg.engram_check_errors() == 0
