@@ -90,22 +90,29 @@ constexpr int kPoisonSlots = 8;
 // Of a tile's probabilities against an older maximum. With 1, where nearly every tile looks for its
 // maximum, the prompt of 16384 tokens took 1093 us instead of 661.
 constexpr float kMostSum = 512.f;
-// Over an 8-bit cache in bf16, whose keys' sizes differ more from row to row in the cases measured: 512 has a
-// quarter of the tiles find their maximum (chunks of 1024 and 300 tokens beside six single ones 215 us), this
-// hardly any (205). Sums stay finite for values up to 2^100.
+// Over an 8-bit cache in bf16, whose keys' sizes differ more from row to row in the cases measured. With 512 a
+// quarter of the tiles find their maximum: chunks of 1024 and 300 tokens beside six single ones 215 us; with this
+// and the lift below hardly any: @@ us. Sums stay finite for values up to 2^100.
 constexpr float kMostSumFp8 = 65536.f;
 // Probabilities are rounded to the values' type for the product with them, since the MMA takes both
 // operands in one 16-bit type: each by half a unit in its last place, as the result is at the end.
 // They are summed as they are, so what rounding takes from a small one is lost, and a long cache may
 // hold much weight in keys that f16 has no value for beside 1. So they are 2^kLift times larger there,
 // kMostSum of it below f16's largest value. bf16 has the exponents of f32.
-template <bool kBf16>
-constexpr float kLift = kBf16 ? 0.f : 6.f;
+// (With an 8-bit cache they are lowered instead: a maximum may grow by 2^40 before it is found anew, and
+// products with values down to 2^-100 are normal numbers still.)
+template <bool kBf16, class Kv>
+constexpr float kLift = !kBf16 ? 6.f : Kv::kFp8 ? -24.f : 0.f;
 template <bool kBf16, class Kv>
 constexpr float kMostLifted = !kBf16 ? kMostSum * 64.f : Kv::kFp8 ? kMostSumFp8 : kMostSum;
 // The maximum is subtracted in the multiply-add that scales a score, so the rounding of its product stays in
 // the difference: from here on (2^24 in units of log2) it is subtracted first.
 constexpr float kFarScore = 16777216.f;
+// Tiles of an item whose maximum is found at once: among the first ones it grows, and taking exponentials twice
+// costs more. (f16 over an 8-bit cache, where it may grow by no more than kSpare, 2^14 with the lift.)
+template <bool kBf16, class Kv>
+constexpr int kYoung = Kv::kFp8 && !kBf16 ? 32 : 1;
+constexpr float kSpare = 8.f;
 // An item's fixed time in key tiles: fetching its queries, filling the pipeline, writing its rows.
 // With 1, 2, 3: a prompt of 8192 tokens 210, 194, 194 us, 14 prompts of 0-801 tokens 45.8, 44.5,
 // 46.3, chunks of 1024 and 300 tokens beside six single ones 151, 133, 137.
@@ -590,7 +597,7 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
           // exponentials are taken against the one that is there, and only if their sum says that
           // some were far above it (or nothing had been seen), the maximum is found after all, O
           // and l are scaled down to it and the exponentials taken again.
-          bool fresh = j == seg.tile0 || far;
+          bool fresh = j < seg.tile0 + kYoung<kBf16, Kv> || far;
           float sums;
 #pragma unroll 1
           for (;;) {
@@ -601,8 +608,12 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                   mt[i] = max3(mt[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
-              const float top = fmaxf(m, fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])));
-              if (j > seg.tile0) {
+              float top = fmaxf(m, fmaxf(fmaxf(mt[0], mt[1]), fmaxf(mt[2], mt[3])));
+              // The old maximum will do where no row's has grown by much.
+              if (kYoung<kBf16, Kv> > 1 && j > seg.tile0 && !far &&
+                  !__any_sync(0xFFFFFFFFu, m == -INFINITY ? top > m : (top - m) * c > kSpare))
+                top = m;
+              else if (j > seg.tile0) {
                 // The score MMA that this tile waited for came after the last product with V, so
                 // O is at rest.
                 const float f = m == -INFINITY ? 0.f : exp2_fast((m - top) * c);
@@ -628,7 +639,7 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
                       s[i][e] = __float_as_uint(__uint_as_float(s[i][e]) - (m == -INFINITY ? 0.f : m));
               }
             }
-            const float base = m == -INFINITY ? 0.f : far ? kLift<kBf16> : fmaf(-m, c, kLift<kBf16>);
+            const float base = m == -INFINITY ? 0.f : far ? kLift<kBf16, Kv> : fmaf(-m, c, kLift<kBf16, Kv>);
             const uint64_t c2 = pair(c, c), b2 = pair(base, base);
             uint64_t sum[4] = {};
 #pragma unroll
@@ -698,7 +709,7 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
                                                                   : seg.tile0 * kTileKeys;
         const int32_t k1 = limit < seg.tile1 * kTileKeys ? limit : seg.tile1 * kTileKeys;
         const int32_t end = seg.keys < seg.tile1 * kTileKeys ? seg.keys : seg.tile1 * kTileKeys;
-        const float base = m == -INFINITY ? 0.f : fmaf(-m, c, kLift<kBf16>);
+        const float base = m == -INFINITY ? 0.f : fmaf(-m, c, kLift<kBf16, Kv>);
         const uint16_t* q = a.q + static_cast<int64_t>(seg.token0 + tok) * a.q_token +
                             static_cast<int64_t>(head) * a.q_head;
         // 32 keys at a time, the same for all rows: which of them hold such values, and which of those
@@ -802,7 +813,7 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
       }
       tc_fence_before();   // the next product into O follows this thread's next P
       if (valid) {
-        const float base = fmaf(m, c, -kLift<kBf16>);   // of the exponentials
+        const float base = fmaf(m, c, -kLift<kBf16, Kv>);   // of the exponentials
         if (!whole)
           *reinterpret_cast<float2*>(pieces.ml + slot * 2) = make_float2(base, l);
         else if (a.lse != nullptr)
