@@ -130,12 +130,19 @@ struct Geo {
   static constexpr uint32_t kO = 256;                        // TMEM columns: S0 S1 O0 O1
 };
 
+template <int kCodes>
+struct CodeRing {
+  uint64_t code_full[kCodes], code_empty[kCodes];
+  uint8_t scales[kCodes][kTileKeys];
+};
+template <>
+struct CodeRing<0> {};
+
 template <int DH, class Kv>
-struct Shared {
-  static constexpr int kStages = Geo<DH, Kv>::kStages, kCodes = Kv::kFp8 ? Geo<DH, Kv>::kCodeStages : 1;
+struct alignas(16) Shared : CodeRing<Geo<DH, Kv>::kCodeStages> {
+  static constexpr int kStages = Geo<DH, Kv>::kStages;
   static constexpr int kGuards = Kv::kFp8 ? kConvertWarps : 2;
   uint64_t full[kStages], empty[kStages], vok[kStages];
-  uint64_t code_full[kCodes], code_empty[kCodes];
   uint64_t qfull, qempty, sfull[2], pfull[2], ofull[2];
   uint64_t drain;
   uint64_t seg_full[kSegments], seg_empty[kSegments];
@@ -144,7 +151,6 @@ struct Shared {
   int poison[kGuards][kPoisonSlots];   // of warps 10 and 11 (12-15), by segment
   uint32_t tmem_base;
   int abort;
-  alignas(16) uint8_t scales[kCodes][kTileKeys];
 };
 
 template <int DH, class Kv>
@@ -487,10 +493,11 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
       mbar_init(&sh->empty[s], Kv::kFp8 ? 1 : 3);   // the MMAs that read it, and warps 10 and 11
       mbar_init(&sh->vok[s], 2);
     }
-    for (int s = 0; s < G::kCodeStages; ++s) {
-      mbar_init(&sh->code_full[s], 1 + 32);   // the codes, and each lane's scales
-      mbar_init(&sh->code_empty[s], kConvertWarps);
-    }
+    if constexpr (Kv::kFp8)
+      for (int s = 0; s < G::kCodeStages; ++s) {
+        mbar_init(&sh->code_full[s], 1 + 32);   // the codes, and each lane's scales
+        mbar_init(&sh->code_empty[s], kConvertWarps);
+      }
     mbar_init(&sh->qfull, 1);
     mbar_init(&sh->qempty, 1);
     for (int t = 0; t < 2; ++t) {
@@ -597,7 +604,7 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
           // exponentials are taken against the one that is there, and only if their sum says that
           // some were far above it (or nothing had been seen), the maximum is found after all, O
           // and l are scaled down to it and the exponentials taken again.
-          bool fresh = j < seg.tile0 + kYoung<kBf16, Kv> || far;
+          bool fresh = kYoung<kBf16, Kv> > 1 ? j < seg.tile0 + kYoung<kBf16, Kv> || far : j == seg.tile0 || far;
           float sums;
 #pragma unroll 1
           for (;;) {
@@ -680,11 +687,8 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
       const int32_t head = seg.h * a.group + sub;
       const int64_t slot =
           (static_cast<int64_t>(blockIdx.x) * 2 + (seg.begins() ? 1 : 0)) * kItemRows + row;
-      bool poison = false;
-      if (tiles)
-#pragma unroll
-        for (int i = 0; i < Shared<DH, Kv>::kGuards; ++i)
-          poison |= *static_cast<volatile int*>(&sh->poison[i][slot8]) != 0;
+      auto found = [&](int part) { return *static_cast<volatile int*>(&sh->poison[part][slot8]); };
+      const bool poison = tiles && (Kv::kFp8 ? found(0) | found(1) | found(2) | found(3) : found(0) | found(1)) != 0;
       // Rows leave in pieces of 16 bytes that four lanes exchange, so that each store writes 64
       // bytes of a row: the lane's own row, and those of its three neighbours.
       const int64_t place = !valid ? -1
@@ -914,8 +918,11 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
       // ----------------------------------------------------------- TMA producer
       // of tiles, or of their codes
       constexpr int kRing = Kv::kFp8 ? G::kCodeStages : G::kStages;
-      uint64_t* const ring_full = Kv::kFp8 ? sh->code_full : sh->full;
-      uint64_t* const ring_empty = Kv::kFp8 ? sh->code_empty : sh->empty;
+      uint64_t *ring_full = sh->full, *ring_empty = sh->empty;
+      if constexpr (Kv::kFp8) {
+        ring_full = sh->code_full;
+        ring_empty = sh->code_empty;
+      }
       TmaRingT<kRing> ring;
       bool stop = false;
       AttnCursor cur = sh->start.cursor;
