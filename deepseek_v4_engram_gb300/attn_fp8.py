@@ -22,26 +22,25 @@ _pack_cache = _lib.PACK_CACHE_FP8.pack
 
 
 def _cache(desc: EngramAttnDesc, k_cache, v_cache, k_scale, v_scale, block_table, device: int, n_seqs: int):
-    if (isinstance(k_cache, torch.Tensor) and isinstance(v_cache, torch.Tensor) and isinstance(k_scale, torch.Tensor)
-            and isinstance(v_scale, torch.Tensor) and isinstance(block_table, torch.Tensor)
-            and k_cache.get_device() == device and v_cache.get_device() == device and k_scale.get_device() == device
-            and v_scale.get_device() == device and block_table.get_device() == device):
-        codes, scales, shape, table = k_cache.dtype, k_scale.dtype, k_cache.shape, block_table.shape
-        if ((codes is _U8 or codes is _CODES) and v_cache.dtype is codes and (scales is _U8 or scales is _SCALES)
-                and v_scale.dtype is scales and block_table.dtype is _INT and len(shape) == 4 and len(table) == 2):
-            pages, page_size, heads, dim = shape
-            n, width = table
-            if (heads == desc.n_kv_heads and dim == desc.head_dim and n == n_seqs and v_cache.shape == shape
-                    and k_scale.shape == (pages, heads, page_size) and v_scale.shape == k_scale.shape
-                    and block_table.is_contiguous()):
-                k0, k1, k2, k3 = k_cache.stride()
-                v0, v1, v2, v3 = v_cache.stride()
-                a0, a1, a2 = k_scale.stride()
-                b0, b1, b2 = v_scale.stride()
-                if k3 == 1 and v3 == 1 and a2 == 1 and b2 == 1:
-                    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                                       k0, k1, k2, v0, v1, v2, a0, a1, b0, b1, pages, page_size,
-                                       block_table.data_ptr(), width)
+    try:   # what is no tensor, or has another number of dimensions, ends here
+        pages, page_size, heads, dim = shape = k_cache.shape
+        k0, k1, k2, k3 = k_cache.stride()
+        v0, v1, v2, v3 = v_cache.stride()
+        a0, a1, a2 = k_scale.stride()
+        b0, b1, b2 = v_scale.stride()
+        n, width = block_table.shape
+        codes, scales, of_scales = k_cache.dtype, k_scale.dtype, k_scale.shape
+        if (k_cache.get_device() == device and v_cache.get_device() == device and k_scale.get_device() == device
+                and v_scale.get_device() == device and block_table.get_device() == device
+                and (codes is _U8 or codes is _CODES) and v_cache.dtype is codes
+                and (scales is _U8 or scales is _SCALES) and v_scale.dtype is scales and block_table.dtype is _INT
+                and heads == desc.n_kv_heads and dim == desc.head_dim and n == n_seqs and v_cache.shape == shape
+                and of_scales == (pages, heads, page_size) and v_scale.shape == of_scales
+                and k3 == 1 and v3 == 1 and a2 == 1 and b2 == 1 and block_table.is_contiguous()):
+            return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                               k0, k1, k2, v0, v1, v2, a0, a1, b0, b1, pages, page_size, block_table.data_ptr(), width)
+    except (AttributeError, TypeError, ValueError):
+        pass
     name = "k_cache, v_cache, k_scale, v_scale and block_table"
     want = (f"[pages, page_size, {desc.n_kv_heads}, {desc.head_dim}] whose last dimension is dense, keys and values "
             f"alike, with scales [pages, {desc.n_kv_heads}, page_size] whose last dimension is dense and a contiguous "

@@ -22,6 +22,16 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// Pairs of f32 in one 64-bit register, for instructions that take two at once.
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
 // Not zero where one of the two 16-bit values in `w` is an infinity or NaN: one added to an
 // exponent of all ones carries into the sign's place.
 template <bool kBf16>

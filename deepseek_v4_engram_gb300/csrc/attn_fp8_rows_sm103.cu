@@ -16,11 +16,26 @@
 // of a key row are the columns of four steps, and 16 bytes of four value rows, their bytes interleaved in
 // pairs, are eight tiles of V^T. S^T becomes P^T's operand by two 8 x 8 transposes in registers.
 //
-// Roles (384 threads): warps 8-10 request the tiles; warps 0-7 each take 16 of a tile's 128 keys, so every warp has its own base, sum and output and
-// no step of the loop waits for another warp. Work is shared out by key tiles (attn_plan.cuh).
+// Roles (384 threads): warps 8-10 request the tiles; warps 0-7 each take 16 or 32 of a stage's keys, so every
+// warp has its own base, sum and output and no step of the loop waits for another warp. Work is shared out by key
+// tiles (attn_plan.cuh).
+//
+// Two key-value heads make an item where they lie beside each other (the usual [slot, head, column] order): TMA is
+// slow per row, not per byte, and 128 bytes of every kilobyte are a poor diet for memory. The even warps then take
+// one head, the odd ones the other.
 //
 // The base B_r lags behind the maximum: it is found anew only when some y exceeds it by 2^kSlack or more,
 // which a warp finds out with one vote instead of the shuffles of a maximum.
+//
+// Measured (replayed, inputs larger than L2): one token each over 64 caches of 1584-2048 positions, 32 heads of
+// 128 over 8, 49.6 us (a 16-bit cache 80), over 4 caches of 70001-131072 139 us, 6.4 TB/s; 24 caches of 100-7061
+// with 16 heads of 64, f16, 40.7; one token over 511 positions 8.2. A call's fixed time is about 9 us: range, first
+// page entry, page and tile, joining warps and pieces. A stage of 32 KB takes 0.75 us where memory alone sets
+// the pace (a copy that only reads; 0.73 at the copy rate) and 0.74-0.8 here with 8 rows of a head, 0.82 with 16,
+// 1.65 with 32, whose chain of steps is longer than the wait for memory. What brought it there: all copies
+// of a tile from one warp 0.92; scales by TMA 100 cycles a copy like codes; L2 fetches of 256 bytes for rows of
+// 128 (44% more traffic); one 16-key step of a warp at a time 1105 cycles, two overlapped 1550. Slower: the codes
+// by 16-byte asynchronous copies (1.4 us a tile), two chains for a score, value rows read before the keys.
 #include "kernels.h"
 #include "kv_fp8.cuh"
 #include "wkv_tiles.cuh"

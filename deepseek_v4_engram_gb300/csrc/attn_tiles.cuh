@@ -44,6 +44,16 @@
 // row of the item must not see harmless (below). Registers: the softmax warps hold a row of 128
 // scores, so they take 192 each and the other four 120.
 //
+// Over an 8-bit cache there are four warps more, 12-15: TMA brings codes (warp 9; the scales by warp 11), and
+// they write them out as 16-bit tiles times their scales, through registers, with the work of warps 10-11 below
+// done on the way. All else is the same; so a call takes what it would over 16 bits (379 us for a chunk of 2047 over
+// 30000 positions, 16 heads of 128 over 4, f16, on keys of these sizes; 163 for chunks of 1024 and 300 beside six
+// single tokens) and 15-20% more: 446 and 184. What the conversion costs: 64 KB written and 32 read per pair of
+// tiles in shared memory, where the MMAs take their operands (without any stores 409 us instead of 468, without
+// any arithmetic 389, without the conversion 358), and issue slots beside the softmax. A tile takes four warps
+// 1030-1490 cycles in f16, up to 2150 in bf16, whose codes go through f32. Not faster: bf16 codes put in place bit
+// by bit, three tiles' room for codes and four for tiles, keys and values requested by a warp each (10% slower).
+//
 // A probability of 0 does not undo an infinity or NaN that it multiplies. In the tiles that reach
 // past what the item's first row sees, warps 10-11 clear the value rows that no row sees (another
 // sequence's, or memory that was never written) and replace infinities and NaN in the others by
@@ -92,7 +102,7 @@ constexpr int kPoisonSlots = 8;
 constexpr float kMostSum = 512.f;
 // Over an 8-bit cache in bf16, whose keys' sizes differ more from row to row in the cases measured. With 512 a
 // quarter of the tiles find their maximum: chunks of 1024 and 300 tokens beside six single ones 215 us; with this
-// and the lift below hardly any: @@ us. Sums stay finite for values up to 2^100.
+// 206 us, and with the lift below, where hardly any does, 182. Sums stay finite for values up to 2^100.
 constexpr float kMostSumFp8 = 65536.f;
 // Probabilities are rounded to the values' type for the product with them, since the MMA takes both
 // operands in one 16-bit type: each by half a unit in its last place, as the result is at the end.
@@ -109,7 +119,9 @@ constexpr float kMostLifted = !kBf16 ? kMostSum * 64.f : Kv::kFp8 ? kMostSumFp8 
 // the difference: from here on (2^24 in units of log2) it is subtracted first.
 constexpr float kFarScore = 16777216.f;
 // Tiles of an item whose maximum is found at once: among the first ones it grows, and taking exponentials twice
-// costs more. (f16 over an 8-bit cache, where it may grow by no more than kSpare, 2^14 with the lift.)
+// costs more. (f16 over an 8-bit cache, where it may grow by no more than kSpare, 2^14 with the lift. With 1, 8, 32
+// and all of them: five drafted tokens over 16 caches 48.6, 46.2, 44.6, 44.6 us, a chunk of 2047 over 30000 456, 456,
+// 448, 463.)
 template <bool kBf16, class Kv>
 constexpr int kYoung = Kv::kFp8 && !kBf16 ? 32 : 1;
 constexpr float kSpare = 8.f;
@@ -262,23 +274,10 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Pairs of f32 in one 64-bit register: two multiply-adds or adds per instruction.
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
+// Two multiply-adds or adds per instruction.
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
@@ -317,49 +316,6 @@ __device__ __forceinline__ const uint16_t* kv_row(const AttnArgs& a, const AttnS
   if (page < 0 || page >= a.n_pages) return nullptr;
   return p + page * (values ? a.v_page : a.k_page) + (pos - int64_t(col) * a.page_size) * token +
          s.h * head;
-}
-
-// Two codes times a scale in the 16-bit type, rounded once, as engram_kv_read_fp8 gives them.
-template <bool kBf16>
-__device__ __forceinline__ uint32_t scaled16x2(uint32_t codes, float scale) {
-  const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(codes));
-  float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
-  const float most = kBf16 ? __uint_as_float(0x7F7F0000u) : 65504.f;
-  x.x *= scale;
-  x.y *= scale;
-  x.x = fabsf(x.x) > most ? copysignf(most, x.x) : x.x;   // NaN stays
-  x.y = fabsf(x.y) > most ? copysignf(most, x.y) : x.y;
-  return pack16x2<kBf16>(x.x, x.y);
-}
-
-// The same for four codes whose scale is from 2^-14 to 2^7 (f16, with one product for two) or from 2^-100 to
-// 2^118 (bf16, through f32): nothing goes beyond the type's range. `scale`: what fast_scale gives.
-template <bool kBf16>
-__device__ __forceinline__ bool is_fast(uint32_t byte) {
-  return kBf16 ? byte >= kMinScale && byte <= 245 : byte >= 113 && byte <= 134;
-}
-template <bool kBf16>
-__device__ __forceinline__ uint32_t fast_scale(uint32_t byte) {
-  const uint32_t half = (byte - 112) << 10;
-  return kBf16 ? byte << 23 : half | half << 16;
-}
-template <bool kBf16>
-__device__ __forceinline__ void scaled16x4(uint32_t codes, uint32_t scale, uint32_t& lo, uint32_t& hi) {
-  lo = e4m3x2_to_f16x2(static_cast<uint16_t>(codes));
-  hi = e4m3x2_to_f16x2(static_cast<uint16_t>(codes >> 16));
-  if constexpr (kBf16) {
-    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-    const uint64_t f = pair(__uint_as_float(scale), __uint_as_float(scale));
-    float p, q;
-    unpair(mul2(pair(x.x, x.y), f), p, q);
-    lo = pack16x2<true>(p, q);
-    unpair(mul2(pair(y.x, y.y), f), p, q);
-    hi = pack16x2<true>(p, q);
-  } else {
-    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(scale));
-    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(scale));
-  }
 }
 
 __device__ __forceinline__ uint2 lds64(uint32_t saddr) {

@@ -47,6 +47,56 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t codes) {
   return r;
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Two codes times a scale in the 16-bit type, rounded once. What that cannot hold becomes its largest value:
+// rounding to a code may carry a value past it (bf16's largest one becomes 2^128).
+template <bool kBf16>
+__device__ __forceinline__ uint32_t scaled16x2(uint32_t codes, float scale) {
+  const uint32_t h = e4m3x2_to_f16x2(static_cast<uint16_t>(codes));
+  float2 x = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  const float most = kBf16 ? __uint_as_float(0x7F7F0000u) : 65504.f;
+  x.x *= scale;
+  x.y *= scale;
+  x.x = fabsf(x.x) > most ? copysignf(most, x.x) : x.x;   // NaN stays
+  x.y = fabsf(x.y) > most ? copysignf(most, x.y) : x.y;
+  return pack16x2<kBf16>(x.x, x.y);
+}
+
+// The same for four codes whose scale is from 2^-14 to 2^7 (f16, with one product for two) or from 2^-100 to
+// 2^118 (bf16, through f32): nothing goes beyond the type's range. `scale`: what fast_scale gives.
+template <bool kBf16>
+__device__ __forceinline__ bool is_fast(uint32_t byte) {
+  return kBf16 ? byte >= kMinScale && byte <= 245 : byte >= 113 && byte <= 134;
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t fast_scale(uint32_t byte) {
+  const uint32_t half = (byte - 112) << 10;
+  return kBf16 ? byte << 23 : half | half << 16;
+}
+template <bool kBf16>
+__device__ __forceinline__ void scaled16x4(uint32_t codes, uint32_t scale, uint32_t& lo, uint32_t& hi) {
+  lo = e4m3x2_to_f16x2(static_cast<uint16_t>(codes));
+  hi = e4m3x2_to_f16x2(static_cast<uint16_t>(codes >> 16));
+  if constexpr (kBf16) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+    const uint64_t f = pair(__uint_as_float(scale), __uint_as_float(scale));
+    float p, q;
+    unpair(mul2(pair(x.x, x.y), f), p, q);
+    lo = pack16x2<true>(p, q);
+    unpair(mul2(pair(y.x, y.y), f), p, q);
+    hi = pack16x2<true>(p, q);
+  } else {
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(scale));
+    asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(scale));
+  }
+}
+
 // The bytes of `w` that are NaN codes, by their top bits.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;

@@ -562,7 +562,7 @@ typedef struct engram_kv_cache_fp8 {
  * smallest power of two, from 2^-100 on, for which no value exceeds 448 times it (1 for a row of
  * zeros), its codes the values over the scale rounded to nearest, ties to even. A row that holds an
  * infinity or NaN gets the byte 255 and codes of 0. Tokens, positions, lengths and errors as in
- * engram_kv_append. The cache's four arrays may share no byte with each other or any other argument
+ * engram_kv_append, and a slot that two tokens are given is left with parts of both. The cache's four arrays may share no byte with each other or any other argument
  * (ENGRAM_EINVAL).
  */
 ENGRAM_API int engram_kv_append_fp8(const engram_attn_desc_t* desc, const engram_attn_view_t* k,
