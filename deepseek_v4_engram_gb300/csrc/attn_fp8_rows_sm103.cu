@@ -61,39 +61,36 @@ constexpr float kMostExponent = 15.5f;
 // whose probability has underflowed in f32 are missing: values 2^100 below the ones that count.)
 constexpr int kSumDrop = 6;
 
-// kHeads: key-value heads of an item, 1 or 2. NT: tiles of 8 rows of each.
-template <int DH, int NT, int kHeads>
+// An item's rows are one part, or two that the even and the odd warps take: of a key-value head each (kHeads = 2),
+// or of the same one (kGroups = 2). NT: tiles of 8 rows of a part.
+template <int DH, int NT, int kHeads, int kGroups>
 struct Geo {
-  static constexpr int kHeadRows = 8 * NT, kRows = kHeads * kHeadRows;
-  static constexpr int kKeys = DH == 128 && kHeads == 2 && NT > 2 ? 64 : kTileKeys;   // of a stage
-  static constexpr int kTensorBytes = kKeys * kHeads * DH;                  // codes of K or V of a stage
-  static constexpr int kScaleBytes = kKeys * kHeads;
+  static constexpr int kParts = kHeads * kGroups, kPartRows = 8 * NT, kRows = kParts * kPartRows;
+  static constexpr int kTensorBytes = kTileKeys * kHeads * DH;         // codes of K or V of a stage
+  static constexpr int kScaleBytes = kTileKeys * kHeads;
   static constexpr int kJoinRow = DH + 4;
-  static constexpr int kJoinRows = NT == 1 ? 8 : 16;                   // of a head, joined at a time
+  static constexpr int kJoinRows = NT == 2 ? 16 : 8;                   // of a part, joined at a time
   static constexpr int kJoinBytes = kConsumers * kJoinRows * kJoinRow * 4;
-  static constexpr bool kQueriesShared = NT == 4;                      // else in registers
-  static constexpr int kQueryBytes = kQueriesShared ? DH / 16 * NT * kHeads * 32 * 8 : 0;
-  static constexpr int kStages = kTensorBytes == 32768 ? 2 : kTensorBytes == 16384 ? (NT == 1 ? 5 : 4) : 8;
+  static constexpr int kStages = kTensorBytes == 32768 ? 2 : kTensorBytes == 16384 ? (NT == 2 ? 4 : 5) : 8;
 };
 
-template <int DH, int NT, int kHeads>
+template <int DH, int NT, int kHeads, int kGroups>
 struct Shared {
-  using G = Geo<DH, NT, kHeads>;
+  using G = Geo<DH, NT, kHeads, kGroups>;
   uint64_t full[G::kStages];
   uint64_t empty[G::kStages];
   AttnStart start;
-  float2 ml[kConsumers][G::kHeadRows];   // bases and sums
-  float row_scale[G::kRows];
-  uint32_t poison[G::kRows][DH / 32];   // columns of a row that are NaN by a value's code
+  float2 ml[kConsumers][G::kPartRows];   // bases and sums
+  uint32_t poison[G::kRows][DH / 32];    // columns of a row that are NaN by a value's code
   int poisoned;
   int abort;
 };
 
-template <int DH, int NT, int kHeads>
+template <int DH, int NT, int kHeads, int kGroups>
 constexpr size_t smem_bytes() {
-  using G = Geo<DH, NT, kHeads>;
+  using G = Geo<DH, NT, kHeads, kGroups>;
   return 1024 + size_t(G::kStages) * 2 * (G::kTensorBytes + G::kScaleBytes) + G::kJoinBytes +
-         G::kQueryBytes + sizeof(Shared<DH, NT, kHeads>);
+         sizeof(Shared<DH, NT, kHeads, kGroups>);
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -146,22 +143,20 @@ __device__ __forceinline__ int key_of(int i) {
   return ((t & 1) | ((t & 2) << 1)) ^ (up * 3);
 }
 
-template <int DH, int NT, int kHeads, bool kBf16>
+template <int DH, int NT, int kHeads, int kGroups, bool kBf16>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fp8_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                          const __grid_constant__ AttnArgs a, const KvFp8Part ks, const KvFp8Part vs,
                          const AttnPieces pieces) {
-  using G = Geo<DH, NT, kHeads>;
-  constexpr int kStagesPerTile = kTileKeys / G::kKeys;
-  constexpr int kWarpKeys = G::kKeys * kHeads / kConsumers;   // of a stage: 16 or 32
-  constexpr int U = NT == 4 ? 1 : kWarpKeys / 16;   // times 16 keys at once, whose chains of steps overlap
-  constexpr int kSteps = DH / 16;   // of a score's contraction; and tiles of V^T
+  using G = Geo<DH, NT, kHeads, kGroups>;
+  constexpr int kWarpKeys = kTileKeys * G::kParts / kConsumers;   // of a stage: 16 or 32
+  constexpr int U = kWarpKeys / 16;   // times 16 keys at once, whose chains of steps overlap
+  constexpr int kSteps = DH / 16;     // of a score's contraction; and tiles of V^T
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
   uint8_t* scales = smem + G::kStages * 2 * G::kTensorBytes;
-  uint2* queries = reinterpret_cast<uint2*>(scales + G::kStages * 2 * G::kScaleBytes);
-  float* join = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(queries) + G::kQueryBytes);
-  using S = Shared<DH, NT, kHeads>;
+  float* join = reinterpret_cast<float*>(scales + G::kStages * 2 * G::kScaleBytes);
+  using S = Shared<DH, NT, kHeads, kGroups>;
   S* sh = reinterpret_cast<S*>(reinterpret_cast<uint8_t*>(join) + G::kJoinBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -195,10 +190,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool stop = part > 2;
     while (!stop && cur.next(a.plan, seg)) {
       const int32_t h0 = seg.h * kHeads;
-      for (int32_t k0 = seg.tile0 * kTileKeys; k0 < seg.tile1 * kTileKeys && k0 < seg.keys; k0 += G::kKeys) {
-        const int32_t n = seg.keys - k0 < G::kKeys ? seg.keys - k0 : G::kKeys;
+      for (int32_t k0 = seg.tile0 * kTileKeys; k0 < seg.tile1 * kTileKeys && k0 < seg.keys; k0 += kTileKeys) {
+        const int32_t n = seg.keys - k0 < kTileKeys ? seg.keys - k0 : kTileKeys;
         const int32_t grans = (n + a.granule - 1) / a.granule;
-        const int32_t mine = part < 2 ? lane * a.granule : lane * 4 % G::kKeys;   // first slot of the lane's copy
+        const int32_t mine = part < 2 ? lane * a.granule : lane * 4;   // first slot of the lane's copy
         const bool live = mine < grans * a.granule;
         KvPlace at{0, 0};
         if (live) at = kv_place(a, seg, k0 + mine);
@@ -212,17 +207,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_load_4d(smem + (ring.stage * 2 + part) * G::kTensorBytes + lane * a.granule * kHeads * DH,
                         part == 0 ? &tmK : &tmV, full, 0, DH == 64 ? seg.h : h0, at.z, at.w);
         } else {
-          // lanes 0 .. kKeys / 4 - 1 the first head's, and so on
           const bool there = at.w < a.n_pages;
 #pragma unroll
-          for (int r = 0; r < kHeads; r += 128 / G::kKeys) {
-            const int32_t sub = r + lane * 4 / G::kKeys;
-            if (live) {
-              const uint32_t to = smem_u32(scales + ring.stage * 2 * G::kScaleBytes + sub * G::kKeys + mine);
-              copy4(to, ks.scales + (there ? at.w * ks.scale_page + (h0 + sub) * ks.scale_head + at.z : 0), there);
-              copy4(to + G::kScaleBytes,
-                    vs.scales + (there ? at.w * vs.scale_page + (h0 + sub) * vs.scale_head + at.z : 0), there);
-            }
+          for (int head = 0; head < kHeads; ++head) {
+            if (!live) continue;
+            const uint32_t to = smem_u32(scales + ring.stage * 2 * G::kScaleBytes + head * kTileKeys + mine);
+            copy4(to, ks.scales + (there ? at.w * ks.scale_page + (h0 + head) * ks.scale_head + at.z : 0), there);
+            copy4(to + G::kScaleBytes,
+                  vs.scales + (there ? at.w * vs.scale_page + (h0 + head) * vs.scale_head + at.z : 0), there);
           }
           arrive_after_copies(full);
         }
@@ -237,11 +229,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     AttnCursor cur = sh->start.cursor;
     AttnSegment seg;
     const int g = lane >> 2, t4 = lane & 3;
-    const int sub = kHeads == 2 ? warp & 1 : 0;                 // the warp's key-value head
-    const int keys_at = warp / kHeads * kWarpKeys;              // its first key of a stage
+    const int part = G::kParts == 2 ? warp & 1 : 0;
+    const int sub = kHeads == 2 ? part : 0;                     // the warp's key-value head
+    const int row0 = kGroups == 2 ? part * G::kPartRows : 0;    // its first row of those of the head
+    const int keys_at = warp / G::kParts * kWarpKeys;           // its first key of a stage
     const int group = a.group / kHeads;                         // query heads of a key-value head
     const int kg = key_of<DH, kHeads>(g);                       // rows g and g + 8 of S^T: keys kg and kg + 8
-    const int scale0 = sub * G::kKeys + keys_at + kg;
+    const int scale0 = sub * kTileKeys + keys_at + kg;
     // Where chunk `c` of 16 bytes of the warp's head in key `key` of a stage lies. Two heads: 128-byte rows of
     // one key and head each, in this order, or of both heads of a key.
     auto row_at = [&](int key, int c) -> uint32_t {
@@ -268,13 +262,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) attn_no_pieces(pieces);
     while (cur.next(a.plan, seg)) {
       // ---- queries: row n of a head's is token n / group of the item, its query head n % group
-      uint2 qf[G::kQueriesShared ? 1 : NT][kSteps];
+      uint2 qf[NT][kSteps];
       float rc[NT][2];       // of rows 2 t4 and + 1: what turns a product into a score, but for the key's scale
       int32_t limit[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (!G::kQueriesShared || warp / kHeads == nt) {
-          const int32_t r = nt * 8 + g, tok = r / group;
+        {
+          const int32_t r = row0 + nt * 8 + g, tok = r / group;
           const bool valid = tok < seg.ntok;
           const uint16_t* qp = a.q + static_cast<int64_t>(seg.token0 + tok) * a.q_token +
                                static_cast<int64_t>(seg.h * a.group + sub * group + (r - tok * group)) * a.q_head;
@@ -316,48 +310,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[kk][e] = pack16x2<false>(__uint_as_float(w[kk][e] << 16) * f,
                                            __uint_as_float(w[kk][e] & 0xFFFF0000u) * f);
           }
-          if constexpr (G::kQueriesShared) {
 #pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk)
-              queries[((kk * kHeads + sub) * NT + nt) * 32 + lane] = make_uint2(w[kk][0], w[kk][1]);
-            if (t4 == 0) sh->row_scale[sub * G::kHeadRows + nt * 8 + g] = back;
-          } else {
+          for (int kk = 0; kk < kSteps; ++kk) qf[nt][kk] = make_uint2(w[kk][0], w[kk][1]);
 #pragma unroll
-            for (int kk = 0; kk < kSteps; ++kk) qf[nt][kk] = make_uint2(w[kk][0], w[kk][1]);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) rc[nt][j] = __shfl_sync(0xFFFFFFFFu, back, (2 * t4 + j) * 4);
-          }
+          for (int j = 0; j < 2; ++j) rc[nt][j] = __shfl_sync(0xFFFFFFFFu, back, (2 * t4 + j) * 4);
         }
       }
-      if constexpr (G::kQueriesShared) named_bar_sync(1, kConsumers * 32);
       float base[NT][2], sum[NT][2];
       float o[NT][kSteps][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int32_t r = nt * 8 + 2 * t4 + j, tok = r / group;
+          const int32_t tok = (row0 + nt * 8 + 2 * t4 + j) / group;
           const bool valid = tok < seg.ntok;
           const int32_t lim = seg.first + tok;
           limit[nt][j] = valid && lim > 0 ? lim : 0;
           base[nt][j] = valid ? -INFINITY : 1e30f;   // rows that are not there never ask for a new one
           sum[nt][j] = 0.f;
-          if constexpr (G::kQueriesShared) rc[nt][j] = sh->row_scale[sub * G::kHeadRows + r];
         }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
       }
 
       for (int32_t first = seg.tile0 * kTileKeys; first < seg.tile1 * kTileKeys && first < seg.keys;
-           first += G::kKeys) {
+           first += kTileKeys) {
         const bool here = !__any_sync(0xFFFFFFFFu, !attn_wait(&sh->full[stage], phase, abort));
-#pragma unroll 1
-        for (int step = 0; step < kWarpKeys; step += 16 * U) {
-          const int32_t key0 = first + keys_at + step;   // of U times 16
-          if (!here || key0 >= seg.keys) break;
-          const uint8_t* sk = smem + stage * 2 * G::kTensorBytes + step * kKeyBytes;
+        const int32_t key0 = first + keys_at;   // of U times 16
+        if (here && key0 < seg.keys) {
+          const uint8_t* sk = smem + stage * 2 * G::kTensorBytes;
           const uint8_t* sv = sk + G::kTensorBytes;
-          const uint8_t* ss = scales + stage * 2 * G::kScaleBytes + step;
+          const uint8_t* ss = scales + stage * 2 * G::kScaleBytes;
           // ---- scores of 16 U keys by the rows
           float s[U][NT][4] = {};
 #pragma unroll
@@ -378,11 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t f[4] = {codes_lo(wl[u][i]), codes_lo(wh[u][i]), codes_hi(wl[u][i]), codes_hi(wh[u][i])};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                  uint2 q;
-                  if constexpr (G::kQueriesShared)
-                    q = queries[(((half * 4 + i) * kHeads + sub) * NT + nt) * 32 + lane];
-                  else
-                    q = qf[nt][half * 4 + i];
+                  const uint2 q = qf[nt][half * 4 + i];
                   mma_f16(s[u][nt], f, q.x, q.y);
                 }
               }
@@ -421,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int key = keys_at + u * 16 + (i & 1 ? vb : va) + (i & 2 ? 8 : 0);
-                if (ss[G::kScaleBytes + sub * G::kKeys + key] == kNanScale)
+                if (ss[G::kScaleBytes + sub * kTileKeys + key] == kNanScale)
 #pragma unroll
                   for (int w = 0; w < kWords; ++w) v[u][i][w] = 0x7F7F7F7Fu;
               }
@@ -518,9 +497,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sh->poisoned = 1;
                 const int bit = g * (DH / 8);
 #pragma unroll 1
-                for (int r = 0; r < seg.ntok * group; ++r)
-                  if (key < seg.first + r / group)
-                    atomicOr(&sh->poison[sub * G::kHeadRows + r][bit / 32], columns << (bit % 32));
+                for (int n = 0; n < G::kPartRows; ++n) {
+                  const int tok = (row0 + n) / group;
+                  if (tok < seg.ntok && key < seg.first + tok)
+                    atomicOr(&sh->poison[part * G::kPartRows + n][bit / 32], columns << (bit % 32));
+                }
               }
           }
           // ---- products with the values
@@ -552,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg.begins() ? 1 : 0);
       constexpr float drop = 1.f / (1 << kSumDrop);
 #pragma unroll
-      for (int r0 = 0; r0 < G::kHeadRows; r0 += G::kJoinRows) {
+      for (int r0 = 0; r0 < G::kPartRows; r0 += G::kJoinRows) {
         if (r0 >= seg.ntok * group) break;
         named_bar_sync(1, kConsumers * 32);   // what was there has been read
 #pragma unroll
@@ -575,20 +556,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kLanes = DH / 4;   // of a row
         const int col = lane % kLanes * 4;
 #pragma unroll 1
-        for (int at = warp * (32 / kLanes) + lane / kLanes; at < kHeads * G::kJoinRows;
+        for (int at = warp * (32 / kLanes) + lane / kLanes; at < G::kParts * G::kJoinRows;
              at += kConsumers * (32 / kLanes)) {
-          const int n = at / kHeads, head = at % kHeads;   // a row of one of the heads
-          const int r = r0 + n, tok = r / group;
+          const int n = at / G::kParts, of = at % G::kParts;   // a row of one of the parts
+          const int r = r0 + n + (kGroups == 2 ? of * G::kPartRows : 0), tok = r / group;
           if (tok >= seg.ntok) continue;
           float m = -INFINITY, l = 0.f, acc[4] = {};
 #pragma unroll
-          for (int w = 0; w < kConsumers; w += kHeads) m = fmaxf(m, sh->ml[w + head][r].x);
+          for (int w = 0; w < kConsumers; w += G::kParts) m = fmaxf(m, sh->ml[w + of][r0 + n].x);
           const float b = m == -INFINITY ? 0.f : m;
 #pragma unroll
-          for (int w = 0; w < kConsumers; w += kHeads) {
-            const float2 ml = sh->ml[w + head][r];
-            const float4 v = *reinterpret_cast<const float4*>(
-                join + ((w + head) * G::kJoinRows + n) * G::kJoinRow + col);
+          for (int w = 0; w < kConsumers; w += G::kParts) {
+            const float2 ml = sh->ml[w + of][r0 + n];
+            const float4 v =
+                *reinterpret_cast<const float4*>(join + ((w + of) * G::kJoinRows + n) * G::kJoinRow + col);
             const float f = exp2_fast(ml.x - b);
             l += f * ml.y;
             acc[0] += f * v.x;
@@ -599,10 +580,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (sh->poisoned) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (sh->poison[head * G::kHeadRows + r][col / 32] >> (col % 32 + e) & 1)
+              if (sh->poison[of * G::kPartRows + r0 + n][col / 32] >> (col % 32 + e) & 1)
                 acc[e] = __uint_as_float(0x7FC00000u);
           }
-          const int32_t of_token = head * group + (r - tok * group);   // which of a token's rows
+          const int32_t of_token = (kHeads == 2 ? of * group : 0) + (r - tok * group);   // which of a token's rows
           if (whole) {
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int32_t query = seg.h * a.group + of_token;
@@ -633,41 +614,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) attn_report(abort, a.err);
 }
 
-template <int DH, int NT, int kHeads, bool kBf16>
+template <int DH, int NT, int kHeads, int kGroups, bool kBf16>
 cudaError_t launch(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, const CUtensorMap (&tm)[2],
                    cudaStream_t st) {
-  constexpr size_t smem = smem_bytes<DH, NT, kHeads>();
+  constexpr size_t smem = smem_bytes<DH, NT, kHeads, kGroups>();
   static_assert(smem <= 232448, "shared memory");
-  const auto kernel = attn_fp8_rows_kernel<DH, NT, kHeads, kBf16>;
+  const auto kernel = attn_fp8_rows_kernel<DH, NT, kHeads, kGroups, kBf16>;
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), smem);
   if (e != cudaSuccess) return e;
   return launch_ex(kernel, dim3(a.plan.workers), dim3(kThreads), smem, st, true, tm[0], tm[1], a, k, v,
-                   attn_pieces_at(a.workspace, a.plan.workers, Geo<DH, NT, kHeads>::kRows));
+                   attn_pieces_at(a.workspace, a.plan.workers, Geo<DH, NT, kHeads, kGroups>::kRows));
 }
 
-template <int NT, int kHeads>
+template <int NT, int kHeads, int kGroups>
 cudaError_t launch_any(AttnArgs a, const KvFp8Part& k, const KvFp8Part& v, cudaStream_t st) {
-  const int width = attn_width(a.head_dim);
+  constexpr int32_t rows = 8 * NT * kHeads * kGroups;
   // An item's heads are one key-value head to the plan and to the joining kernel.
   a.plan.kv_heads /= kHeads;
   a.group *= kHeads;
-  a.plan.tokens = 8 * NT * kHeads / a.group;
+  a.plan.tokens = rows / a.group;
   a.plan.workers = device_sm_count();
   a.plan.extra = kExtraUnits;
-  if (kHeads == 2 && width == 128 && NT > 2 && a.granule > 64) a.granule = 64;   // a stage's keys
   alignas(64) CUtensorMap tm[2];
   if (!attn_fp8_tensor_maps(a, k, v, kHeads, tm)) return cudaErrorInvalidValue;
-  cudaError_t e;
-  if (width == 64)
-    e = a.bf16 ? launch<64, NT, kHeads, true>(a, k, v, tm, st) : launch<64, NT, kHeads, false>(a, k, v, tm, st);
-  else
-    e = a.bf16 ? launch<128, NT, kHeads, true>(a, k, v, tm, st) : launch<128, NT, kHeads, false>(a, k, v, tm, st);
-  return e != cudaSuccess ? e : launch_attn_combine(a, 8 * NT * kHeads, st);
-}
-
-template <int NT>
-cudaError_t launch_heads(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, bool two, cudaStream_t st) {
-  return two ? launch_any<NT, 2>(a, k, v, st) : launch_any<NT, 1>(a, k, v, st);
+  cudaError_t e = cudaErrorInvalidValue;
+  if (attn_width(a.head_dim) == 64)
+    e = a.bf16 ? launch<64, NT, kHeads, kGroups, true>(a, k, v, tm, st)
+               : launch<64, NT, kHeads, kGroups, false>(a, k, v, tm, st);
+  else if constexpr (NT <= 2)
+    e = a.bf16 ? launch<128, NT, kHeads, kGroups, true>(a, k, v, tm, st)
+               : launch<128, NT, kHeads, kGroups, false>(a, k, v, tm, st);
+  return e != cudaSuccess ? e : launch_attn_combine(a, rows, st);
 }
 
 }  // namespace
@@ -682,9 +659,9 @@ cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const Kv
   const int64_t most = int64_t(a.plan.n_seqs) * a.plan.kv_heads * ((a.plan.kv_cap + kTileKeys - 1) / kTileKeys);
   const bool two = a.plan.kv_heads % 2 == 0 && a.head_dim == width && k.head == width && v.head == width &&
                    most > device_sm_count();
-  return rows <= 8    ? launch_heads<1>(a, k, v, two, st)
-         : rows <= 16 ? launch_heads<2>(a, k, v, two, st)
-                      : launch_heads<4>(a, k, v, two, st);
+  if (rows <= 8) return two ? launch_any<1, 2, 1>(a, k, v, st) : launch_any<1, 1, 1>(a, k, v, st);
+  if (rows <= 16) return two ? launch_any<2, 2, 1>(a, k, v, st) : launch_any<2, 1, 1>(a, k, v, st);
+  return rows <= 32 ? launch_any<2, 1, 2>(a, k, v, st) : launch_any<4, 1, 2>(a, k, v, st);   // of 64 columns
 }
 
 }  // namespace engram

@@ -31,9 +31,9 @@ cudaError_t launch_kv_append_fp8(const KvFp8Args& a, cudaStream_t st);   // 16 b
 cudaError_t launch_kv_read_fp8(const KvFp8Args& a, cudaStream_t st);     // the pages to 16 bits
 
 // Attention over such a cache, `a` as for a paged cache of 16 bits, but for its keys and values.
-// Items of up to kAttnFp8FewRows rows (attn_fp8_rows_sm103.cu); `rows`: of the longest chunk, at least
+// Items of up to attn_fp8_few_rows rows (attn_fp8_rows_sm103.cu); `rows`: of the longest chunk, at least
 // the heads that share a key-value head.
-constexpr int32_t kAttnFp8FewRows = 32;
+constexpr int32_t attn_fp8_few_rows(int32_t head_dim) { return attn_width(head_dim) == 64 ? 64 : 32; }
 cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows,
                                  cudaStream_t st);
 

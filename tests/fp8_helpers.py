@@ -83,7 +83,8 @@ class PagedFp8:
 
 #: A call whose longest chunk has more rows (tokens x heads that share a key-value head) goes to the kernel
 #: that computes on 16-bit tiles.
-FEW_ROWS = 32
+def few_rows(rows, head_dim):
+    return rows <= (64 if head_dim <= 64 else 32)
 
 
 def tolerance(ref, extra, dtype, head_dim, scale, rows):
@@ -107,7 +108,7 @@ def tolerance(ref, extra, dtype, head_dim, scale, rows):
     out, lse, mass, dot, vsum = ref
     small, steps = extra
     u = UNIT[dtype]
-    few = rows <= FEW_ROWS
+    few = few_rows(rows, head_dim)
     e = (head_dim + 6) * 2.0 ** -24 * dot + small + 2.0 ** -21 * (1 + dot / 16)
     t = ((2.0 ** -11 if few else u) + 2 * e + 2.0 ** -16)[..., None] * mass + (steps if few else STEP[dtype] * vsum)
     return t + u * (np.abs(out) + t) + STEP[dtype], e + 2.0 ** -16 + 2.0 ** -22 * np.abs(dot)
