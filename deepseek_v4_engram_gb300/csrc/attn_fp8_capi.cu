@@ -182,8 +182,8 @@ ENGRAM_API int engram_attn_paged_fp8(const engram_attn_desc_t* desc, const engra
   const int64_t rows = int64_t(max_q > 1 ? max_q : 1) * a.group;
   const KvFp8Part k = part(cache, false), v = part(cache, true);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return report(rows <= attn_fp8_few_rows(desc->head_dim) ? launch_attn_fp8_rows(a, k, v, static_cast<int32_t>(rows), st)
-                                        : launch_attn_fp8_tiles(a, k, v, st),
+  const bool few = rows <= attn_fp8_few_rows(desc->head_dim);
+  return report(few ? launch_attn_fp8_rows(a, k, v, static_cast<int32_t>(rows), st) : launch_attn_fp8_tiles(a, k, v, st),
                 "engram_attn_paged_fp8");
 }
 

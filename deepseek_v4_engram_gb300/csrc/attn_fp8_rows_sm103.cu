@@ -1,5 +1,5 @@
-// Attention over an 8-bit paged cache for items of at most 8, 16 or 32 query rows: decoding, a few
-// drafted tokens, any chunk of a sequence whose rows (tokens x heads that share a key-value head) are few.
+// Attention over an 8-bit paged cache for items of at most 8, 16 or 32 query rows (48 or 64 too where heads have
+// up to 64 columns): decoding, a few drafted tokens, any chunk of a sequence whose rows (tokens x heads that share a key-value head) are few.
 //
 //   x_rj = scale log2(e) 2^k_j q_r . K_j,   y_rj = x_rj + v_j        K_j, V_j: codes; k_j, v_j: scales
 //   o_r  = sum_j 2^(y_rj - B_r) V_j / sum_j 2^(y_rj - B_r) 2^-v_j
@@ -21,8 +21,11 @@
 // tiles (attn_plan.cuh).
 //
 // Two key-value heads make an item where they lie beside each other (the usual [slot, head, column] order): TMA is
-// slow per row, not per byte, and 128 bytes of every kilobyte are a poor diet for memory. The even warps then take
-// one head, the odd ones the other.
+// slow per row, not per byte, and memory gives less where 128 bytes of every kilobyte are read. The even warps then
+// take one head, the odd ones the other. With more than 16 rows they take one half of a head's rows each instead:
+// every code is then converted by two warps, but a warp's rows leave it the registers for 32 keys at once (32 rows:
+// two caches of 100003 and 131072 positions with 8 heads 151 us; all the rows in every warp, 16 keys at a time,
+// 163-170).
 //
 // The base B_r lags behind the maximum: it is found anew only when some y exceeds it by 2^kSlack or more,
 // which a warp finds out with one vote instead of the shuffles of a maximum.
@@ -32,7 +35,7 @@
 // with 16 heads of 64, f16, 40.7; one token over 511 positions 8.2. A call's fixed time is about 9 us: range, first
 // page entry, page and tile, joining warps and pieces. A stage of 32 KB takes 0.75 us where memory alone sets
 // the pace (a copy that only reads; 0.73 at the copy rate) and 0.74-0.8 here with 8 rows of a head, 0.82 with 16,
-// 1.65 with 32, whose chain of steps is longer than the wait for memory. What brought it there: all copies
+// 1.5 with 32, whose chain of steps is longer than the wait for memory. What brought it there: all copies
 // of a tile from one warp 0.92; scales by TMA 100 cycles a copy like codes; L2 fetches of 256 bytes for rows of
 // 128 (44% more traffic); one 16-key step of a warp at a time 1105 cycles, two overlapped 1550. Slower: the codes
 // by 16-byte asynchronous copies (1.4 us a tile), two chains for a score, value rows read before the keys.
@@ -45,7 +48,9 @@ namespace engram {
 namespace {
 
 constexpr int kConsumers = 8;
-constexpr int kExtraUnits = 2;   // an item's fixed time, in key tiles
+// An item's fixed time, in key tiles. With 0, 1, 2: 24 caches with 16 heads of 64 51.6, 44.6, 42.9 us, two long caches
+// with 16 rows 106, 104.5, 102.6, others the same.
+constexpr int kExtraUnits = 2;
 constexpr int kThreads = (kConsumers + 4) * 32;
 // 256 * 232 + 128 * 40 = 384 * 168
 constexpr int kConsumerRegs = 232, kProducerRegs = 40;
@@ -661,7 +666,10 @@ cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const Kv
                    most > device_sm_count();
   if (rows <= 8) return two ? launch_any<1, 2, 1>(a, k, v, st) : launch_any<1, 1, 1>(a, k, v, st);
   if (rows <= 16) return two ? launch_any<2, 2, 1>(a, k, v, st) : launch_any<2, 1, 1>(a, k, v, st);
-  return rows <= 32 ? launch_any<2, 1, 2>(a, k, v, st) : launch_any<4, 1, 2>(a, k, v, st);   // of 64 columns
+  if (rows <= 32) return launch_any<2, 1, 2>(a, k, v, st);
+  // Of 64 columns only (attn_fp8_few_rows): 24 caches of 148-6558 positions with 16 heads, 48 rows 124 us with three
+  // tiles, 143 with four, 157 on tcgen05; 64 rows 144, 155 on tcgen05. Of 128 columns 40 rows took 233, tcgen05 219.
+  return rows <= 48 ? launch_any<3, 1, 2>(a, k, v, st) : launch_any<4, 1, 2>(a, k, v, st);
 }
 
 }  // namespace engram

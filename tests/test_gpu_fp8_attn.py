@@ -69,6 +69,15 @@ def test_items_of_one_and_of_two_heads(q_lens, heads, kv_heads, head_dim, dtype,
     check(q_lens[:1], [9000 + 17 * kv_heads], page, heads, kv_heads, head_dim, dtype, seed=7, columns=4000)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("rows", [17, 31, 32, 33, 40, 47, 48, 49, 56, 63, 64, 65])
+@pytest.mark.parametrize("head_dim", [48, 64, 128])
+def test_rows_about_the_limits_of_the_kernels(rows, head_dim, dtype):
+    # the rows of a key-value head as tokens, and as heads
+    check([rows, 1, rows // 2], [rows + 500, 3, rows - 9], 48, 2, 2, head_dim, dtype, seed=11)
+    check([1, 1, 1], [20001, 1, 130], 64, rows, 1, head_dim, dtype, seed=12)
+
+
 @pytest.mark.parametrize("head_dim", [64, 128])
 @pytest.mark.parametrize("m", [1, 15, 16, 17, 31, 33, 63, 64, 65, 95, 97, 111, 127, 128, 129, 161, 191, 193, 255, 257])
 def test_ends_inside_a_tile(m, head_dim):
@@ -142,7 +151,8 @@ def test_much_weight_in_small_probabilities(q_len, dtype):
 
 @pytest.mark.parametrize("where", ["scale", "code"])
 @pytest.mark.parametrize("which", ["k", "v"])
-@pytest.mark.parametrize("q_len,at", [(1, 399), (4, 399), (4, 397), (100, 399), (100, 340), (100, 5)])
+@pytest.mark.parametrize("q_len,at", [(1, 399), (4, 399), (4, 397), (10, 399), (10, 391), (20, 385), (28, 399), (28, 377),
+                                      (100, 399), (100, 340), (100, 5)])
 @pytest.mark.parametrize("columns", [2, 4000])
 def test_nan_reaches_only_the_rows_that_see_it(q_len, at, which, where, columns):
     cache = PagedFp8([400], 16, 2, 64, 8, columns=columns)
