@@ -86,8 +86,10 @@ struct Shared {
   uint64_t empty[G::kStages];
   AttnStart start;
   float2 ml[kConsumers][G::kPartRows];   // bases and sums
-  uint32_t poison[G::kRows][DH / 32];    // columns of a row that are NaN by a value's code
-  int poisoned;
+  // Columns of a row that are NaN by a value's code, and whether there are any. Of a segment and of the next, which
+  // a warp may be at while others still write the rows of the first.
+  uint32_t poison[2][G::kRows][DH / 32];
+  int poisoned[2];
   int abort;
 };
 
@@ -171,8 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh->empty[s], kConsumers);
     }
     sh->abort = 0;
-    sh->poisoned = 0;
-    for (int i = 0; i < G::kRows * (DH / 32); ++i) (&sh->poison[0][0])[i] = 0;
+    sh->poisoned[0] = sh->poisoned[1] = 0;
+    for (int i = 0; i < 2 * G::kRows * (DH / 32); ++i) (&sh->poison[0][0][0])[i] = 0;
     fence_mbar_init();
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
@@ -264,8 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t va_off = v_at(va), vb_off = v_at(vb);
     const uint32_t sel_lo = swapped ? 0x1504 : 0x5140, sel_hi = swapped ? 0x3726 : 0x7362;
     uint32_t stage = 0, phase = 0;
+    int turn = 1;   // which of the two sets of marks is the segment's
     if (threadIdx.x == 0) attn_no_pieces(pieces);
     while (cur.next(a.plan, seg)) {
+      turn ^= 1;
       // ---- queries: row n of a head's is token n / group of the item, its query head n % group
       uint2 qf[NT][kSteps];
       float rc[NT][2];       // of rows 2 t4 and + 1: what turns a product into a score, but for the key's scale
@@ -499,13 +503,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                   columns |= ((n | n >> 7 | n >> 14 | n >> 21) & 15u) << (4 * w);
                 }
                 if (columns == 0) continue;
-                sh->poisoned = 1;
+                sh->poisoned[turn] = 1;
                 const int bit = g * (DH / 8);
 #pragma unroll 1
                 for (int n = 0; n < G::kPartRows; ++n) {
                   const int tok = (row0 + n) / group;
                   if (tok < seg.ntok && key < seg.first + tok)
-                    atomicOr(&sh->poison[part * G::kPartRows + n][bit / 32], columns << (bit % 32));
+                    atomicOr(&sh->poison[turn][part * G::kPartRows + n][bit / 32], columns << (bit % 32));
                 }
               }
           }
@@ -541,6 +545,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int r0 = 0; r0 < G::kPartRows; r0 += G::kJoinRows) {
         if (r0 >= seg.ntok * group) break;
         named_bar_sync(1, kConsumers * 32);   // what was there has been read
+        // so have the marks of the segment before, and the next one begins behind the barrier below
+        if (r0 == 0 && threadIdx.x == 0 && sh->poisoned[turn ^ 1]) {
+          for (int i = 0; i < G::kRows * (DH / 32); ++i) (&sh->poison[turn ^ 1][0][0])[i] = 0;
+          sh->poisoned[turn ^ 1] = 0;
+        }
 #pragma unroll
         for (int n = 0; n < G::kJoinRows / 8; ++n) {
           const int nt = r0 / 8 + n;
@@ -582,10 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc[2] += f * v.z;
             acc[3] += f * v.w;
           }
-          if (sh->poisoned) {
+          if (sh->poisoned[turn]) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (sh->poison[of * G::kPartRows + r0 + n][col / 32] >> (col % 32 + e) & 1)
+              if (sh->poison[turn][of * G::kPartRows + r0 + n][col / 32] >> (col % 32 + e) & 1)
                 acc[e] = __uint_as_float(0x7FC00000u);
           }
           const int32_t of_token = (kHeads == 2 ? of * group : 0) + (r - tok * group);   // which of a token's rows
@@ -604,12 +613,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (col == 0) *reinterpret_cast<float2*>(pieces.ml + to * 2) = make_float2(m, l);
           }
         }
-      }
-      if (*static_cast<volatile int*>(&sh->poisoned)) {   // the same for every warp: read before it is cleared
-        named_bar_sync(1, kConsumers * 32);
-        for (int i = threadIdx.x; i < G::kRows * (DH / 32); i += kConsumers * 32) (&sh->poison[0][0])[i] = 0;
-        sh->poisoned = 0;
-        named_bar_sync(1, kConsumers * 32);
       }
       if (threadIdx.x == 0) attn_piece(pieces, seg);
     }
@@ -668,7 +671,7 @@ cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const Kv
   if (rows <= 16) return two ? launch_any<2, 2, 1>(a, k, v, st) : launch_any<2, 1, 1>(a, k, v, st);
   if (rows <= 32) return launch_any<2, 1, 2>(a, k, v, st);
   // Of 64 columns only (attn_fp8_few_rows): 24 caches of 148-6558 positions with 16 heads, 48 rows 124 us with three
-  // tiles, 143 with four, 157 on tcgen05; 64 rows 144, 155 on tcgen05. Of 128 columns 40 rows took 233, tcgen05 219.
+  // tiles, 143 with four, 157 on tcgen05; 64 rows 146, 155 on tcgen05. Of 128 columns 40 rows took 233, tcgen05 219.
   return rows <= 48 ? launch_any<3, 1, 2>(a, k, v, st) : launch_any<4, 1, 2>(a, k, v, st);
 }
 

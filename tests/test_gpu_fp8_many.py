@@ -60,3 +60,27 @@ def test_append_and_read(count):
             np.testing.assert_array_equal(got[seen:seen + m], want)
         at += n
         seen += m
+
+
+@pytest.mark.parametrize("max_q", [1, 64], ids=["few rows", "tiles"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_nan_values_stay_with_their_items(max_q, dtype):
+    # many items one after the other in a worker, every third of which has a NaN code at its end, in another column
+    kv = [1 + 7 * i % 40 for i in range(2000)]
+    cache = PagedFp8(kv, 16, HK, D, 3)
+    q_lens = [min(n, 2) for n in kv]
+    q, clean, lse = run(cache, q_lens, H, D, dtype, max_q=max_q)
+    for i in range(0, 2000, 3):
+        page, slot = cache.place(i, kv[i] - 1, 1)
+        cache.v[page, slot, i % HK, i % D] = 0x7F
+    for _ in range(5):
+        _, out, got = run(cache, q_lens, H, D, dtype, max_q=max_q, q=q)
+        assert eg.engram_check_errors() == 0
+        want = f64(clean).copy()
+        last = np.cumsum(q_lens) - 1
+        for i in range(0, 2000, 3):     # only the last token sees its own position
+            of = i % HK * (H // HK)
+            want[last[i], of:of + H // HK, i % D] = np.nan
+        np.testing.assert_array_equal(np.isnan(f64(out)), np.isnan(want))
+        np.testing.assert_allclose(f64(out), want, rtol=2 ** -7, atol=1e-4)
+        np.testing.assert_array_equal(f64(got), f64(lse))
