@@ -562,8 +562,8 @@ typedef struct engram_kv_cache_fp8 {
  * smallest power of two, from 2^-100 on, for which no value exceeds 448 times it (1 for a row of
  * zeros), its codes the values over the scale rounded to nearest, ties to even. A row that holds an
  * infinity or NaN gets the byte 255 and codes of 0. Tokens, positions, lengths and errors as in
- * engram_kv_append, and a slot that two tokens are given is left with parts of both. The cache's four arrays may share no byte with each other or any other argument
- * (ENGRAM_EINVAL).
+ * engram_kv_append, and a slot that two tokens are given is left with parts of both. The cache's four
+ * arrays may share no byte with each other or any other argument (ENGRAM_EINVAL).
  */
 ENGRAM_API int engram_kv_append_fp8(const engram_attn_desc_t* desc, const engram_attn_view_t* k,
                                     const engram_attn_view_t* v, const int32_t* cu_seqlens,
@@ -591,9 +591,10 @@ ENGRAM_API int engram_kv_read_fp8(const engram_attn_desc_t* desc, const int32_t*
  * engram_attn_paged over an 8-bit cache: the same chunks, masks, lengths, workspace and errors; keys
  * and values are the cache's, as above. Scores, maxima and sums in f32. Where max_q * n_heads /
  * n_kv_heads is at most 32 (64 where head_dim is at most 64), products take codes and queries in f16,
- * which holds both exactly (a bf16 query row is first scaled by a power of two; what lies 2^-39 below its largest element is rounded away), and
- * probabilities are rounded to f16 times their value's scale; what a value contributes to a row 2^-35
- * below the largest contribution, or what lies 2^100 below the largest value of the head, may be lost.
+ * which holds both exactly (a bf16 query row is first scaled by a power of two; what lies 2^-39 below its
+ * largest element is rounded away), and probabilities are rounded to f16 times their value's scale; what
+ * a value contributes to a row 2^-35 below the largest contribution, or what lies 2^100 below the
+ * largest value of the head, may be lost.
  * Above, keys and values are rounded to dtype as engram_kv_read_fp8 gives them (exact where they were
  * appended in dtype) and probabilities to dtype. A NaN in a row that a token does not see does not reach
  * it.
