@@ -1,5 +1,6 @@
-// Attention over an 8-bit paged cache for items of at most 8, 16 or 32 query rows (48 or 64 too where heads have
-// up to 64 columns): decoding, a few drafted tokens, any chunk of a sequence whose rows (tokens x heads that share a key-value head) are few.
+// Attention over an 8-bit paged cache for items of at most 8, 16, 32 or 48 query rows (64 too where heads have up
+// to 64 columns): decoding, a few drafted tokens, any chunk of a sequence whose rows (tokens x heads that share a
+// key-value head) are few.
 //
 //   x_rj = scale log2(e) 2^k_j q_r . K_j,   y_rj = x_rj + v_j        K_j, V_j: codes; k_j, v_j: scales
 //   o_r  = sum_j 2^(y_rj - B_r) V_j / sum_j 2^(y_rj - B_r) 2^-v_j
@@ -25,7 +26,8 @@
 // take one head, the odd ones the other. With more than 16 rows they take one half of a head's rows each instead:
 // every code is then converted by two warps, but a warp's rows leave it the registers for 32 keys at once (32 rows:
 // two caches of 100003 and 131072 positions with 8 heads 151 us; all the rows in every warp, 16 keys at a time,
-// 163-170).
+// 163-170). 24 rows of 128 columns leave it that room only with the queries in shared memory (40 or 48 rows over
+// those caches 196 us; 16 keys at a time with the queries in registers 233).
 //
 // The base B_r lags behind the maximum: it is found anew only when some y exceeds it by 2^kSlack or more,
 // which a warp finds out with one vote instead of the shuffles of a maximum.
@@ -35,7 +37,7 @@
 // with 16 heads of 64, f16, 40.7; one token over 511 positions 8.2. A call's fixed time is about 9 us: range, first
 // page entry, page and tile, joining warps and pieces. A stage of 32 KB takes 0.75 us where memory alone sets
 // the pace (a copy that only reads; 0.73 at the copy rate) and 0.74-0.8 here with 8 rows of a head, 0.82 with 16,
-// 1.5 with 32, whose chain of steps is longer than the wait for memory. What brought it there: all copies
+// 1.5 with 32, 2.0 with 48, whose chain of steps is longer than the wait for memory. What brought it there: all copies
 // of a tile from one warp 0.92; scales by TMA 100 cycles a copy like codes; L2 fetches of 256 bytes for rows of
 // 128 (44% more traffic); one 16-key step of a warp at a time 1105 cycles, two overlapped 1550. Slower: the codes
 // by 16-byte asynchronous copies (1.4 us a tile), two chains for a score, value rows read before the keys.
@@ -76,6 +78,9 @@ struct Geo {
   static constexpr int kJoinRow = DH + 4;
   static constexpr int kJoinRows = NT == 2 ? 16 : 8;                   // of a part, joined at a time
   static constexpr int kJoinBytes = kConsumers * kJoinRows * kJoinRow * 4;
+  // Queries in shared memory, where registers have no room for them: [part][step][tile][lane]
+  static constexpr bool kQueriesShared = DH == 128 && NT == 3;
+  static constexpr int kQueryBytes = kQueriesShared ? kParts * (DH / 16) * NT * 32 * 8 : 0;
   static constexpr int kStages = kTensorBytes == 32768 ? 2 : kTensorBytes == 16384 ? (NT == 2 ? 4 : 5) : 8;
 };
 
@@ -85,6 +90,7 @@ struct Shared {
   uint64_t full[G::kStages];
   uint64_t empty[G::kStages];
   AttnStart start;
+  float row_scale[G::kQueriesShared ? G::kRows : 1];
   float2 ml[kConsumers][G::kPartRows];   // bases and sums
   // Columns of a row that are NaN by a value's code, and whether there are any. Of a segment and of the next, which
   // a warp may be at while others still write the rows of the first.
@@ -96,7 +102,7 @@ struct Shared {
 template <int DH, int NT, int kHeads, int kGroups>
 constexpr size_t smem_bytes() {
   using G = Geo<DH, NT, kHeads, kGroups>;
-  return 1024 + size_t(G::kStages) * 2 * (G::kTensorBytes + G::kScaleBytes) + G::kJoinBytes +
+  return 1024 + size_t(G::kStages) * 2 * (G::kTensorBytes + G::kScaleBytes) + G::kQueryBytes + G::kJoinBytes +
          sizeof(Shared<DH, NT, kHeads, kGroups>);
 }
 
@@ -162,7 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
   uint8_t* scales = smem + G::kStages * 2 * G::kTensorBytes;
-  float* join = reinterpret_cast<float*>(scales + G::kStages * 2 * G::kScaleBytes);
+  uint2* queries = reinterpret_cast<uint2*>(scales + G::kStages * 2 * G::kScaleBytes);
+  float* join = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(queries) + G::kQueryBytes);
   using S = Shared<DH, NT, kHeads, kGroups>;
   S* sh = reinterpret_cast<S*>(reinterpret_cast<uint8_t*>(join) + G::kJoinBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -271,12 +278,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (cur.next(a.plan, seg)) {
       turn ^= 1;
       // ---- queries: row n of a head's is token n / group of the item, its query head n % group
-      uint2 qf[NT][kSteps];
+      uint2 qf[G::kQueriesShared ? 1 : NT][kSteps];
       float rc[NT][2];       // of rows 2 t4 and + 1: what turns a product into a score, but for the key's scale
       int32_t limit[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        {
+        if (!G::kQueriesShared || warp / G::kParts == nt) {
           const int32_t r = row0 + nt * 8 + g, tok = r / group;
           const bool valid = tok < seg.ntok;
           const uint16_t* qp = a.q + static_cast<int64_t>(seg.token0 + tok) * a.q_token +
@@ -319,12 +326,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[kk][e] = pack16x2<false>(__uint_as_float(w[kk][e] << 16) * f,
                                            __uint_as_float(w[kk][e] & 0xFFFF0000u) * f);
           }
+          if constexpr (G::kQueriesShared) {
 #pragma unroll
-          for (int kk = 0; kk < kSteps; ++kk) qf[nt][kk] = make_uint2(w[kk][0], w[kk][1]);
+            for (int kk = 0; kk < kSteps; ++kk)
+              queries[((part * kSteps + kk) * NT + nt) * 32 + lane] = make_uint2(w[kk][0], w[kk][1]);
+            if (t4 == 0) sh->row_scale[part * G::kPartRows + nt * 8 + g] = back;
+          } else {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) rc[nt][j] = __shfl_sync(0xFFFFFFFFu, back, (2 * t4 + j) * 4);
+            for (int kk = 0; kk < kSteps; ++kk) qf[nt][kk] = make_uint2(w[kk][0], w[kk][1]);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) rc[nt][j] = __shfl_sync(0xFFFFFFFFu, back, (2 * t4 + j) * 4);
+          }
         }
       }
+      if constexpr (G::kQueriesShared) named_bar_sync(1, kConsumers * 32);
       float base[NT][2], sum[NT][2];
       float o[NT][kSteps][4];
 #pragma unroll
@@ -337,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           limit[nt][j] = valid && lim > 0 ? lim : 0;
           base[nt][j] = valid ? -INFINITY : 1e30f;   // rows that are not there never ask for a new one
           sum[nt][j] = 0.f;
+          if constexpr (G::kQueriesShared) rc[nt][j] = sh->row_scale[part * G::kPartRows + nt * 8 + 2 * t4 + j];
         }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
@@ -364,16 +380,21 @@ __global__ void __launch_bounds__(kThreads, 1)
               wh[u][0] = hi.x, wh[u][1] = hi.y, wh[u][2] = hi.z, wh[u][3] = hi.w;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+              uint2 q[NT];
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                if constexpr (G::kQueriesShared)
+                  q[nt] = queries[((part * kSteps + half * 4 + i) * NT + nt) * 32 + lane];
+                else
+                  q[nt] = qf[nt][half * 4 + i];
 #pragma unroll
               for (int u = 0; u < U; ++u) {
                 const uint32_t f[4] = {codes_lo(wl[u][i]), codes_lo(wh[u][i]), codes_hi(wl[u][i]), codes_hi(wh[u][i])};
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                  const uint2 q = qf[nt][half * 4 + i];
-                  mma_f16(s[u][nt], f, q.x, q.y);
-                }
+                for (int nt = 0; nt < NT; ++nt) mma_f16(s[u][nt], f, q[nt].x, q[nt].y);
               }
+            }
           }
           // ---- values: four rows of 16 (8) columns, pairs of rows to be interleaved
           constexpr int kWords = DH / 32;
@@ -649,7 +670,7 @@ cudaError_t launch_any(AttnArgs a, const KvFp8Part& k, const KvFp8Part& v, cudaS
   if (attn_width(a.head_dim) == 64)
     e = a.bf16 ? launch<64, NT, kHeads, kGroups, true>(a, k, v, tm, st)
                : launch<64, NT, kHeads, kGroups, false>(a, k, v, tm, st);
-  else if constexpr (NT <= 2)
+  else if constexpr (NT <= 3)
     e = a.bf16 ? launch<128, NT, kHeads, kGroups, true>(a, k, v, tm, st)
                : launch<128, NT, kHeads, kGroups, false>(a, k, v, tm, st);
   return e != cudaSuccess ? e : launch_attn_combine(a, rows, st);
@@ -670,8 +691,10 @@ cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const Kv
   if (rows <= 8) return two ? launch_any<1, 2, 1>(a, k, v, st) : launch_any<1, 1, 1>(a, k, v, st);
   if (rows <= 16) return two ? launch_any<2, 2, 1>(a, k, v, st) : launch_any<2, 1, 1>(a, k, v, st);
   if (rows <= 32) return launch_any<2, 1, 2>(a, k, v, st);
-  // Of 64 columns only (attn_fp8_few_rows): 24 caches of 148-6558 positions with 16 heads, 48 rows 124 us with three
-  // tiles, 143 with four, 157 on tcgen05; 64 rows 146, 155 on tcgen05. Of 128 columns 40 rows took 233, tcgen05 219.
+  // With three tiles and on tcgen05: 40 or 48 rows over two caches of 100003 and 131072 positions, 8 heads of 128, 196
+  // and 220 us, over 16 of 3000-4665 in pages of 48, 4 heads, 41 and 45; 48 rows over 24 of 148-6558, 16 heads of 64,
+  // 123 (four tiles 143) and 157. With four, of 64 columns only: 64 rows over the last ones 146 and 155, but of 128
+  // columns over the first ones, where registers spill, 350 and 220.
   return rows <= 48 ? launch_any<3, 1, 2>(a, k, v, st) : launch_any<4, 1, 2>(a, k, v, st);
 }
 

@@ -33,7 +33,7 @@ cudaError_t launch_kv_read_fp8(const KvFp8Args& a, cudaStream_t st);     // the 
 // Attention over such a cache, `a` as for a paged cache of 16 bits, but for its keys and values.
 // Items of up to attn_fp8_few_rows rows (attn_fp8_rows_sm103.cu); `rows`: of the longest chunk, at least
 // the heads that share a key-value head.
-constexpr int32_t attn_fp8_few_rows(int32_t head_dim) { return attn_width(head_dim) == 64 ? 64 : 32; }
+constexpr int32_t attn_fp8_few_rows(int32_t head_dim) { return attn_width(head_dim) == 64 ? 64 : 48; }
 cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows,
                                  cudaStream_t st);
 

@@ -590,7 +590,7 @@ ENGRAM_API int engram_kv_read_fp8(const engram_attn_desc_t* desc, const int32_t*
 /*
  * engram_attn_paged over an 8-bit cache: the same chunks, masks, lengths, workspace and errors; keys
  * and values are the cache's, as above. Scores, maxima and sums in f32. Where max_q * n_heads /
- * n_kv_heads is at most 32 (64 where head_dim is at most 64), products take codes and queries in f16,
+ * n_kv_heads is at most 48 (64 where head_dim is at most 64), products take codes and queries in f16,
  * which holds both exactly (a bf16 query row is first scaled by a power of two; what lies 2^-39 below its
  * largest element is rounded away), and probabilities are rounded to f16 times their value's scale; what
  * a value contributes to a row 2^-35 below the largest contribution, or what lies 2^100 below the

@@ -84,7 +84,7 @@ class PagedFp8:
 #: A call whose longest chunk has more rows (tokens x heads that share a key-value head) goes to the kernel
 #: that computes on 16-bit tiles.
 def few_rows(rows, head_dim):
-    return rows <= (64 if head_dim <= 64 else 32)
+    return rows <= (64 if head_dim <= 64 else 48)
 
 
 def tolerance(ref, extra, dtype, head_dim, scale, rows):
