@@ -78,6 +78,13 @@ def test_rows_about_the_limits_of_the_kernels(rows, head_dim, dtype):
     check([1, 1, 1], [20001, 1, 130], 64, rows, 1, head_dim, dtype, seed=12)
 
 
+@pytest.mark.parametrize("q_len", [3, 4, 6, 7, 9])
+@pytest.mark.parametrize("group", [5, 7, 11])
+@pytest.mark.parametrize("head_dim", [64, 112])
+def test_tokens_whose_heads_two_warps_share(group, q_len, head_dim):
+    check([q_len, 1, q_len - 1, 0, 2], [q_len, 1, 2000, 5, 129], 16, 2 * group, 2, head_dim, BF16, seed=13)
+
+
 @pytest.mark.parametrize("head_dim", [64, 128])
 @pytest.mark.parametrize("m", [1, 15, 16, 17, 31, 33, 63, 64, 65, 95, 97, 111, 127, 128, 129, 161, 191, 193, 255, 257])
 def test_ends_inside_a_tile(m, head_dim):
@@ -178,6 +185,25 @@ def test_nan_reaches_only_the_rows_that_see_it(q_len, at, which, where, columns)
         assert np.isnan(seen[..., 5]).all()
         keep = np.arange(64) != 5
         np.testing.assert_allclose(seen[..., keep], c[first:, :2][..., keep], rtol=2 ** -7, atol=1e-4)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("q_len", [1, 4, 10, 20, 28, 100])
+@pytest.mark.parametrize("head_dim,dtype", [(64, BF16), (128, BF16), (128, F16)])
+def test_not_finite_queries_stay_with_their_rows(q_len, bad, head_dim, dtype):
+    cache = PagedFp8([400, 150], 16, 2, head_dim, 8)
+    q, clean, lse = run(cache, [q_len, 3], 4, head_dim, dtype, 9)
+    q[q_len // 2, 1, 5] = bad
+    _, out, got = run(cache, [q_len, 3], 4, head_dim, dtype, q=q)
+    assert eg.engram_check_errors() == 0
+    o, c, row = f64(out), f64(clean), (q_len // 2, 1)
+    assert np.isnan(o[row]).all() and np.isnan(f64(got)[row])
+    o[row] = c[row]
+    # another maximum may be taken for the rows beside it
+    np.testing.assert_allclose(o, c, rtol=2 ** -7, atol=1e-4)
+    others = np.ones(lse.shape, bool)
+    others[row] = False
+    np.testing.assert_allclose(f64(got)[others], f64(lse)[others], rtol=1e-5, atol=1e-5)
 
 
 @pytest.mark.parametrize("max_q", [1, 3, 64])
