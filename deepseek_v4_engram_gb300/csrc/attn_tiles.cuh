@@ -48,11 +48,15 @@
 // they write them out as 16-bit tiles times their scales, through registers, with the work of warps 10-11 below
 // done on the way. All else is the same; so a call takes what it would over 16 bits (379 us for a chunk of 2047 over
 // 30000 positions, 16 heads of 128 over 4, f16, on keys of these sizes; 163 for chunks of 1024 and 300 beside six
-// single tokens) and 15-20% more: 446 and 184. What the conversion costs: 64 KB written and 32 read per pair of
+// single tokens) and 5-18% more: 447 and 172. What the conversion costs: 64 KB written and 32 read per pair of
 // tiles in shared memory, where the MMAs take their operands (without any stores 409 us instead of 468, without
-// any arithmetic 389, without the conversion 358), and issue slots beside the softmax. A tile takes four warps
-// 1030-1490 cycles in f16, up to 2150 in bf16, whose codes go through f32. Not faster: bf16 codes put in place bit
-// by bit, three tiles' room for codes and four for tiles, keys and values requested by a warp each (10% slower).
+// any arithmetic 389, without the conversion 358), issue slots beside the softmax, and the room of its instructions
+// beside the softmax's: its loop takes one row of a team of lanes at a time (with batches of two and of four rows the
+// mixed chunks take 176 and 183 us, with twice four unrolled 220, with half a row 203). Not faster: bf16 codes put in
+// place bit by bit, three tiles' room for codes and four for tiles, keys and values requested by a warp each (10%
+// slower) or converted by two warps each (467 and 199 us), the next row's codes or scale fetched a turn ahead
+// (187, 180). Items of one row tile with the even key tiles in one half of the softmax warps and the odd ones in the
+// other: 16 chunks of 128 rows 42 us instead of 44.5, but the mixed chunks 10 us more.
 //
 // A probability of 0 does not undo an infinity or NaN that it multiplies. In the tiles that reach
 // past what the item's first row sees, warps 10-11 clear the value rows that no row sees (another
@@ -343,45 +347,36 @@ __device__ __forceinline__ bool convert_tile(uint32_t codes, const uint8_t* scal
   };
   const uint32_t own = first + lane < end ? scales[first + lane] : 127u;   // of row `lane`
   if (__all_sync(0xFFFFFFFFu, is_fast<kBf16>(own))) {
-    // the swizzle repeats every 8 rows: with two sets of addresses (one, for 64 columns) the rest is offsets
-    constexpr int kSets = 8 / kAtOnce, kBatch = 16 / kAtOnce;
-    uint32_t at[kSets][2], put[kSets][2];
+    // kAtOnce rows further a 128-byte swizzle has its third bit the other way round, the others are as they were
+    uint32_t at[2], put[2];
 #pragma unroll
-    for (int e = 0; e < kSets; ++e)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        at[e][h] = from(first + in + e * kAtOnce, h);
-        put[e][h] = to(first + in + e * kAtOnce, h);
-      }
+    for (int h = 0; h < 2; ++h) {
+      at[h] = from(first + in, h);
+      put[h] = to(first + in, h);
+    }
     const uint32_t scale = fast_scale<kBf16>(own);
     const bool edge = values && (first + 32 > end || first + 32 > guard);   // the same for all lanes
     uint32_t bad = 0;
 #pragma unroll 1
-    for (int i = 0; i < 32; i += 16) {
-      uint2 w[kBatch][2];
+    for (int i = 0; i < 32; i += kAtOnce) {
+      uint2 w[2] = {lds64(at[0]), lds64(at[1])};
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) w[b][h] = lds64(at[b % kSets][h] + (i + b / kSets * 8) * DH);
+      for (int h = 0; h < 2; ++h) at[h] = (DH == 128 ? at[h] ^ 64u : at[h]) + kAtOnce * DH;
+      const uint32_t s = __shfl_sync(0xFFFFFFFFu, scale, in + i);
       if (edge) {
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (first + in + i + b * kAtOnce >= end) w[b][h] = make_uint2(0, 0);
-            bad |= nan_codes(w[b][h].x) | nan_codes(w[b][h].y);
-          }
+        for (int h = 0; h < 2; ++h) {
+          if (first + in + i >= end) w[h] = make_uint2(0, 0);
+          bad |= nan_codes(w[h].x) | nan_codes(w[h].y);
+        }
       }
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const uint32_t s = __shfl_sync(0xFFFFFFFFu, scale, in + i + b * kAtOnce);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 x;
-          scaled16x4<kBf16>(w[b][h].x, s, x.x, x.y);
-          scaled16x4<kBf16>(w[b][h].y, s, x.z, x.w);
-          sts128(put[b % kSets][h] + (i + b / kSets * 8) * 128, x);
-        }
+      for (int h = 0; h < 2; ++h) {
+        uint4 x;
+        scaled16x4<kBf16>(w[h].x, s, x.x, x.y);
+        scaled16x4<kBf16>(w[h].y, s, x.z, x.w);
+        sts128(put[h], x);
+        put[h] = (DH == 128 ? put[h] ^ 64u : put[h]) + kAtOnce * 128;
       }
     }
     if (!__any_sync(0xFFFFFFFFu, bad != 0)) return false;
