@@ -692,7 +692,7 @@ cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const Kv
   if (rows <= 16) return two ? launch_any<2, 2, 1>(a, k, v, st) : launch_any<2, 1, 1>(a, k, v, st);
   if (rows <= 32) return launch_any<2, 1, 2>(a, k, v, st);
   // With three tiles and on tcgen05: 40 or 48 rows over two caches of 100003 and 131072 positions, 8 heads of 128, 196
-  // and 220 us, over 16 of 3000-4665 in pages of 48, 4 heads, 41 and 45; 48 rows over 24 of 148-6558, 16 heads of 64,
+  // and 220 us (208 since), over 16 of 3000-4665 in pages of 48, 4 heads, 41 and 45; 48 rows over 24 of 148-6558, 16 heads of 64,
   // 123 (four tiles 143) and 157. With four, of 64 columns only: 64 rows over the last ones 146 and 155, but of 128
   // columns over the first ones, where registers spill, 350 and 220.
   return rows <= 48 ? launch_any<3, 1, 2>(a, k, v, st) : launch_any<4, 1, 2>(a, k, v, st);

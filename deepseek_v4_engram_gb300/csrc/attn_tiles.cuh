@@ -48,7 +48,7 @@
 // they write them out as 16-bit tiles times their scales, through registers, with the work of warps 10-11 below
 // done on the way. All else is the same; so a call takes what it would over 16 bits (379 us for a chunk of 2047 over
 // 30000 positions, 16 heads of 128 over 4, f16, on keys of these sizes; 163 for chunks of 1024 and 300 beside six
-// single tokens) and 5-18% more: 447 and 172. What the conversion costs: 64 KB written and 32 read per pair of
+// single tokens) and 5-18% more: 447 and 171. What the conversion costs: 64 KB written and 32 read per pair of
 // tiles in shared memory, where the MMAs take their operands (without any stores 409 us instead of 468, without
 // any arithmetic 389, without the conversion 358), issue slots beside the softmax, and the room of its instructions
 // beside the softmax's: its loop takes one row of a team of lanes at a time (with batches of two and of four rows the
@@ -92,11 +92,13 @@ constexpr int kTileRows = 128;
 constexpr int kItemRows = kAttnItemRows;   // two row tiles
 // 256 * 192 + 128 * 120 = 384 * 168. With 176 + 152 the softmax warps spill, with 208 + 88 the others
 // do: the prompt of 16384 tokens takes 676, 641, 658 us.
-// 256 * 184 + 256 * 72 = 512 * 128 with the four warps more that an 8-bit cache takes.
-template <class Kv>
-constexpr int kSoftmaxRegs = Kv::kFp8 ? 184 : 192;
-template <class Kv>
-constexpr int kOtherRegs = Kv::kFp8 ? 72 : 120;
+// 256 * 184 + 256 * 72 = 512 * 128 with the four warps more that an 8-bit cache takes, 176 + 80 in bf16, whose
+// conversion takes more: chunks of 1024 and 300 tokens beside six single ones, bf16, 185, 172, 169, 173 us with 192, 184,
+// 176, 168, a chunk of 2047 over 30000, f16, 455, 449, 459, 478.
+template <bool kBf16, class Kv>
+constexpr int kSoftmaxRegs = !Kv::kFp8 ? 192 : kBf16 ? 176 : 184;
+template <bool kBf16, class Kv>
+constexpr int kOtherRegs = !Kv::kFp8 ? 120 : kBf16 ? 80 : 72;
 constexpr int kSegments = 4;                 // in the ring from warp 9 to the others
 template <class Kv>
 constexpr int kSegmentReaders = kSoftmaxWarps + 3 + (Kv::kFp8 ? kConvertWarps : 0);
@@ -510,7 +512,7 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
 
   if (warp < 8) {
     // ------------------------------------------------------------- softmax and output
-    set_max_regs_up<kSoftmaxRegs<Kv>>();
+    set_max_regs_up<kSoftmaxRegs<kBf16, Kv>>();
     const int t = warp >> 2;
     const int32_t row = t * kTileRows + (warp & 3) * 32 + lane;   // of the item
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -778,7 +780,7 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
       __syncwarp();
     }
   } else {
-    set_max_regs_down<kOtherRegs<Kv>>();
+    set_max_regs_down<kOtherRegs<kBf16, Kv>>();
     if (warp == 8) {
       // ----------------------------------------------------------- MMA issuer
       constexpr uint32_t kIdS = idesc<kBf16>(128, 128, false), kIdO = idesc<kBf16>(128, DH, true);
