@@ -281,31 +281,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint2 qf[G::kQueriesShared ? 1 : NT][kSteps];
       float rc[NT][2];       // of rows 2 t4 and + 1: what turns a product into a score, but for the key's scale
       int32_t limit[NT][2];
+      auto load_row = [&](int nt, uint32_t (&w)[kSteps][2]) {
+        const int32_t r = row0 + nt * 8 + g, tok = r / group;
+        const bool valid = tok < seg.ntok;
+        const uint16_t* qp = a.q + static_cast<int64_t>(seg.token0 + tok) * a.q_token +
+                             static_cast<int64_t>(seg.h * a.group + sub * group + (r - tok * group)) * a.q_head;
+#pragma unroll
+        for (int half = 0; half < DH / 64; ++half) {   // columns 16 (t4 + 4 half) + 0 .. 15
+          const int col = 16 * (t4 + 4 * half);
+          uint4 x = make_uint4(0, 0, 0, 0), y = x;
+          if (valid && col < a.head_dim) {
+            x = *reinterpret_cast<const uint4*>(qp + col);
+            y = *reinterpret_cast<const uint4*>(qp + col + 8);
+          }
+          w[half * 4][0] = x.x;
+          w[half * 4][1] = x.y;
+          w[half * 4 + 1][0] = x.z;
+          w[half * 4 + 1][1] = x.w;
+          w[half * 4 + 2][0] = y.x;
+          w[half * 4 + 2][1] = y.y;
+          w[half * 4 + 3][0] = y.z;
+          w[half * 4 + 3][1] = y.w;
+        }
+      };
+      // All the loads before the first shuffle, which no load passes (24 caches with 64 rows, bf16, 176 -> 151 us).
+      uint32_t words[NT][kSteps][2];
+      if constexpr (!G::kQueriesShared)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) load_row(nt, words[nt]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if (!G::kQueriesShared || warp / G::kParts == nt) {
-          const int32_t r = row0 + nt * 8 + g, tok = r / group;
-          const bool valid = tok < seg.ntok;
-          const uint16_t* qp = a.q + static_cast<int64_t>(seg.token0 + tok) * a.q_token +
-                               static_cast<int64_t>(seg.h * a.group + sub * group + (r - tok * group)) * a.q_head;
-          uint32_t w[kSteps][2];
-#pragma unroll
-          for (int half = 0; half < DH / 64; ++half) {   // columns 16 (t4 + 4 half) + 0 .. 15
-            const int col = 16 * (t4 + 4 * half);
-            uint4 x = make_uint4(0, 0, 0, 0), y = x;
-            if (valid && col < a.head_dim) {
-              x = *reinterpret_cast<const uint4*>(qp + col);
-              y = *reinterpret_cast<const uint4*>(qp + col + 8);
-            }
-            w[half * 4][0] = x.x;
-            w[half * 4][1] = x.y;
-            w[half * 4 + 1][0] = x.z;
-            w[half * 4 + 1][1] = x.w;
-            w[half * 4 + 2][0] = y.x;
-            w[half * 4 + 2][1] = y.y;
-            w[half * 4 + 3][0] = y.z;
-            w[half * 4 + 3][1] = y.w;
-          }
+          uint32_t (&w)[kSteps][2] = words[nt];
+          if constexpr (G::kQueriesShared) load_row(nt, w);
           float back = a.scale_log2;
           if constexpr (kBf16) {
             // the largest element goes to 2^14 .. 2^15
@@ -692,9 +700,9 @@ cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const Kv
   if (rows <= 16) return two ? launch_any<2, 2, 1>(a, k, v, st) : launch_any<2, 1, 1>(a, k, v, st);
   if (rows <= 32) return launch_any<2, 1, 2>(a, k, v, st);
   // With three tiles and on tcgen05: 40 or 48 rows over two caches of 100003 and 131072 positions, 8 heads of 128, 196
-  // and 220 us (208 since), over 16 of 3000-4665 in pages of 48, 4 heads, 41 and 45; 48 rows over 24 of 148-6558, 16 heads of 64,
-  // 123 (four tiles 143) and 157. With four, of 64 columns only: 64 rows over the last ones 146 and 155, but of 128
-  // columns over the first ones, where registers spill, 350 and 220.
+  // and 212-222 us, over 16 of 3000-4665 in pages of 48, 4 heads, 41 and 45; 48 rows over 24 of 148-6558, 16 heads of
+  // 64, f16 and bf16, 117, 124 and 158, 149. With four, of 64 columns only: 64 rows over the last ones 138, 151 and
+  // 154, 149, but of 128 columns over the first ones, where registers spill, 350 and 220.
   return rows <= 48 ? launch_any<3, 1, 2>(a, k, v, st) : launch_any<4, 1, 2>(a, k, v, st);
 }
 
