@@ -93,8 +93,8 @@ constexpr int kItemRows = kAttnItemRows;   // two row tiles
 // 256 * 192 + 128 * 120 = 384 * 168. With 176 + 152 the softmax warps spill, with 208 + 88 the others
 // do: the prompt of 16384 tokens takes 676, 641, 658 us.
 // 256 * 184 + 256 * 72 = 512 * 128 with the four warps more that an 8-bit cache takes, 176 + 80 in bf16, whose
-// conversion takes more: chunks of 1024 and 300 tokens beside six single ones, bf16, 185, 172, 169, 173 us with 192, 184,
-// 176, 168, a chunk of 2047 over 30000, f16, 455, 449, 459, 478.
+// conversion takes more: chunks of 1024 and 300 tokens beside six single ones, bf16, 185, 172, 169, 173 us with 192,
+// 184, 176, 168, a chunk of 2047 over 30000, f16, 455, 449, 459, 478.
 template <bool kBf16, class Kv>
 constexpr int kSoftmaxRegs = !Kv::kFp8 ? 192 : kBf16 ? 176 : 184;
 template <bool kBf16, class Kv>
