@@ -594,7 +594,8 @@ ENGRAM_API int engram_kv_read_fp8(const engram_attn_desc_t* desc, const int32_t*
  * which holds both exactly (a bf16 query row is first scaled by a power of two; what lies 2^-39 below its
  * largest element is rounded away), and probabilities are rounded to f16 times their value's scale; what
  * a value contributes to a row 2^-35 below the largest contribution, or what lies 2^100 below the
- * largest value of the head, may be lost.
+ * largest value of the head, may be lost. (Contributions as the scales have them, the smallest that hold
+ * their rows' values. A row of zeros counts as one of scale 2^-92, or by its byte where that is below 127.)
  * Above, keys and values are rounded to dtype as engram_kv_read_fp8 gives them (exact where they were
  * appended in dtype) and probabilities to dtype. A NaN in a row that a token does not see does not reach
  * it.
