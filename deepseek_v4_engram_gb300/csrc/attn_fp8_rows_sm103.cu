@@ -459,7 +459,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 2 * U; ++i) {
             ve[i] = static_cast<float>(static_cast<int>(max(vb8[i], kMinScale)) - 127);
-            unscale[i] = __uint_as_float((254u - kSumDrop - min(max(vb8[i], kMinScale), 247u)) << 23);
+            // (below f32's normal numbers from byte 248 on, and exact there too)
+            unscale[i] = __uint_as_float((255u - max(vb8[i], kMinScale)) << 23) * (0.5f / (1 << kSumDrop));
           }
           const bool edge = key0 + 16 * U > seg.first;   // some row does not see all of them
           bool over = false;
