@@ -17,7 +17,8 @@ from ._lib import EngramAttnDesc
 from .api import _check, lib
 from .attn import _TORCH, _device, _ints, _lse, _refuse, _scratch, _sequences, _stream, _view
 
-_U8, _CODES, _SCALES, _INT = torch.uint8, torch.float8_e4m3fn, torch.float8_e8m0fnu, torch.int32
+_U8, _CODES, _INT = torch.uint8, torch.float8_e4m3fn, torch.int32
+_SCALES = getattr(torch, "float8_e8m0fnu", None)   # an older torch has no such type: scales are uint8 there
 _pack_cache = _lib.PACK_CACHE_FP8.pack
 
 
