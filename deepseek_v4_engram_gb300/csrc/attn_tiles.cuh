@@ -108,7 +108,8 @@ constexpr int kPoisonSlots = 8;
 constexpr float kMostSum = 512.f;
 // Over an 8-bit cache in bf16, whose keys' sizes differ more from row to row in the cases measured. With 512 a
 // quarter of the tiles find their maximum: chunks of 1024 and 300 tokens beside six single ones 215 us; with this
-// 206 us, and with the lift below, where hardly any does, 182. Sums stay finite for values up to 2^100.
+// 206 us, and with the lift below, where hardly any does, 182. A tile adds up to 2^16 times its largest value to an
+// output's sum, which is finite for values up to 2^99 over 2^12 tiles, and 2^88 over 2^23, all that there may be.
 constexpr float kMostSumFp8 = 65536.f;
 // Probabilities are rounded to the values' type for the product with them, since the MMA takes both
 // operands in one 16-bit type: each by half a unit in its last place, as the result is at the end.

@@ -593,12 +593,14 @@ ENGRAM_API int engram_kv_read_fp8(const engram_attn_desc_t* desc, const int32_t*
  * n_kv_heads is at most 48 (64 where head_dim is at most 64), products take codes and queries in f16,
  * which holds both exactly (a bf16 query row is first scaled by a power of two; what lies 2^-39 below its
  * largest element is rounded away), and probabilities are rounded to f16 times their value's scale; what
- * a value contributes to a row 2^-35 below the largest contribution, or what lies 2^100 below the
- * largest value of the head, may be lost. (Contributions as the scales have them, the smallest that hold
- * their rows' values. A row of zeros counts as one of scale 2^-92, or by its byte where that is below 127.)
+ * a value contributes to a row 2^-35 below the largest contribution may be lost, and what lies 2^100 below
+ * the largest value of the head, its key's weight included. (Contributions as the scales have them, the
+ * smallest that hold their rows' values. A row of zeros counts as one of scale 2^-92, or by its byte where
+ * that is below 127.)
  * Above, keys and values are rounded to dtype as engram_kv_read_fp8 gives them (exact where they were
- * appended in dtype) and probabilities to dtype. A NaN in a row that a token does not see does not reach
- * it.
+ * appended in dtype) and probabilities to dtype. In bf16 an output's sum has room for values up to 2^88, or
+ * 2^99 where no row sees more than 2^19 positions, and may overflow to infinity beyond; of a result, what is
+ * below 2^-100 may be lost. A NaN in a row that a token does not see does not reach it.
  */
 ENGRAM_API int engram_attn_paged_fp8(const engram_attn_desc_t* desc, const engram_attn_view_t* q,
                                      const int32_t* cu_seqlens, int32_t n_seqs, int32_t total,

@@ -1,4 +1,6 @@
 """GPU: attention over an 8-bit cache whose values are near the ends of what its format and its type hold."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -36,3 +38,26 @@ def test_the_largest_scales(tokens, heads, head_dim, m, low):
     assert eg.engram_check_errors() == 0
     scale = head_dim ** -0.5
     assert_close(out, lse, *reference(cache, 0, q, scale), BF16, head_dim, scale, tokens * heads)
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 60])
+@pytest.mark.parametrize("exponent", [98, -90])
+@pytest.mark.parametrize("head_dim", [64, 128])
+def test_large_and_small_values_whose_scores_grow(tokens, exponent, head_dim):
+    """Maxima that grow by 2^80 from the first key to the last, evenly, so that as much as there may be lies
+    between a sum's base and its largest term."""
+    m = 1500
+    cache = PagedFp8([m], 16, 2, head_dim, 6)
+    g = np.random.default_rng(7)
+    k = np.zeros((m, 2, head_dim))
+    k[..., 0] = (np.arange(m) * (80 * math.log(2) / m))[:, None] / 4
+    kc, ks = kv_fp8.quantise(k)
+    vc, vs = kv_fp8.quantise(np.ldexp(g.uniform(-1.9, 1.9, (m, 2, head_dim)), exponent))
+    cache.write(0, 0, kc, ks, vc, vs)
+    cache.keys[0], cache.values[0] = kv_fp8.values(kc, ks), kv_fp8.values(vc, vs)
+    cache.codes[0], cache.exponents[0] = e4m3_to_f64(vc), vs.astype(np.int64) - 127
+    q = torch.zeros((tokens, 4, head_dim), dtype=BF16, device="cuda")
+    q[..., 0] = 4.0
+    _, out, lse = run(cache, [tokens], 4, head_dim, BF16, q=q, scale=1.0)
+    assert eg.engram_check_errors() == 0
+    assert_close(out, lse, *reference(cache, 0, q, 1.0), BF16, head_dim, 1.0, tokens * 2)
