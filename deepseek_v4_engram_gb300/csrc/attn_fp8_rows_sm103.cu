@@ -25,16 +25,17 @@
 // slow per row, not per byte, and memory gives less where 128 bytes of every kilobyte are read. The even warps then
 // take one head, the odd ones the other. With more than 16 rows they take one half of a head's rows each instead:
 // every code is then converted by two warps, but a warp's rows leave it the registers for 32 keys at once (32 rows:
-// two caches of 100003 and 131072 positions with 8 heads 151 us; all the rows in every warp, 16 keys at a time,
+// two caches of 100003 and 131072 positions with 8 heads 150 us; all the rows in every warp, 16 keys at a time,
 // 163-170). 24 rows of 128 columns leave it that room only with the queries in shared memory (40 or 48 rows over
-// those caches 196 us; 16 keys at a time with the queries in registers 233).
+// those caches 197 us; 16 keys at a time with the queries in registers 233), and registers spill all the same: 160
+// bytes a thread are stored and 68 loaded (128 and 40 with 32 rows of 64 columns, less than 80 in the other forms).
 //
 // The base B_r lags behind the maximum: it is found anew only when some y exceeds it by 2^kSlack or more,
 // which a warp finds out with one vote instead of the shuffles of a maximum.
 //
 // Measured (replayed, inputs larger than L2): one token each over 64 caches of 1584-2048 positions, 32 heads of
-// 128 over 8, 49.6 us (a 16-bit cache 80), over 4 caches of 70001-131072 139 us, 6.4 TB/s; 24 caches of 100-7061
-// with 16 heads of 64, f16, 40.7; one token over 511 positions 8.2. A call's fixed time is about 9 us: range, first
+// 128 over 8, 50-51 us (a 16-bit cache 82), over 4 caches of 70001-131072 140-144 us, 6.2-6.4 TB/s from one GPU to
+// another; 24 caches of 100-7061 with 16 heads of 64, f16, 40.7; one token over 511 positions 8.2. A call's fixed time is about 9 us: range, first
 // page entry, page and tile, joining warps and pieces. A stage of 32 KB takes 0.75 us where memory alone sets
 // the pace (a copy that only reads; 0.73 at the copy rate) and 0.74-0.8 here with 8 rows of a head, 0.82 with 16,
 // 1.5 with 32, 2.0 with 48, whose chain of steps is longer than the wait for memory. What brought it there: all copies
@@ -52,8 +53,8 @@ namespace engram {
 namespace {
 
 constexpr int kConsumers = 8;
-// An item's fixed time, in key tiles. With 0, 1, 2: 24 caches with 16 heads of 64 51.6, 44.6, 42.9 us, two long caches
-// with 16 rows 106, 104.5, 102.6, others the same.
+// An item's fixed time, in key tiles. With 0, 1, 2: 24 caches with 16 heads of 64 48.8, 42.5, 40.8 us, five drafted
+// tokens over 16 caches 45.5, 45.4, 43.3, two long caches with 16 rows 91.0, 89.8, 88.4, others the same.
 constexpr int kExtraUnits = 2;
 constexpr int kThreads = (kConsumers + 4) * 32;
 // 256 * 232 + 128 * 40 = 384 * 168
@@ -738,9 +739,11 @@ cudaError_t launch_any(AttnArgs a, const KvFp8Part& k, const KvFp8Part& v, cudaS
 cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const KvFp8Part& v, int32_t rows,
                                  cudaStream_t st) {
   // Two key-value heads an item where they lie beside each other in memory: TMA then takes rows twice as long,
-  // and memory pieces of 256 bytes. (24 caches of 100-7061 positions with 16 heads of 64: 63 us with one, 45
-  // with two; 4 of 70001-131072 with 8 heads of 128: 146 and 144.) But not where even tables that are full leave
-  // SMs without a tile of one head: one token over 511 positions 8.0 us with one, 8.7 with two.
+  // and memory pieces of 256 bytes. (24 caches of 100-7061 positions with 16 heads of 64: 64 us with one, 40.8
+  // with two; 4 of 70001-131072 with 8 heads of 128: 161 and 144; two long caches with 16 rows 104 and 88.5.) But not
+  // where even tables that are full leave SMs without a tile of one head: one token over 511 positions 8.2 us with
+  // one, 8.6 with two. The lengths are on the device, so that a short cache takes two, and that time, where the
+  // table has room for a long one.
   const int64_t width = attn_width(a.head_dim);
   const int64_t most = int64_t(a.plan.n_seqs) * a.plan.kv_heads * ((a.plan.kv_cap + kTileKeys - 1) / kTileKeys);
   const bool two = a.plan.kv_heads % 2 == 0 && a.head_dim == width && k.head == width && v.head == width &&
@@ -748,10 +751,11 @@ cudaError_t launch_attn_fp8_rows(const AttnArgs& a, const KvFp8Part& k, const Kv
   if (rows <= 8) return two ? launch_any<1, 2, 1>(a, k, v, st) : launch_any<1, 1, 1>(a, k, v, st);
   if (rows <= 16) return two ? launch_any<2, 2, 1>(a, k, v, st) : launch_any<2, 1, 1>(a, k, v, st);
   if (rows <= 32) return launch_any<2, 1, 2>(a, k, v, st);
-  // With three tiles and on tcgen05: 40 or 48 rows over two caches of 100003 and 131072 positions, 8 heads of 128, 196
-  // and 212-222 us, over 16 of 3000-4665 in pages of 48, 4 heads, 41 and 45; 48 rows over 24 of 148-6558, 16 heads of
-  // 64, f16 and bf16, 117, 124 and 158, 149. With four, of 64 columns only: 64 rows over the last ones 138, 151 and
-  // 154, 149, but of 128 columns over the first ones, where registers spill, 350 and 220.
+  // With three tiles and on tcgen05: 40 or 48 rows over two caches of 100003 and 131072 positions, 8 heads of 128, 197
+  // and 212 us, over 16 of 3000-4665 in pages of 48, 4 heads, 43.4 and 46.0; 40 or 48 rows over 24 of 140-6558, 16 heads
+  // of 64, f16 and bf16, 117-118, 125 and 156-158, 148. With four, of 64 columns only: 64 rows over the last ones 143,
+  // 150 and 154, 148 (bf16 is as fast on either), but of 128 columns over the first ones, where registers spill more,
+  // 350 and 209.
   return rows <= 48 ? launch_any<3, 1, 2>(a, k, v, st) : launch_any<4, 1, 2>(a, k, v, st);
 }
 

@@ -46,9 +46,10 @@
 //
 // Over an 8-bit cache there are four warps more, 12-15: TMA brings codes (warp 9; the scales by warp 11), and
 // they write them out as 16-bit tiles times their scales, through registers, with the work of warps 10-11 below
-// done on the way. All else is the same; so a call takes what it would over 16 bits (379 us for a chunk of 2047 over
-// 30000 positions, 16 heads of 128 over 4, f16, on keys of these sizes; 163 for chunks of 1024 and 300 beside six
-// single tokens) and 5-18% more: 447 and 171. What the conversion costs: 64 KB written and 32 read per pair of
+// done on the way. All else is the same; so a call takes what it would over 16 bits (378 us for a chunk of 2047 over
+// 30000 positions, 16 heads of 128 over 4, f16, on keys of these sizes; 160 for chunks of 1024 and 300 beside six
+// single tokens) and 7-18% more: 447 and 171. (On keys of one size, whose maxima hardly grow, 316 and 398, 128 and 166.)
+// Registers spill a little: 72 bytes a thread stored and 116 loaded in f16 with 128 columns, 40 and 92 in bf16. What the conversion costs: 64 KB written and 32 read per pair of
 // tiles in shared memory, where the MMAs take their operands (without any stores 409 us instead of 468, without
 // any arithmetic 389, without the conversion 358), issue slots beside the softmax, and the room of its instructions
 // beside the softmax's: its loop takes one row of a team of lanes at a time (with batches of two and of four rows the
@@ -107,8 +108,9 @@ constexpr int kPoisonSlots = 8;
 // maximum, the prompt of 16384 tokens took 1093 us instead of 661.
 constexpr float kMostSum = 512.f;
 // Over an 8-bit cache in bf16, whose keys' sizes differ more from row to row in the cases measured. With 512 a
-// quarter of the tiles find their maximum: chunks of 1024 and 300 tokens beside six single ones 215 us; with this
-// 206 us, and with the lift below, where hardly any does, 182. A tile adds up to 2^16 times its largest value to an
+// quarter of the tiles find their maximum: chunks of 1024 and 300 tokens beside six single ones 203 us; with this and
+// the lift below, where hardly any does, 171 (a chunk of 512 over 16000 positions 96 and 81; on keys of one size
+// 165 and 166, 78 and 79). A tile adds up to 2^16 times its largest value to an
 // output's sum, which is finite for values up to 2^99 over 2^12 tiles, and 2^88 over 2^23, all that there may be.
 constexpr float kMostSumFp8 = 65536.f;
 // Probabilities are rounded to the values' type for the product with them, since the MMA takes both
@@ -126,9 +128,10 @@ constexpr float kMostLifted = !kBf16 ? kMostSum * 64.f : Kv::kFp8 ? kMostSumFp8 
 // the difference: from here on (2^24 in units of log2) it is subtracted first.
 constexpr float kFarScore = 16777216.f;
 // Tiles of an item whose maximum is found at once: among the first ones it grows, and taking exponentials twice
-// costs more. (f16 over an 8-bit cache, where it may grow by no more than kSpare, 2^14 with the lift. With 1, 8, 32
-// and all of them: 16 chunks of 40 rows over 3000-4665 positions 48.6, 46.2, 44.6, 44.6 us, when they were still
-// computed here, a chunk of 2047 over 30000 456, 456, 448, 463.)
+// costs more. (f16 over an 8-bit cache, where it may grow by no more than kSpare, 2^14 with the lift. With 1, 8, 32:
+// 16 chunks of 128 rows over 3000-4665 positions 50.0, 47.9, 45.2 us, chunks of 1024 and 300 tokens beside single ones
+// 191, 187, 180, one of 512 over 16000 91, 89, 81, of 2047 over 30000 459, 459, 448, and with all of them 463. Keys of
+// one size, whose maxima hardly grow, want few: the mixed chunks 150, 152, 163, the last one 391, 393, 398.)
 template <bool kBf16, class Kv>
 constexpr int kYoung = Kv::kFp8 && !kBf16 ? 32 : 1;
 constexpr float kSpare = 8.f;
