@@ -22,6 +22,16 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// A warpgroup's share of the block's registers, up or down to N per thread.
+template <int N>
+__device__ __forceinline__ void set_max_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Pairs of f32 in one 64-bit register, for instructions that take two at once.
 __device__ __forceinline__ uint64_t pair(float lo, float hi) {
   uint64_t r;

@@ -136,15 +136,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   return d;
 }
 
-template <int N>
-__device__ __forceinline__ void set_max_regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void set_max_regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 __device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
   return e4m3x2_to_f16x2(static_cast<uint16_t>(w));
 }

@@ -269,15 +269,6 @@ __device__ __forceinline__ void tc_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-template <int N>
-__device__ __forceinline__ void set_max_regs_up() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void set_max_regs_down() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -448,7 +439,7 @@ __global__ void __launch_bounds__(kThreads<Kv>, 1)
     for (int s = 0; s < G::kStages; ++s) {
       mbar_init(&sh->full[s], Kv::kFp8 ? kConvertWarps : 1);
       mbar_init(&sh->empty[s], Kv::kFp8 ? 1 : 3);   // the MMAs that read it, and warps 10 and 11
-      mbar_init(&sh->vok[s], 2);
+      if constexpr (!Kv::kFp8) mbar_init(&sh->vok[s], 2);
     }
     if constexpr (Kv::kFp8)
       for (int s = 0; s < G::kCodeStages; ++s) {
