@@ -139,6 +139,23 @@ def run_case(form, lens, exponent, above, byte, where, dtype):
         check(cache, i, q[s], out[s], lse[s], dtype, D ** -0.5, tokens * heads // kv_heads)
 
 
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("exponent", [-20, -30])
+def test_columns_of_small_values(form, exponent):
+    """Rows that have ordinary values in the even columns alone, and as many with small values in the odd ones: what
+    those columns hold is lost only below 2^-36 of the ordinary rows' products."""
+    tokens, heads, kv_heads, D, _ = FORMS[form]
+    cache, q = make(FORMS[form], (450,), 0, 0.0, None, "some", BF16)
+    v = cache.values[0].copy()
+    v[0::2, :, 1::2] = 0.0
+    v[1::2, :, 0::2] = 0.0
+    v[1::2] = np.ldexp(v[1::2], exponent)
+    put(cache, 0, cache.keys[0], v)
+    _, out, lse = run(cache, [tokens], heads, D, BF16, q=q)
+    assert eg.engram_check_errors() == 0
+    check(cache, 0, q, out, lse, BF16, D ** -0.5, tokens * heads // kv_heads)
+
+
 @pytest.mark.parametrize("form", ["8 rows, 128", "16 rows of two heads, 64", "48 rows, 128", "tiles, 64"])
 def test_nothing_but_zeros(form):
     """Outputs are zeros; the logarithm of the sum is as ever."""
